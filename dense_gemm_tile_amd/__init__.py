@@ -1,4 +1,5 @@
-"""Python binding of the MI355X dense GEMM library (C ABI in include/dense_gemm_tile.h).
+"""Python binding of the MI355X dense GEMM library (C ABI in include/dense_gemm_tile.h
+and include/gemm_layer.h).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libdense_gemm_tile_amd.so. Importing this package loads that
@@ -29,6 +30,8 @@ GEMM_DTYPE_F32_F16 = 2   # float32 A and B, rounded to f16 while staged
 GEMM_DTYPE_F32_BF16 = 3  # float32 A and B, rounded to bf16 while staged
 GEMM_DTYPE_F8_E4M3 = 4   # 8-bit float codes, OCP E4M3
 GEMM_DTYPE_F8_E5M2 = 5   # 8-bit float codes, OCP E5M2
+GEMM_DTYPE_F32 = 6       # float32 results and rows of the layer operators
+GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_ERF, GEMM_ACT_SILU = range(5)
 
 # Every symbol the header declares, with its ctypes signature.
 _i64, _int, _f32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p
@@ -45,6 +48,29 @@ _SIGNATURES = {
     "gemm_last_path": (ctypes.c_char_p, []),
     "gemm_tile_order": (_int, [_i64, _i64, _int, ctypes.POINTER(ctypes.c_int32),
                                ctypes.POINTER(ctypes.c_int32)]),
+    # Layer operators.
+    "gemm_linear": (_int, [_i64, _i64, _i64, _int, _int, _int, _vp, _i64, _vp, _i64, _vp, _int,
+                           _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp]),
+    "gemm_linear_validate": (_int, [_i64, _i64, _i64, _int, _int, _int, _vp, _i64, _vp, _i64, _vp,
+                                    _int, _vp, _i64, _vp, _i64, _int, _vp, _i64]),
+    "gemm_grouped": (_int, [_i64, _i64, _i64, _i64, _int, _int, _vp, _vp, _i64, _vp, _i64, _i64,
+                            _vp, _int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp]),
+    "gemm_grouped_validate": (_int, [_i64, _i64, _i64, _i64, _int, _int, _vp, _vp, _i64, _vp, _i64,
+                                     _i64, _vp, _int, _vp, _i64, _vp, _i64, _int, _vp, _i64]),
+    "gemm_grouped_grad_weight": (_int, [_i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _i64,
+                                        _vp, _i64, _i64, _int, _int, _vp]),
+    "gemm_grouped_grad_weight_validate": (_int, [_i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp,
+                                                 _i64, _vp, _i64, _i64, _int, _int]),
+    "gemm_act_grad": (_int, [_i64, _i64, _i64, _int, _int, _vp, _vp, _i64, _vp, _i64, _vp, _i64,
+                             _vp, _vp, _i64, _vp]),
+    "gemm_act_grad_workspace": (_i64, [_i64, _i64, _i64]),
+    "gemm_route": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "gemm_route_workspace": (_i64, [_i64, _i64, _i64]),
+    "gemm_dispatch": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "gemm_combine": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
+                            _vp]),
+    "gemm_combine_grad": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                                 _vp, _vp]),
 }
 
 
@@ -88,13 +114,26 @@ def _stream(s):
 
 _DTYPE_CODES = {"f16": GEMM_DTYPE_F16, "bf16": GEMM_DTYPE_BF16, "f32_f16": GEMM_DTYPE_F32_F16,
                 "f32_bf16": GEMM_DTYPE_F32_BF16, "f8e4m3": GEMM_DTYPE_F8_E4M3,
-                "f8e5m2": GEMM_DTYPE_F8_E5M2}
+                "f8e5m2": GEMM_DTYPE_F8_E5M2, "f32": GEMM_DTYPE_F32}
+_ACT_CODES = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GELU,
+              "gelu_erf": GEMM_ACT_GELU_ERF, "silu": GEMM_ACT_SILU}
 
 
 def _dtype(d):
     if isinstance(d, str):
         return _DTYPE_CODES[d]
     return int(d)
+
+
+def _act(a):
+    if isinstance(a, str):
+        return _ACT_CODES[a]
+    return int(a)
+
+
+def _check(st: int) -> None:
+    if st != GEMM_OK:
+        raise GemmError(st, gemm_last_error())
 
 
 def gemm(M, N, K, dtype, transA, transB, alpha, beta, A, lda, B, ldb, C, ldc, D, ldd,
@@ -136,6 +175,102 @@ def gemm_i8_validate(M, N, K, transA, transB, alpha, beta, A, lda, B, ldb, C, ld
                                  _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, _ptr(D), ldd)
 
 
+def gemm_linear(M, N, K, dtype, transA, transB, A, lda, B, ldb, bias, act, R, ldr, Y, ldy,
+                out_dtype, Z=None, ldz=0, stream=None):
+    """Enqueue Z = op(A)@op(B) + bias, Y = act(Z) + R (bias, R and Z may be None); act is one of
+    "none", "relu", "gelu", "gelu_erf", "silu"; raises GemmError on a non-zero status."""
+    _check(_lib.gemm_linear(M, N, K, _dtype(dtype), int(transA), int(transB), _ptr(A), lda,
+                            _ptr(B), ldb, _ptr(bias), _act(act), _ptr(R), ldr, _ptr(Y), ldy,
+                            _dtype(out_dtype), _ptr(Z), ldz, _stream(stream)))
+
+
+def gemm_linear_validate(M, N, K, dtype, transA, transB, A, lda, B, ldb, bias, act, R, ldr, Y, ldy,
+                         out_dtype, Z=None, ldz=0) -> int:
+    """Host-only checks and kernel choice of gemm_linear(); returns the status code."""
+    return _lib.gemm_linear_validate(M, N, K, _dtype(dtype), int(transA), int(transB), _ptr(A),
+                                     lda, _ptr(B), ldb, _ptr(bias), _act(act), _ptr(R), ldr,
+                                     _ptr(Y), ldy, _dtype(out_dtype), _ptr(Z), ldz)
+
+
+def gemm_grouped(G, M, N, K, dtype, transB, offsets, A, lda, B, ldb, stride_b, bias, act, R, ldr,
+                 Y, ldy, out_dtype, Z=None, ldz=0, stream=None):
+    """Enqueue gemm_linear() with one B and bias per group of rows offsets[g] .. offsets[g+1]-1."""
+    _check(_lib.gemm_grouped(G, M, N, K, _dtype(dtype), int(transB), _ptr(offsets), _ptr(A), lda,
+                             _ptr(B), ldb, stride_b, _ptr(bias), _act(act), _ptr(R), ldr, _ptr(Y),
+                             ldy, _dtype(out_dtype), _ptr(Z), ldz, _stream(stream)))
+
+
+def gemm_grouped_validate(G, M, N, K, dtype, transB, offsets, A, lda, B, ldb, stride_b, bias, act,
+                          R, ldr, Y, ldy, out_dtype, Z=None, ldz=0) -> int:
+    """Host-only checks and kernel choice of gemm_grouped(); returns the status code."""
+    return _lib.gemm_grouped_validate(G, M, N, K, _dtype(dtype), int(transB), _ptr(offsets),
+                                      _ptr(A), lda, _ptr(B), ldb, stride_b, _ptr(bias), _act(act),
+                                      _ptr(R), ldr, _ptr(Y), ldy, _dtype(out_dtype), _ptr(Z), ldz)
+
+
+def gemm_grouped_grad_weight(G, M, N, K, dtype, offsets, A, lda, B, ldb, D, ldd, stride_d,
+                             out_dtype, accumulate=False, stream=None):
+    """Enqueue D_g = A_g^T @ B_g (+ D_g when accumulate) over the rows of each group."""
+    _check(_lib.gemm_grouped_grad_weight(G, M, N, K, _dtype(dtype), _ptr(offsets), _ptr(A), lda,
+                                         _ptr(B), ldb, _ptr(D), ldd, stride_d, _dtype(out_dtype),
+                                         int(accumulate), _stream(stream)))
+
+
+def gemm_grouped_grad_weight_validate(G, M, N, K, dtype, offsets, A, lda, B, ldb, D, ldd, stride_d,
+                                      out_dtype, accumulate=False) -> int:
+    """Host-only checks of gemm_grouped_grad_weight(); returns the status code."""
+    return _lib.gemm_grouped_grad_weight_validate(G, M, N, K, _dtype(dtype), _ptr(offsets),
+                                                  _ptr(A), lda, _ptr(B), ldb, _ptr(D), ldd,
+                                                  stride_d, _dtype(out_dtype), int(accumulate))
+
+
+def gemm_act_grad(G, M, N, dtype, act, offsets, dY, lddy, Z, ldz, dZ, lddz, db, workspace,
+                  workspace_bytes, stream=None):
+    """Enqueue dZ = dY * act'(Z) and db[g] = the sum of dZ over each group's rows (float32).
+    offsets None: one group. workspace: gemm_act_grad_workspace(G, M, N) bytes on the device."""
+    _check(_lib.gemm_act_grad(G, M, N, _dtype(dtype), _act(act), _ptr(offsets), _ptr(dY), lddy,
+                              _ptr(Z), ldz, _ptr(dZ), lddz, _ptr(db), _ptr(workspace),
+                              workspace_bytes, _stream(stream)))
+
+
+def gemm_act_grad_workspace(G, M, N) -> int:
+    """Bytes of workspace that gemm_act_grad() needs."""
+    return _lib.gemm_act_grad_workspace(G, M, N)
+
+
+def gemm_route(T, top, E, ids, offsets, order, slot, workspace, workspace_bytes, stream=None):
+    """Enqueue the stable sort of T x top int32 expert ids: offsets[E + 1], order[T * top] and
+    slot[T * top] (int32). workspace: gemm_route_workspace(T, top, E) bytes on the device."""
+    _check(_lib.gemm_route(T, top, E, _ptr(ids), _ptr(offsets), _ptr(order), _ptr(slot),
+                           _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemm_route_workspace(T, top, E) -> int:
+    """Bytes of workspace that gemm_route() needs."""
+    return _lib.gemm_route_workspace(T, top, E)
+
+
+def gemm_dispatch(T, top, H, dtype, X, ldx, slot, Xs, ldxs, stream=None):
+    """Enqueue Xs[slot[t][j]] = X[t] ("f16", "bf16" or "f32" rows of H values)."""
+    _check(_lib.gemm_dispatch(T, top, H, _dtype(dtype), _ptr(X), ldx, _ptr(slot), _ptr(Xs), ldxs,
+                              _stream(stream)))
+
+
+def gemm_combine(T, top, H, dtype, Ys, ldys, slot, weights, R, ldr, Y, ldy, stream=None):
+    """Enqueue Y[t] = sum_j weights[t][j] * Ys[slot[t][j]] + R[t] (weights float32 or None for
+    ones, R may be None)."""
+    _check(_lib.gemm_combine(T, top, H, _dtype(dtype), _ptr(Ys), ldys, _ptr(slot), _ptr(weights),
+                             _ptr(R), ldr, _ptr(Y), ldy, _stream(stream)))
+
+
+def gemm_combine_grad(T, top, H, dtype, dY, lddy, Ys, ldys, slot, weights, dYs, lddys, dweights,
+                      stream=None):
+    """Enqueue dYs[slot[t][j]] = weights[t][j] * dY[t] and dweights[t][j] = <dY[t], Ys[slot]>."""
+    _check(_lib.gemm_combine_grad(T, top, H, _dtype(dtype), _ptr(dY), lddy, _ptr(Ys), ldys,
+                                  _ptr(slot), _ptr(weights), _ptr(dYs), lddys, _ptr(dweights),
+                                  _stream(stream)))
+
+
 def gemm_last_error() -> str:
     return _lib.gemm_last_error().decode()
 
@@ -159,4 +294,9 @@ __all__ = ["gemm_i8", "gemm_i8_validate", "gemm", "gemm_status", "gemm_validate"
            "gemm_tile_order", "GemmError", "GEMM_OK", "GEMM_ERR_INVALID_ARG",
            "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_ALIAS", "GEMM_ERR_HIP", "GEMM_DTYPE_F16",
            "GEMM_DTYPE_BF16", "GEMM_DTYPE_F32_F16", "GEMM_DTYPE_F32_BF16", "GEMM_DTYPE_F8_E4M3",
-           "GEMM_DTYPE_F8_E5M2", "LIB_PATH"]
+           "GEMM_DTYPE_F8_E5M2", "LIB_PATH",
+           "gemm_linear", "gemm_linear_validate", "gemm_grouped", "gemm_grouped_validate",
+           "gemm_grouped_grad_weight", "gemm_grouped_grad_weight_validate", "gemm_act_grad",
+           "gemm_act_grad_workspace", "gemm_route", "gemm_route_workspace", "gemm_dispatch",
+           "gemm_combine", "gemm_combine_grad", "GEMM_DTYPE_F32", "GEMM_ACT_NONE",
+           "GEMM_ACT_RELU", "GEMM_ACT_GELU", "GEMM_ACT_GELU_ERF", "GEMM_ACT_SILU"]

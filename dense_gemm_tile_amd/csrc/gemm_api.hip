@@ -13,6 +13,7 @@
 #include <string>
 
 #include "dense_gemm_tile.h"
+#include "api_state.h"
 #include "common.h"
 
 extern char** environ;  // POSIX: the process environment (read by read_env)
@@ -41,8 +42,15 @@ struct MfmaPath {
 };
 thread_local MfmaPath g_mpath;
 thread_local bool g_path_lazy = false;
+// Writes the path of a call whose entry point keeps its own description (the
+// layer operators), when it is asked for.
+thread_local void (*g_path_writer)(std::string&) = nullptr;
 
 const std::string& current_path() {
+  if (g_path_writer) {
+    g_path_writer(g_path);
+    g_path_writer = nullptr;
+  }
   if (g_path_lazy) {
     const MfmaPath& m = g_mpath;
     char buf[512], ksplit[32] = "", fold[48] = "";
@@ -82,6 +90,7 @@ struct EnvSwitches {
   const char* log = nullptr;         // GEMM_LOG
   const char* ring_mode = nullptr;   // GEMM_RING_MODE: form of the 128x128 ring kernel
   const char* stage_depth = nullptr; // GEMM_STAGE_DEPTH: slices of staged loads ahead (1 or 2)
+  const char* layer_tile = nullptr;  // GEMM_LAYER_TILE: product kernel of the layer operators
 };
 thread_local EnvSwitches g_env;
 
@@ -96,12 +105,14 @@ void read_env() {
     else if (std::strncmp(v, "LOG=", 4) == 0) g_env.log = v + 4;
     else if (std::strncmp(v, "RING_MODE=", 10) == 0) g_env.ring_mode = v + 10;
     else if (std::strncmp(v, "STAGE_DEPTH=", 12) == 0) g_env.stage_depth = v + 12;
+    else if (std::strncmp(v, "LAYER_TILE=", 11) == 0) g_env.layer_tile = v + 11;
   }
   if (g_env.force_path && !*g_env.force_path) g_env.force_path = nullptr;
   if (g_env.force_tile && !*g_env.force_tile) g_env.force_tile = nullptr;
   if (g_env.log && !*g_env.log) g_env.log = nullptr;
   if (g_env.ring_mode && !*g_env.ring_mode) g_env.ring_mode = nullptr;
   if (g_env.stage_depth && !*g_env.stage_depth) g_env.stage_depth = nullptr;
+  if (g_env.layer_tile && !*g_env.layer_tile) g_env.layer_tile = nullptr;
 }
 
 // Largest dimension the int32 index arithmetic in the kernels supports.
@@ -122,12 +133,44 @@ struct Plan {
   GemmByteArgs bargs{};
 };
 
+}  // namespace
+
+void begin_call() {
+  g_err.clear();
+  g_path.clear();
+  g_path_lazy = false;
+  g_path_writer = nullptr;
+  read_env();
+}
+
 int fail(int code, const std::string& msg) {
   g_err = msg;
   return code;
 }
 
-// Byte extent of a row-major [rows, cols] matrix with leading dimension ld.
+void set_path(const std::string& text) {
+  g_path = text;
+  g_path_lazy = false;
+  g_path_writer = nullptr;
+}
+
+void set_path_writer(void (*write)(std::string&)) {
+  g_path_lazy = false;
+  g_path_writer = write;
+}
+
+const char* forced_layer_tile() { return g_env.layer_tile; }
+
+void log_layer_call(const char* op, int64_t M, int64_t N, int64_t K, int status) {
+  if (!g_env.log || std::strcmp(g_env.log, "debug") != 0) return;
+  if (status == GEMM_OK)
+    std::fprintf(stderr, "[gemm] %s %lld x %lld x %lld -> %s\n", op, (long long)M, (long long)N,
+                 (long long)K, current_path().c_str());
+  else
+    std::fprintf(stderr, "[gemm] %s %lld x %lld x %lld -> error %d: %s\n", op, (long long)M,
+                 (long long)N, (long long)K, status, g_err.c_str());
+}
+
 unsigned __int128 extent_bytes(int64_t rows, int64_t cols, int64_t ld, int elem) {
   if (rows <= 0 || cols <= 0) return 0;
   return ((unsigned __int128)(rows - 1) * (unsigned __int128)ld + (unsigned __int128)cols) *
@@ -139,6 +182,8 @@ bool overlaps(const void* p, unsigned __int128 np, const void* q, unsigned __int
   const unsigned __int128 a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + nq && b < a + np;
 }
+
+namespace {
 
 // Widest staging load (in elements of esz bytes, at most 16 bytes) whose byte
 // size divides both the operand's base address and its row pitch.
@@ -253,10 +298,7 @@ void set_byte_tiles(GemmByteArgs& b, int transA, int transB) {
 int plan_call(int64_t M, int64_t N, int64_t K, int dtype, int transA, int transB, float alpha,
               float beta, const void* A, int64_t lda, const void* B, int64_t ldb, const float* C,
               int64_t ldc, const float* D, int64_t ldd, Plan& plan) {
-  g_err.clear();
-  g_path.clear();
-  g_path_lazy = false;
-  read_env();
+  begin_call();
   char buf[256];
   transA = transA != 0;
   transB = transB != 0;
@@ -642,10 +684,7 @@ int plan_call(int64_t M, int64_t N, int64_t K, int dtype, int transA, int transB
 int plan_i8(int64_t M, int64_t N, int64_t K, int transA, int transB, int32_t alpha, int32_t beta,
             const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const int32_t* C,
             int64_t ldc, const int32_t* D, int64_t ldd, GemmByteArgs& a, bool& noop) {
-  g_err.clear();
-  g_path.clear();
-  g_path_lazy = false;
-  read_env();
+  begin_call();
   noop = false;
   char buf[256];
   transA = transA != 0;

@@ -1,0 +1,417 @@
+// The layer operators' products: what one call carries, how a workgroup finds
+// its tile, the activations, and the epilogue.
+//
+//   dense     Y = act(op(A) @ op(B) + bias) + R
+//   by rows   the rows of A and Y are cut into groups by offsets held on the
+//             GPU, each with its own B and bias
+//   by sum    the summed dimension is cut into groups instead, each with its
+//             own Y (the gradient of grouped weights)
+#pragma once
+
+#include "gemm_mfma_impl.h"
+
+namespace dgt {
+
+enum LayerMode : int { LAYER_DENSE = 0, LAYER_ROWS = 1, LAYER_SUM = 2 };
+enum LayerAct : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_ERF = 3, ACT_SILU = 4 };
+
+struct LayerArgs {
+  const void* A;
+  const void* B;
+  const void* bias;  // null: none
+  const void* R;     // null: none
+  void* Y;
+  void* Z;           // null: not kept
+  const int* offsets;
+  int64_t lda, ldb, ldr, ldy, ldz;  // elements
+  int64_t stride_b;  // by rows: elements from one group's B to the next
+  int64_t stride_y;  // by sum: elements from one group's Y (and R) to the next
+  int M, N, K;       // by rows: M counts all rows; by sum: K does
+  int G, mode, act;
+  int out32;         // Y (and R) hold float32, else the operands' 16-bit type
+  int vec;           // bits 0-3: bias, R, Y, Z allow 16-byte accesses of 8 columns
+  int a_vw, b_vw;    // staging vector widths of A and B (general kernel)
+  int tiles_m, tiles_n;  // of one group (by sum, dense); by rows: tiles_m is not used
+  int group_m;
+};
+enum LayerVec : int { VEC_BIAS = 1, VEC_R = 2, VEC_Y = 4, VEC_Z = 8 };
+
+// One group's product and one tile of it. Pointers and sizes are uniform.
+struct LayerTile {
+  const char* A;
+  const char* B;
+  const char* bias;
+  const char* R;
+  char* Y;
+  char* Z;
+  int M, N, K;   // of this group
+  int m0, n0;    // the tile's first row and column
+};
+
+__device__ __forceinline__ int layer_clamp(int v, int hi) { return v < 0 ? 0 : (v > hi ? hi : v); }
+template <class T>
+__device__ __forceinline__ T* layer_uniform(T* p) {
+  const uint64_t u = (uint64_t)p;
+  const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)u);
+  const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(u >> 32));
+  return (T*)(((uint64_t)hi << 32) | lo);
+}
+
+// Rows [first, first + count) of group g, clamped to the call's rows whatever
+// the offsets hold.
+__device__ __forceinline__ void layer_group(const int* offsets, int g, int rows, int& first,
+                                            int& count) {
+  first = layer_clamp(offsets[g], rows);
+  const int end = layer_clamp(offsets[g + 1], rows);
+  count = end > first ? end - first : 0;
+}
+
+// Tiles of BM rows that the groups hold in all, and, for a tile index below
+// that, its group and its index within the group. Each lane counts the tiles
+// of one group of 64; a scan over the wave places them. Every wave of a
+// workgroup does this for itself: the offsets stay in its caches, and no LDS
+// has to be kept for it.
+template <int BM>
+struct LayerRows {
+  __device__ static inline int tiles_of(const LayerArgs& p, int g, int& first, int& count) {
+    if (g >= p.G) return first = count = 0;
+    layer_group(p.offsets, g, p.M, first, count);
+    return (count + BM - 1) / BM;
+  }
+  __device__ static inline int wave_scan(int v, int lane) {  // inclusive
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(v, d, 64);
+      if (lane >= d) v += o;
+    }
+    return v;
+  }
+  __device__ static inline int total(const LayerArgs& p, int lane) {
+    int sum = 0;
+    for (int g0 = 0; g0 < p.G; g0 += 64) {
+      int f, c;
+      sum += tiles_of(p, g0 + lane, f, c);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    return __builtin_amdgcn_readfirstlane(sum);
+  }
+  // t counts tiles with tiles_n column tiles to each row tile. Returns the
+  // group, its rows, and the tile's index within the group.
+  __device__ static inline int find(const LayerArgs& p, int t, int tiles_n, int lane, int& first,
+                                    int& count, int& in) {
+    int base = 0;
+    for (int g0 = 0; g0 < p.G; g0 += 64) {
+      int f, c;
+      const int n = tiles_of(p, g0 + lane, f, c);
+      const int incl = wave_scan(n, lane);
+      const int chunk = __builtin_amdgcn_readlane(incl, 63);
+      if (t < (base + chunk) * tiles_n) {
+        // the first lane whose inclusive count lies past the tile
+        const uint64_t past = __ballot((int64_t)(base + incl) * tiles_n > t);
+        const int src = __builtin_ctzll(past);
+        first = __builtin_amdgcn_readlane(f, src);
+        count = __builtin_amdgcn_readlane(c, src);
+        const int before = base + __builtin_amdgcn_readlane(incl - n, src);
+        in = t - before * tiles_n;
+        return g0 + src;
+      }
+      base += chunk;
+    }
+    first = count = in = 0;
+    return 0;
+  }
+};
+
+// Tiles of the whole call (an exact count, uniform).
+template <int MODE, int BM>
+__device__ inline int layer_tiles(const LayerArgs& p, int lane) {
+  if constexpr (MODE == LAYER_ROWS) return LayerRows<BM>::total(p, lane) * p.tiles_n;
+  return p.tiles_m * p.tiles_n * (MODE == LAYER_SUM ? p.G : 1);
+}
+
+// Tile t (in the order that puts tiles sharing operand panels on one XCD) of
+// `total`. Consecutive tiles belong to one group, walked in grouped order.
+// The mode is fixed at compile time: with a branch on it at run time this
+// compiler left the pointers that the third branch does not change (bias, Z)
+// undefined there.
+template <int MODE, int BM, int BN>
+__device__ inline LayerTile layer_tile(const LayerArgs& p, int t, int total, int lane) {
+  LayerTile q;
+  const int lid = xcd_remap(t, total);
+  const int osz = p.out32 ? 4 : 2;
+  int tm, tn;
+  q.M = p.M;
+  q.N = p.N;
+  q.K = p.K;
+  q.A = static_cast<const char*>(p.A);
+  q.B = static_cast<const char*>(p.B);
+  q.bias = static_cast<const char*>(p.bias);
+  q.R = static_cast<const char*>(p.R);
+  q.Y = static_cast<char*>(p.Y);
+  q.Z = static_cast<char*>(p.Z);
+  if constexpr (MODE == LAYER_DENSE) {
+    grouped_tile(lid, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+  } else if constexpr (MODE == LAYER_ROWS) {
+    int first, count, in;
+    const int g = LayerRows<BM>::find(p, lid, p.tiles_n, lane, first, count, in);
+    grouped_tile(in, (count + BM - 1) / BM, p.tiles_n, p.group_m, tm, tn);
+    q.M = count;
+    q.A += (int64_t)first * p.lda * 2;
+    q.B += (int64_t)g * p.stride_b * 2;
+    if (q.bias) q.bias += (int64_t)g * p.N * 2;
+    if (q.R) q.R += (int64_t)first * p.ldr * osz;
+    q.Y += (int64_t)first * p.ldy * osz;
+    if (q.Z) q.Z += (int64_t)first * p.ldz * 2;
+  } else {
+    const int per = p.tiles_m * p.tiles_n;
+    const int g = lid / per;
+    grouped_tile(lid - g * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    int first, count;
+    layer_group(p.offsets, g, p.K, first, count);
+    first = __builtin_amdgcn_readfirstlane(first);
+    q.K = __builtin_amdgcn_readfirstlane(count);
+    q.A += (int64_t)first * p.lda * 2;
+    q.B += (int64_t)first * p.ldb * 2;
+    q.bias = nullptr;
+    q.Z = nullptr;
+    if (q.R) q.R += (int64_t)g * p.stride_y * osz;
+    q.Y += (int64_t)g * p.stride_y * osz;
+  }
+  q.m0 = tm * BM;
+  q.n0 = tn * BN;
+  return q;
+}
+
+// -------------------------------------------------------------- 16-bit types --
+__device__ __forceinline__ float layer_f32(TagF16, unsigned short u) {
+  return (float)__builtin_bit_cast(_Float16, u);
+}
+__device__ __forceinline__ float layer_f32(TagBF16, unsigned short u) {
+  return __builtin_bit_cast(float, (unsigned)u << 16);
+}
+// To nearest, ties to even (the hardware conversions round so).
+__device__ __forceinline__ unsigned short layer_16(TagF16, float x) {
+  return __builtin_bit_cast(unsigned short, (_Float16)x);
+}
+__device__ __forceinline__ unsigned short layer_16(TagBF16, float x) {
+  return __builtin_bit_cast(unsigned short, (__bf16)x);
+}
+template <class Tag>
+__device__ __forceinline__ void layer_unpack8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    f[2 * d] = layer_f32(Tag{}, (unsigned short)(v[d] & 0xFFFFu));
+    f[2 * d + 1] = layer_f32(Tag{}, (unsigned short)(v[d] >> 16));
+  }
+}
+template <class Tag>
+__device__ __forceinline__ u32x4 layer_pack8(const float (&f)[8]) {
+  u32x4 v;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    v[d] = (unsigned)layer_16(Tag{}, f[2 * d]) | ((unsigned)layer_16(Tag{}, f[2 * d + 1]) << 16);
+  return v;
+}
+
+// --------------------------------------------------------------- activations --
+// 1 / (1 + exp(-v)): exp overflows to infinity and the reciprocal of that is
+// 0, so both ends come out right without a branch.
+__device__ __forceinline__ float layer_sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
+constexpr float kGeluA = 1.5957691216057308f;       // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// GELU's tanh form, z (1 + tanh(u)) / 2, is z * sigmoid(2 u): no difference
+// of nearly equal numbers for negative z.
+template <int ACT>
+__device__ __forceinline__ float layer_act(float z) {
+  if constexpr (ACT == ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
+  if constexpr (ACT == ACT_GELU) return z * layer_sigmoid(kGeluA * (z + kGeluB * z * z * z));
+  if constexpr (ACT == ACT_GELU_ERF) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+  if constexpr (ACT == ACT_SILU) return z * layer_sigmoid(z);
+  return z;
+}
+// act'(z). Past |z| = 16 GELU's slope is 0 or 1 to float32; the cubic there
+// would give infinity times zero.
+template <int ACT>
+__device__ __forceinline__ float layer_slope(float z) {
+  if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (ACT == ACT_GELU) {
+    const float c = z > 16.0f ? 16.0f : (z < -16.0f ? -16.0f : z);
+    const float s = layer_sigmoid(kGeluA * (c + kGeluB * c * c * c));
+    return s + c * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * c * c);
+  }
+  if constexpr (ACT == ACT_GELU_ERF) {
+    const float c = z > 16.0f ? 16.0f : (z < -16.0f ? -16.0f : z);
+    return 0.5f * erfcf(-0.70710678118654752f * c) +
+           c * 0.3989422804014327f * __expf(-0.5f * c * c);
+  }
+  if constexpr (ACT == ACT_SILU) {
+    const float s = layer_sigmoid(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  return 1.0f;
+}
+template <int ACT>
+__device__ __forceinline__ void layer_act8_of(float (&f)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = layer_act<ACT>(f[e]);
+}
+__device__ __forceinline__ void layer_act8(float (&f)[8], int act) {
+  switch (act) {  // uniform over the launch
+    case ACT_RELU: layer_act8_of<ACT_RELU>(f); break;
+    case ACT_GELU: layer_act8_of<ACT_GELU>(f); break;
+    case ACT_GELU_ERF: layer_act8_of<ACT_GELU_ERF>(f); break;
+    case ACT_SILU: layer_act8_of<ACT_SILU>(f); break;
+    default: break;
+  }
+}
+
+// ------------------------------------------------------------------ epilogue --
+// Row-wise accesses of up to 8 columns of a 16-bit or float32 matrix; nv of
+// the 8 lie inside it. wide: 16-byte accesses are allowed.
+template <class Tag>
+__device__ __forceinline__ void layer_load8_16(const char* p, bool wide, int nv, float (&f)[8]) {
+  if (wide && nv == 8) {
+    layer_unpack8<Tag>(*reinterpret_cast<const u32x4*>(p), f);
+  } else {
+    const unsigned short* s = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < nv ? layer_f32(Tag{}, s[e]) : 0.0f;
+  }
+}
+template <class Tag>
+__device__ __forceinline__ void layer_store8_16(char* p, bool wide, int nv, const float (&f)[8]) {
+  if (wide && nv == 8) {
+    *reinterpret_cast<u32x4*>(p) = layer_pack8<Tag>(f);
+  } else {
+    unsigned short* s = reinterpret_cast<unsigned short*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < nv) s[e] = layer_16(Tag{}, f[e]);
+  }
+}
+__device__ __forceinline__ void layer_load8_32(const char* p, bool wide, int nv, float (&f)[8]) {
+  const float* s = reinterpret_cast<const float*>(p);
+  if (wide && nv == 8) {
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(s), hi = *reinterpret_cast<const f32x4*>(s + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = lo[e], f[e + 4] = hi[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < nv ? s[e] : 0.0f;
+  }
+}
+__device__ __forceinline__ void layer_store8_32(char* p, bool wide, int nv, const float (&f)[8]) {
+  float* s = reinterpret_cast<float*>(p);
+  if (wide && nv == 8) {
+    *reinterpret_cast<f32x4*>(s) = f32x4{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<f32x4*>(s + 4) = f32x4{f[4], f[5], f[6], f[7]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < nv) s[e] = f[e];
+  }
+}
+
+// Z, activation, residual and Y of 8 columns of one row, from the sums x.
+template <class Tag>
+__device__ __forceinline__ void layer_finish8(const LayerArgs& p, const LayerTile& q, int r, int c,
+                                              int nv, const float (&bias)[8], float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] += bias[e];
+  if (q.Z) layer_store8_16<Tag>(q.Z + ((int64_t)r * p.ldz + c) * 2, p.vec & VEC_Z, nv, x);
+  layer_act8(x, p.act);
+  if (q.R) {
+    float rv[8];
+    if (p.out32) layer_load8_32(q.R + ((int64_t)r * p.ldr + c) * 4, p.vec & VEC_R, nv, rv);
+    else layer_load8_16<Tag>(q.R + ((int64_t)r * p.ldr + c) * 2, p.vec & VEC_R, nv, rv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += rv[e];
+  }
+  if (p.out32) layer_store8_32(q.Y + ((int64_t)r * p.ldy + c) * 4, p.vec & VEC_Y, nv, x);
+  else layer_store8_16<Tag>(q.Y + ((int64_t)r * p.ldy + c) * 2, p.vec & VEC_Y, nv, x);
+}
+
+// The epilogue of one wave's TM x TN atoms, whose first output is (r0, c0).
+// The accumulators of a 16- or 32-wide atom hold 4 rows of one column per
+// lane; a row of atoms goes through LDS so that each lane gets 8 consecutive
+// columns of one row, and a wave's stores of 16-bit outputs are 16 bytes a
+// lane, whole 128-byte lines where the wave is 64 columns wide. lds: this
+// wave's own layer_lds_bytes<C>(); no other wave touches it.
+template <class C>
+constexpr int layer_pitch() { return C::TN * C::At::N + 4; }  // floats; 4 apart in banks per row
+template <class C>
+constexpr int layer_lds_bytes() { return C::At::M * layer_pitch<C>() * 4; }
+
+// LDS written by some lanes of a wave is read by others: LDS operations of one
+// wave complete in order, so only the compiler has to keep theirs.
+__device__ __forceinline__ void layer_wave_order() {
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <class C, class Tag>
+__device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][C::TN],
+                                            const LayerArgs& p, const LayerTile& q, int r0, int c0,
+                                            int lane, float* lds) {
+  using At = typename C::At;
+  constexpr int W = C::TN * At::N, P = layer_pitch<C>();
+  constexpr int LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
+  static_assert(W % 8 == 0 && 64 % LPR == 0 && At::M % RPP == 0, "whole passes");
+  const int cl = 8 * (lane % LPR), rl = lane / LPR;
+  const int c = c0 + cl, nv = q.N - c >= 8 ? 8 : q.N - c;
+  float bias[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
+  if (q.bias && nv > 0) layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int v = 0; v < At::NACC; ++v)
+        lds[At::acc_row(lane, v) * P + j * At::N + At::acc_col(lane)] = acc[i][j][v];
+    layer_wave_order();
+#pragma unroll
+    for (int s = 0; s < At::M / RPP; ++s) {
+      const int rr = s * RPP + rl, r = r0 + i * At::M + rr;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(lds + rr * P + cl);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(lds + rr * P + cl + 4);
+      float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (r < q.M && nv > 0) layer_finish8<Tag>(p, q, r, c, nv, bias, x);
+    }
+    layer_wave_order();
+  }
+}
+
+// ----------------------------------------------------------------- launchers --
+// Every product kernel is instantiated for the modes and layouts that the
+// entry points reach: dense calls in four layouts, by rows with A stored
+// [M][K], by sum with both operands stored along the sum. f(mode, ta, tb) gets
+// them as integral constants.
+template <int V>
+struct LayerConst {
+  static constexpr int value = V;
+};
+template <class F>
+hipError_t layer_for_layout(const LayerArgs& a, bool ta, bool tb, F f) {
+  if (a.mode == LAYER_SUM) return f(LayerConst<LAYER_SUM>{}, LayerConst<1>{}, LayerConst<0>{});
+  if (a.mode == LAYER_ROWS)
+    return tb ? f(LayerConst<LAYER_ROWS>{}, LayerConst<0>{}, LayerConst<1>{})
+              : f(LayerConst<LAYER_ROWS>{}, LayerConst<0>{}, LayerConst<0>{});
+  if (!ta)
+    return tb ? f(LayerConst<LAYER_DENSE>{}, LayerConst<0>{}, LayerConst<1>{})
+              : f(LayerConst<LAYER_DENSE>{}, LayerConst<0>{}, LayerConst<0>{});
+  return tb ? f(LayerConst<LAYER_DENSE>{}, LayerConst<1>{}, LayerConst<1>{})
+            : f(LayerConst<LAYER_DENSE>{}, LayerConst<1>{}, LayerConst<0>{});
+}
+
+// The kernels of the products, each next to its definition. dtype: 0 f16, 1
+// bf16. They return the HIP status of the launch.
+hipError_t launch_layer_general(int dtype, bool ta, bool tb, bool small, const LayerArgs& a,
+                                int ntiles, hipStream_t s);
+
+}  // namespace dgt

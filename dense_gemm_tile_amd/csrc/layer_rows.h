@@ -1,0 +1,88 @@
+// The layer operators that move rows and ids: launchers, each next to its
+// kernels in layer_rows.hip and layer_route.hip. They return the HIP status of
+// the first launch that failed.
+#pragma once
+
+#include "common.h"
+
+namespace dgt {
+
+// Element types of rows.
+enum RowType : int { ROW_F16 = 0, ROW_BF16 = 1, ROW_F32 = 2 };
+
+struct ActGradArgs {
+  const int* offsets;  // null: one group of all M rows
+  const void* dY;
+  const void* Z;       // null: no activation
+  void* dZ;            // null: not wanted
+  float* db;           // null: not wanted
+  float* part;         // partial column sums
+  int64_t lddy, ldz, lddz;
+  int G, M, N, act;
+  int wide;            // rows of all three allow 16-byte accesses
+};
+// Rows that one wave sums by itself: a partial sum is kept for each.
+constexpr int kActGradRows = 32;
+inline unsigned act_grad_column_blocks(int64_t n) { return (unsigned)((n + 511) / 512); }
+hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s);
+
+struct RouteArgs {
+  const int* ids;
+  int* offsets;
+  int* order;
+  int* slot;
+  int* counts;  // [blocks][E + 1], more than one block only
+  int n;        // choices
+  int E;
+  int blocks, chunk;  // choices per block
+};
+constexpr int kRouteMaxExperts = 1024;
+// Blocks that a call of n choices is cut into, and choices per block.
+void route_blocks(int64_t n, int& blocks, int& chunk);
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+struct DispatchArgs {
+  const char* X;
+  char* Xs;
+  const int* slot;
+  int64_t ldx, ldxs;  // bytes
+  int T, top;
+  int64_t bytes;      // of a row
+  int piece;          // bytes per access: 16, 8, 4 or 2
+};
+constexpr int kDispatchSpan = 4;  // pieces a lane
+inline int64_t dispatch_column_blocks(const DispatchArgs& a) {
+  const int64_t span = (int64_t)kDispatchSpan * 64 * a.piece;
+  return (a.bytes + span - 1) / span;
+}
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s);
+
+struct CombineArgs {
+  const void* Ys;
+  const int* slot;
+  const float* weights;  // null: ones
+  const void* R;         // null: none
+  void* Y;
+  int64_t ldys, ldr, ldy;  // elements
+  int T, top, H;
+  int piece;  // elements per access
+};
+inline int64_t combine_column_blocks(const CombineArgs& a) {
+  return ((int64_t)a.H + 64 * a.piece - 1) / (64 * a.piece);
+}
+hipError_t launch_combine(int rowtype, const CombineArgs& a, hipStream_t s);
+
+struct CombineGradArgs {
+  const void* dY;
+  const void* Ys;        // null without dw
+  const int* slot;
+  const float* weights;  // null: ones
+  void* dYs;             // null: not wanted
+  float* dw;             // null: not wanted
+  int64_t lddy, ldys, lddys;
+  int T, top, H;
+  int piece;
+};
+hipError_t launch_combine_grad(int rowtype, const CombineGradArgs& a, hipStream_t s);
+
+}  // namespace dgt

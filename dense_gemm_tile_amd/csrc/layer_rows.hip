@@ -1,0 +1,366 @@
+// The layer operators that move rows: activation gradients with bias sums,
+// rows sent to their experts, rows joined again with weights, and the
+// gradients of that. All are bound by memory: each input is read once, each
+// output written once, 16 bytes a lane where alignment allows.
+#include "layer.h"
+#include "layer_rows.h"
+
+namespace dgt {
+
+namespace {
+
+// ------------------------------------------------- activation and bias grads --
+// dZ = dY * act'(Z), and sums of dZ over rows before it is rounded. A wave
+// takes kActGradRows rows of 512 columns (8 a lane) and keeps 8 float32 sums;
+// where its rows cross from one group to the next it starts new ones. Rows
+// block b and group g meet in at most one run of rows, and b + g is another
+// number for each run (each next run has the next b or the next g), so the
+// sums go to row b + g of the workspace. A second kernel adds each group's
+// runs in order.
+template <class Tag, int ACT>
+__global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int b = blockIdx.x * 4 + w;
+  const int c = blockIdx.y * 512 + lane * 8;
+  const int nv = p.N - c >= 8 ? 8 : p.N - c;
+  const int r0 = b * kActGradRows, r1 = r0 + kActGradRows < p.M ? r0 + kActGradRows : p.M;
+  if (r0 >= r1 || nv <= 0) return;
+  // The group of the first row: the last one that starts at or before it.
+  int g = 0, lo = 0, end = p.M;
+  if (p.offsets) {
+    int hi = p.G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.offsets[mid] <= r0) lo = mid;
+      else hi = mid - 1;
+    }
+    g = lo;
+    end = p.offsets[g + 1];
+  }
+  const char* dY = static_cast<const char*>(p.dY);
+  const char* Z = static_cast<const char*>(p.Z);
+  char* dZ = static_cast<char*>(p.dZ);
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  int r = r0;
+  while (r < r1) {
+    while (g < p.G && r >= end) {  // the next group with rows
+      ++g;
+      if (g < p.G) end = p.offsets[g + 1];
+    }
+    if (g >= p.G) break;  // rows of no group
+    const int stop = end < r1 ? end : r1;
+#pragma unroll 4
+    for (; r < stop; ++r) {
+      float d[8];
+      layer_load8_16<Tag>(dY + ((int64_t)r * p.lddy + c) * 2, p.wide, nv, d);
+      if constexpr (ACT != ACT_NONE) {
+        float z[8];
+        layer_load8_16<Tag>(Z + ((int64_t)r * p.ldz + c) * 2, p.wide, nv, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] *= layer_slope<ACT>(z[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += d[e];
+      if (dZ) layer_store8_16<Tag>(dZ + ((int64_t)r * p.lddz + c) * 2, p.wide, nv, d);
+    }
+    if (p.db) {
+      float* out = p.part + (int64_t)(b + g) * p.N + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e < nv) out[e] = sum[e];
+        sum[e] = 0.0f;
+      }
+    }
+  }
+}
+
+// db[g][n]: the group's partial sums, a quarter of them for each wave, joined
+// in wave order.
+__global__ void __launch_bounds__(256) layer_bias_sum_kernel(const ActGradArgs p) {
+  __shared__ float x[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int g = blockIdx.y, n = blockIdx.x * 64 + lane;
+  int first = 0, count = p.M;
+  if (p.offsets) layer_group(p.offsets, g, p.M, first, count);
+  float s = 0.0f;
+  if (count > 0 && n < p.N) {
+    const int b0 = first / kActGradRows, b1 = (first + count - 1) / kActGradRows;
+    const float* part = p.part + (int64_t)g * p.N + n;
+    int b = b0 + w;
+    for (; b + 28 <= b1; b += 32) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(b + 4 * u) * p.N];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    for (; b <= b1; b += 4) s += part[(int64_t)b * p.N];
+  }
+  x[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && n < p.N)
+    p.db[(int64_t)g * p.N + n] = (x[0][lane] + x[1][lane]) + (x[2][lane] + x[3][lane]);
+}
+
+template <class Tag>
+hipError_t launch_act(const ActGradArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 block(256);
+  switch (a.act) {
+    case ACT_RELU:
+      return launch_kernel(layer_act_grad_kernel<Tag, ACT_RELU>, grid, block, s, a);
+    case ACT_GELU:
+      return launch_kernel(layer_act_grad_kernel<Tag, ACT_GELU>, grid, block, s, a);
+    case ACT_GELU_ERF:
+      return launch_kernel(layer_act_grad_kernel<Tag, ACT_GELU_ERF>, grid, block, s, a);
+    case ACT_SILU:
+      return launch_kernel(layer_act_grad_kernel<Tag, ACT_SILU>, grid, block, s, a);
+    default:
+      return launch_kernel(layer_act_grad_kernel<Tag, ACT_NONE>, grid, block, s, a);
+  }
+}
+
+// ----------------------------------------------------------------- dispatch --
+template <int PIECE>
+struct RowPiece;
+template <>
+struct RowPiece<16> { using type = u32x4; };
+template <>
+struct RowPiece<8> { using type = u32x2; };
+template <>
+struct RowPiece<4> { using type = unsigned; };
+template <>
+struct RowPiece<2> { using type = unsigned short; };
+
+// A wave takes one token and kDispatchSpan pieces a lane: the row is read
+// once, whatever the number of experts it goes to.
+template <int PIECE>
+__global__ void __launch_bounds__(256) layer_dispatch_kernel(const DispatchArgs p) {
+  using V = typename RowPiece<PIECE>::type;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + w;
+  if (t >= p.T) return;
+  const int64_t at = ((int64_t)blockIdx.y * kDispatchSpan * 64 + lane) * PIECE;
+  const char* src = p.X + (int64_t)t * p.ldx + at;
+  V v[kDispatchSpan];
+#pragma unroll
+  for (int u = 0; u < kDispatchSpan; ++u)
+    if (at + u * 64 * PIECE < p.bytes) v[u] = *reinterpret_cast<const V*>(src + u * 64 * PIECE);
+  const int rows = p.T * p.top;
+  for (int j = 0; j < p.top; ++j) {
+    const int to = p.slot[(int64_t)t * p.top + j];
+    if ((unsigned)to >= (unsigned)rows) continue;
+    char* dst = p.Xs + (int64_t)to * p.ldxs + at;
+#pragma unroll
+    for (int u = 0; u < kDispatchSpan; ++u)
+      if (at + u * 64 * PIECE < p.bytes) *reinterpret_cast<V*>(dst + u * 64 * PIECE) = v[u];
+  }
+}
+
+// ------------------------------------------------------------------ combine --
+// Elements of rows: loads and stores of E consecutive ones, as float32.
+struct RowF32 {};
+template <class Row, int E>
+struct RowIo {  // 16-bit types
+  __device__ static __forceinline__ void load(const void* base, int64_t at, float (&f)[E]) {
+    using V = typename RowPiece<2 * E>::type;
+    const V v = *reinterpret_cast<const V*>(static_cast<const unsigned short*>(base) + at);
+    const unsigned short* s = reinterpret_cast<const unsigned short*>(&v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = layer_f32(Row{}, s[e]);
+  }
+  __device__ static __forceinline__ void store(void* base, int64_t at, const float (&f)[E]) {
+    using V = typename RowPiece<2 * E>::type;
+    V v;
+    unsigned short* s = reinterpret_cast<unsigned short*>(&v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e] = layer_16(Row{}, f[e]);
+    *reinterpret_cast<V*>(static_cast<unsigned short*>(base) + at) = v;
+  }
+};
+template <int E>
+struct RowIo<RowF32, E> {
+  __device__ static __forceinline__ void load(const void* base, int64_t at, float (&f)[E]) {
+    using V = typename RowPiece<4 * E>::type;
+    const V v = *reinterpret_cast<const V*>(static_cast<const float*>(base) + at);
+    __builtin_memcpy(f, &v, 4 * E);
+  }
+  __device__ static __forceinline__ void store(void* base, int64_t at, const float (&f)[E]) {
+    using V = typename RowPiece<4 * E>::type;
+    V v;
+    __builtin_memcpy(&v, f, 4 * E);
+    *reinterpret_cast<V*>(static_cast<float*>(base) + at) = v;
+  }
+};
+
+// A wave takes one token and E columns a lane; four of the token's rows are
+// in flight at a time, added in the order of its choices.
+template <class Row, int E>
+__global__ void __launch_bounds__(256) layer_combine_kernel(const CombineArgs p) {
+  using Io = RowIo<Row, E>;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + w;
+  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * E;
+  if (t >= p.T || c >= p.H) return;
+  const int rows = p.T * p.top;
+  const int64_t t0 = (int64_t)t * p.top;
+  float sum[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+  for (int j0 = 0; j0 < p.top; j0 += 4) {
+    float f[4][E], wt[4];
+    bool in[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
+      const int at = j < p.top ? p.slot[t0 + j] : -1;
+      in[u] = (unsigned)at < (unsigned)rows;
+      if (in[u]) {
+        Io::load(p.Ys, (int64_t)at * p.ldys + c, f[u]);
+        wt[u] = p.weights ? p.weights[t0 + j] : 1.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (in[u]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = __builtin_fmaf(wt[u], f[u][e], sum[e]);
+      }
+  }
+  if (p.R) {
+    float r[E];
+    Io::load(p.R, (int64_t)t * p.ldr + c, r);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] += r[e];
+  }
+  Io::store(p.Y, (int64_t)t * p.ldy + c, sum);
+}
+
+// A workgroup takes one token; its threads share the columns, and their
+// parts of each choice's product are joined in thread order.
+template <class Row, int E>
+__global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGradArgs p) {
+  using Io = RowIo<Row, E>;
+  __shared__ float part[4][4];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int t = blockIdx.x;
+  const int rows = p.T * p.top;
+  const int64_t t0 = (int64_t)t * p.top;
+  for (int j0 = 0; j0 < p.top; j0 += 4) {
+    int at[4];
+    float wt[4], dot[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
+      at[u] = j < p.top ? p.slot[t0 + j] : -1;
+      if ((unsigned)at[u] >= (unsigned)rows) at[u] = -1;
+      wt[u] = at[u] >= 0 && p.weights ? p.weights[t0 + j] : 1.0f;
+      dot[u] = 0.0f;
+    }
+    for (int64_t c = (int64_t)tid * E; c < p.H; c += 256 * E) {
+      float d[E], y[4][E];
+      Io::load(p.dY, (int64_t)t * p.lddy + c, d);
+      if (p.dw) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (at[u] >= 0) Io::load(p.Ys, (int64_t)at[u] * p.ldys + c, y[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (at[u] < 0) continue;
+        if (p.dw) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) dot[u] = __builtin_fmaf(d[e], y[u][e], dot[u]);
+        }
+        if (p.dYs) {
+          float o[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = wt[u] * d[e];
+          Io::store(p.dYs, (int64_t)at[u] * p.lddys + c, o);
+        }
+      }
+    }
+    if (p.dw) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) dot[u] += __shfl_xor(dot[u], x, 64);
+        if (lane == 0) part[w][u] = dot[u];
+      }
+      __syncthreads();
+      if (tid < 4 && j0 + tid < p.top)
+        p.dw[t0 + j0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      __syncthreads();
+    }
+  }
+}
+
+template <class Row, int E>
+hipError_t combine(const CombineArgs& a, hipStream_t s) {
+  const dim3 grid((a.T + 3) / 4, (unsigned)combine_column_blocks(a));
+  return launch_kernel(layer_combine_kernel<Row, E>, grid, dim3(256), s, a);
+}
+template <class Row, int E>
+hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
+  return launch_kernel(layer_combine_grad_kernel<Row, E>, dim3(a.T), dim3(256), s, a);
+}
+
+}  // namespace
+
+hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s) {
+  if (a.M > 0) {
+    const int blocks = (a.M + kActGradRows - 1) / kActGradRows;
+    const dim3 grid((blocks + 3) / 4, act_grad_column_blocks(a.N));
+    const hipError_t e = dtype == 0 ? launch_act<TagF16>(a, grid, s) : launch_act<TagBF16>(a, grid, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.db) return hipSuccess;
+  return launch_kernel(layer_bias_sum_kernel, dim3((a.N + 63) / 64, a.G), dim3(256), s, a);
+}
+
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
+  const dim3 grid((a.T + 3) / 4, (unsigned)dispatch_column_blocks(a)), block(256);
+  if (a.piece == 16) return launch_kernel(layer_dispatch_kernel<16>, grid, block, s, a);
+  if (a.piece == 8) return launch_kernel(layer_dispatch_kernel<8>, grid, block, s, a);
+  if (a.piece == 4) return launch_kernel(layer_dispatch_kernel<4>, grid, block, s, a);
+  return launch_kernel(layer_dispatch_kernel<2>, grid, block, s, a);
+}
+
+hipError_t launch_combine(int rowtype, const CombineArgs& a, hipStream_t s) {
+  if (rowtype == ROW_F32) {
+    if (a.piece == 4) return combine<RowF32, 4>(a, s);
+    if (a.piece == 2) return combine<RowF32, 2>(a, s);
+    return combine<RowF32, 1>(a, s);
+  }
+  if (rowtype == ROW_F16) {
+    if (a.piece == 8) return combine<TagF16, 8>(a, s);
+    if (a.piece == 4) return combine<TagF16, 4>(a, s);
+    if (a.piece == 2) return combine<TagF16, 2>(a, s);
+    return combine<TagF16, 1>(a, s);
+  }
+  if (a.piece == 8) return combine<TagBF16, 8>(a, s);
+  if (a.piece == 4) return combine<TagBF16, 4>(a, s);
+  if (a.piece == 2) return combine<TagBF16, 2>(a, s);
+  return combine<TagBF16, 1>(a, s);
+}
+
+hipError_t launch_combine_grad(int rowtype, const CombineGradArgs& a, hipStream_t s) {
+  if (rowtype == ROW_F32) {
+    if (a.piece == 4) return combine_grad<RowF32, 4>(a, s);
+    if (a.piece == 2) return combine_grad<RowF32, 2>(a, s);
+    return combine_grad<RowF32, 1>(a, s);
+  }
+  if (rowtype == ROW_F16) {
+    if (a.piece == 8) return combine_grad<TagF16, 8>(a, s);
+    if (a.piece == 4) return combine_grad<TagF16, 4>(a, s);
+    if (a.piece == 2) return combine_grad<TagF16, 2>(a, s);
+    return combine_grad<TagF16, 1>(a, s);
+  }
+  if (a.piece == 8) return combine_grad<TagBF16, 8>(a, s);
+  if (a.piece == 4) return combine_grad<TagBF16, 4>(a, s);
+  if (a.piece == 2) return combine_grad<TagBF16, 2>(a, s);
+  return combine_grad<TagBF16, 1>(a, s);
+}
+
+}  // namespace dgt
