@@ -413,5 +413,14 @@ hipError_t layer_for_layout(const LayerArgs& a, bool ta, bool tb, F f) {
 // bf16. They return the HIP status of the launch.
 hipError_t launch_layer_general(int dtype, bool ta, bool tb, bool small, const LayerArgs& a,
                                 int ntiles, hipStream_t s);
+// Operands in whole 16-byte pieces (layer_direct in layer_api.hip). deep: ten
+// half-slots of LDS instead of five.
+hipError_t launch_layer_pp256(int dtype, bool ta, bool tb, const LayerArgs& a, int ntiles,
+                              hipStream_t s);
+hipError_t launch_layer_pp128(int dtype, bool ta, bool tb, bool deep, const LayerArgs& a,
+                              int ntiles, hipStream_t s);
+// 16 mt x 16 nt outputs a workgroup, A stored [M][K]; dense and by rows.
+hipError_t launch_layer_skinny(int dtype, bool tb, int mt, int nt, const LayerArgs& a, int ntiles,
+                               hipStream_t s);
 
 }  // namespace dgt

@@ -102,20 +102,26 @@ bool wide16(const Mat& m) {
 }
 
 // ----------------------------------------------------------------- products --
-enum LayerKernel : int { LK_GENERAL128 = 0, LK_GENERAL64, NUM_LAYER_KERNELS };
+enum LayerKernel : int {
+  LK_GENERAL128 = 0, LK_GENERAL64, LK_PP256, LK_PP128, LK_PP128_DEEP,
+  LK_SKINNY16, LK_SKINNY16N16, LK_SKINNY32, LK_SKINNY48, LK_SKINNY64, NUM_LAYER_KERNELS
+};
 struct LayerKernelInfo {
   const char* name;
   int bm, bn;
 };
 const LayerKernelInfo kLayerKernels[NUM_LAYER_KERNELS] = {
-    {"g128x128", 128, 128},
-    {"g64x64", 64, 64},
+    {"g128x128", 128, 128}, {"g64x64", 64, 64},     {"pp256x256", 256, 256},
+    {"pp128x128", 128, 128}, {"pp128x128deep", 128, 128},
+    {"s16x32", 16, 32},     {"s16x16", 16, 16},     {"s32x32", 32, 32},
+    {"s48x32", 48, 32},     {"s64x32", 64, 32},
 };
 
 struct LayerPlan {
   LayerArgs a{};
   int dtype = 0;
   bool ta = false, tb = false;
+  bool direct = false;  // both operands load in whole 16-byte pieces
   int kernel = LK_GENERAL128;
   int ntiles = 0;  // workgroups that cover every tile (by rows: at least)
 };
@@ -150,9 +156,42 @@ int64_t count_tiles(const LayerArgs& a, const LayerKernelInfo& k) {
          (a.mode == LAYER_SUM ? a.G : 1);
 }
 
+// Whether an operand loads in whole 16-byte pieces with 32-bit offsets over the
+// 257 rows that a tile of any kernel spans. `along` is its contiguous dimension.
+bool layer_direct(const Mat& m, int64_t along) {
+  return wide16(m) && along % 8 == 0 && m.ld < (int64_t{1} << 31) / (2 * 257) - 4096;
+}
+
+// Whether kernel k can run the call at all.
+bool kernel_runs(const LayerPlan& pl, int k) {
+  if (k == LK_GENERAL128 || k == LK_GENERAL64) return true;
+  if (!pl.direct || pl.a.K == 0) return false;
+  if (k < LK_SKINNY16) return true;
+  if (pl.ta || pl.a.mode == LAYER_SUM) return false;
+  // B stored [K][N] is laid out for 32 columns and 16, 32 or 64 rows.
+  return pl.tb || (k != LK_SKINNY16N16 && k != LK_SKINNY48);
+}
+
 int choose_kernel(const LayerPlan& pl) {
-  // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
-  return count_tiles(pl.a, kLayerKernels[LK_GENERAL128]) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
+  const LayerArgs& a = pl.a;
+  auto tiles = [&](int k) { return count_tiles(a, kLayerKernels[k]); };
+  if (!kernel_runs(pl, LK_PP256))
+    // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
+    return tiles(LK_GENERAL128) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
+  const int64_t rows = a.mode == LAYER_ROWS ? (a.M + a.G - 1) / a.G : a.M;
+  // Few rows: the weights' bytes count, and a wave's loads in flight. Groups'
+  // sizes are only known on average, and a group that needs a second row tile
+  // reads its weights twice (64 groups of 2048x2048, us, 16-row tiles against
+  // 64x64 ones: 94 and 108 at 2 rows a group, 182 and 133 at 16).
+  if (kernel_runs(pl, LK_SKINNY16) && rows <= (a.mode == LAYER_ROWS ? 8 : 64)) {
+    if (rows <= 16)
+      return pl.tb && a.mode == LAYER_DENSE && a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY16;
+    if (rows <= 32) return LK_SKINNY32;
+    return rows <= 48 && pl.tb ? LK_SKINNY48 : LK_SKINNY64;
+  }
+  const int64_t n256 = tiles(LK_PP256);
+  if (n256 >= 256 || (n256 >= 192 && a.K >= 1024) || (n256 >= 128 && a.K >= 2048)) return LK_PP256;
+  return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
 int plan_tiles(LayerPlan& pl, const char* op) {
@@ -164,6 +203,8 @@ int plan_tiles(LayerPlan& pl, const char* op) {
       if (std::strcmp(want, kLayerKernels[k].name) == 0) found = k;
     if (found < 0)
       return fail(GEMM_ERR_INVALID_ARG, std::string("GEMM_LAYER_TILE names no kernel: ") + want);
+    if (!kernel_runs(pl, found))
+      return fail(GEMM_ERR_UNSUPPORTED, std::string("GEMM_LAYER_TILE cannot run this call: ") + want);
     pl.kernel = found;
   }
   const LayerKernelInfo& k = kLayerKernels[pl.kernel];
@@ -181,8 +222,20 @@ int plan_tiles(LayerPlan& pl, const char* op) {
 }
 
 hipError_t launch_product(const LayerPlan& pl, hipStream_t s) {
-  return launch_layer_general(pl.dtype, pl.ta, pl.tb, pl.kernel == LK_GENERAL64, pl.a, pl.ntiles,
-                              s);
+  switch (pl.kernel) {
+    case LK_PP256: return launch_layer_pp256(pl.dtype, pl.ta, pl.tb, pl.a, pl.ntiles, s);
+    case LK_PP128:
+    case LK_PP128_DEEP:
+      return launch_layer_pp128(pl.dtype, pl.ta, pl.tb, pl.kernel == LK_PP128_DEEP, pl.a, pl.ntiles, s);
+    case LK_GENERAL128:
+    case LK_GENERAL64:
+      return launch_layer_general(pl.dtype, pl.ta, pl.tb, pl.kernel == LK_GENERAL64, pl.a,
+                                  pl.ntiles, s);
+    default: {
+      const LayerKernelInfo& k = kLayerKernels[pl.kernel];
+      return launch_layer_skinny(pl.dtype, pl.tb, k.bm / 16, k.bn / 16, pl.a, pl.ntiles, s);
+    }
+  }
 }
 
 // Dense and by-rows products (G < 0: dense).
@@ -270,6 +323,7 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
   pl.dtype = dtype;
   pl.ta = ta;
   pl.tb = tb;
+  pl.direct = layer_direct(ma, ta ? M : K) && layer_direct(mb, tb ? K : N);
   return plan_tiles(pl, dense ? "linear" : "grouped");
 }
 
@@ -329,6 +383,7 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
   pl.dtype = dtype;
   pl.ta = true;
   pl.tb = false;
+  pl.direct = M > 0 && layer_direct(ma, N) && layer_direct(mb, K);
   return plan_tiles(pl, "grad_weight");
 }
 

@@ -1,0 +1,73 @@
+// The layer operators' product on 256x256 tiles: the two-group loop of
+// gemm_mfma_pingpong.h with the layer epilogue, for operands whose rows load in
+// whole 16-byte pieces. Dense, by rows and by sum; pieces outside a group's
+// rows, columns or sum read as zeros.
+//
+// One tile a workgroup: the grid may be an upper bound (groups held on the
+// GPU), and a workgroup past the last tile ends at once.
+#include "gemm_mfma_pingpong.h"
+#include "layer.h"
+
+namespace dgt {
+
+namespace {
+
+template <class Tag, int MODE, bool AMN, bool BMN>
+__global__ void __launch_bounds__(PingPongCfg::THREADS) layer_pp256_kernel(const LayerArgs p) {
+  using C = PingPongCfgT<AMN ? 32 : 16>;  // the atom: see gemm_mfma_pingpong.h
+  using At = typename C::At;
+  using acc_t = typename At::acc_t;
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS_BYTES];
+  static_assert(8 * layer_lds_bytes<C>() <= C::LDS_BYTES, "the epilogue's rows fit the operand LDS");
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave >> 2;
+  const int wm = group, wn = wave & 3;
+  const int total = layer_tiles<MODE, C::BM>(p, threadIdx.x & 63);
+  if ((int)blockIdx.x >= total) return;
+  const int lane = threadIdx.x & 63;
+  int t = blockIdx.x;
+  LayerTile q = layer_tile<MODE, C::BM, C::BN>(p, t, total, lane);
+  GemmArgs ga{};  // what the loop reads of it
+  ga.A = q.A;
+  ga.B = q.B;
+  ga.lda = p.lda;
+  ga.ldb = p.ldb;
+  ga.M = q.M;
+  ga.N = q.N;
+  ga.K = q.K;
+  PingPongPipe<AMN, BMN, At::M, true> pipe;
+  pipe.init(ga, smem, q.m0, q.n0, group, wave, lane, wm, wn);
+  acc_t acc[C::TM][C::TN];
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int v = 0; v < At::NACC; ++v) acc[i][j][v] = 0.0f;
+  pp_mainloop<C, Tag, MODE, AMN, BMN, true>(acc, pipe, q.K, group);
+  // The tile is found again rather than kept in scalar registers, which the
+  // loop has none to spare of.
+  asm volatile("" : "+s"(t));
+  q = layer_tile<MODE, C::BM, C::BN>(p, t, total, lane);
+  layer_store<C, Tag>(acc, p, q, q.m0 + wm * C::WTM, q.n0 + wn * C::WTN, lane,
+                      reinterpret_cast<float*>(smem + wave * layer_lds_bytes<C>()));
+}
+
+template <class Tag>
+hipError_t launch(bool ta, bool tb, const LayerArgs& a, int ntiles, hipStream_t s) {
+  return layer_for_layout(a, ta, tb, [&](auto mode, auto la, auto lb) {
+    return launch_kernel(layer_pp256_kernel<Tag, mode.value, la.value != 0, lb.value == 0>,
+                         dim3(ntiles), dim3(PingPongCfg::THREADS), s, a);
+  });
+}
+
+}  // namespace
+
+hipError_t launch_layer_pp256(int dtype, bool ta, bool tb, const LayerArgs& a, int ntiles,
+                              hipStream_t s) {
+  if (dtype == 0) return launch<TagF16>(ta, tb, a, ntiles, s);
+  return launch<TagBF16>(ta, tb, a, ntiles, s);
+}
+
+}  // namespace dgt
