@@ -104,7 +104,8 @@ bool wide16(const Mat& m) {
 // ----------------------------------------------------------------- products --
 enum LayerKernel : int {
   LK_GENERAL128 = 0, LK_GENERAL64, LK_PP256, LK_PP128, LK_PP128_DEEP,
-  LK_SKINNY16, LK_SKINNY16N16, LK_SKINNY32, LK_SKINNY48, LK_SKINNY64, NUM_LAYER_KERNELS
+  LK_SKINNY16, LK_SKINNY16N16, LK_SKINNY32, LK_SKINNY48, LK_SKINNY64, LK_SKINNY64N64,
+  NUM_LAYER_KERNELS
 };
 struct LayerKernelInfo {
   const char* name;
@@ -115,6 +116,7 @@ const LayerKernelInfo kLayerKernels[NUM_LAYER_KERNELS] = {
     {"pp128x128", 128, 128}, {"pp128x128deep", 128, 128},
     {"s16x32", 16, 32},     {"s16x16", 16, 16},     {"s32x32", 32, 32},
     {"s48x32", 48, 32},     {"s64x32", 64, 32},
+    {"s64x64", 64, 64},
 };
 
 struct LayerPlan {
@@ -191,6 +193,11 @@ int choose_kernel(const LayerPlan& pl) {
   }
   const int64_t n256 = tiles(LK_PP256);
   if (n256 >= 256 || (n256 >= 192 && a.K >= 1024) || (n256 >= 128 && a.K >= 2048)) return LK_PP256;
+  // One round of 64-row tiles with the sum split over waves.
+  if (kernel_runs(pl, LK_SKINNY64) && a.mode == LAYER_DENSE) {
+    if (tiles(LK_SKINNY64) <= 256) return LK_SKINNY64;
+    if (tiles(LK_SKINNY64N64) <= 256) return LK_SKINNY64N64;
+  }
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
@@ -424,8 +431,9 @@ int check_workspace(const void* ws, int64_t have, int64_t need) {
 
 int64_t act_grad_bytes(int64_t G, int64_t M, int64_t N) {
   if (G < 0 || M < 0 || N < 0 || G > kMaxGroups || M > kMaxDim || N > kMaxDim) return 0;
+  const int64_t rows = act_grad_rows(M, N);
   const unsigned __int128 b =
-      (unsigned __int128)((M + kActGradRows - 1) / kActGradRows + G) * (unsigned __int128)N * 4;
+      (unsigned __int128)((M + rows - 1) / rows + G) * (unsigned __int128)N * 4;
   return b > (unsigned __int128)INT64_MAX ? 0 : (int64_t)b;
 }
 
@@ -617,6 +625,7 @@ int gemm_act_grad(int64_t G, int64_t M, int64_t N, int dtype, int act, const int
     a.M = (int)M;
     a.N = (int)N;
     a.act = act;
+    a.rows = act_grad_rows(M, N);
     a.wide = wide16(my) && (!Z || wide16(mz)) && (!dZ || wide16(md));
     set_path(std::string("act_grad act=") + kActNames[act] + (dZ ? " dz" : "") + (db ? " db" : ""));
     return launched(launch_act_grad(dtype, a, static_cast<hipStream_t>(stream)));
@@ -742,7 +751,8 @@ int gemm_combine(int64_t T, int64_t top, int64_t H, int dtype, const void* Ys, i
     a.H = (int)H;
     const Mat* mats[] = {&mi, &mr, &my};
     a.piece = common_piece(H, elem, mats);
-    CHECK(check_span(combine_column_blocks(a)));
+    if (combine_waves(a) > 0x7ffffff0)
+      return fail(GEMM_ERR_UNSUPPORTED, "too many pieces of rows for one launch");
     set_path("combine in pieces of " + std::to_string(a.piece * elem) + " bytes");
     return launched(launch_combine(rowtype, a, static_cast<hipStream_t>(stream)));
   });

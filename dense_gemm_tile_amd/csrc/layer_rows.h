@@ -19,10 +19,18 @@ struct ActGradArgs {
   float* part;         // partial column sums
   int64_t lddy, ldz, lddz;
   int G, M, N, act;
+  int rows;            // act_grad_rows(M, N)
   int wide;            // rows of all three allow 16-byte accesses
 };
-// Rows that one wave sums by itself: a partial sum is kept for each.
-constexpr int kActGradRows = 32;
+// Rows that one wave sums by itself (a partial sum is kept for each): 32, fewer
+// where that would leave less than 16 waves to a CU. At 4096 x 4096 with GELU,
+// 32 rows a wave (4 waves a CU) take 51 us, MEASURE.
+inline int act_grad_rows(int64_t m, int64_t n) {
+  const int64_t blocks = (n + 511) / 512;
+  int rows = 32;
+  while (rows > 4 && (m + rows - 1) / rows * blocks < 16 * 256) rows /= 2;
+  return rows;
+}
 inline unsigned act_grad_column_blocks(int64_t n) { return (unsigned)((n + 511) / 512); }
 hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s);
 
@@ -67,8 +75,9 @@ struct CombineArgs {
   int T, top, H;
   int piece;  // elements per access
 };
-inline int64_t combine_column_blocks(const CombineArgs& a) {
-  return ((int64_t)a.H + 64 * a.piece - 1) / (64 * a.piece);
+// Waves that a call's rows are cut into.
+inline int64_t combine_waves(const CombineArgs& a) {
+  return a.T * (((int64_t)a.H + 64 * a.piece - 1) / (64 * a.piece));
 }
 hipError_t launch_combine(int rowtype, const CombineArgs& a, hipStream_t s);
 

@@ -11,7 +11,7 @@ namespace {
 
 // ------------------------------------------------- activation and bias grads --
 // dZ = dY * act'(Z), and sums of dZ over rows before it is rounded. A wave
-// takes kActGradRows rows of 512 columns (8 a lane) and keeps 8 float32 sums;
+// takes p.rows rows of 512 columns (8 a lane) and keeps 8 float32 sums;
 // where its rows cross from one group to the next it starts new ones. Rows
 // block b and group g meet in at most one run of rows, and b + g is another
 // number for each run (each next run has the next b or the next g), so the
@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p
   const int b = blockIdx.x * 4 + w;
   const int c = blockIdx.y * 512 + lane * 8;
   const int nv = p.N - c >= 8 ? 8 : p.N - c;
-  const int r0 = b * kActGradRows, r1 = r0 + kActGradRows < p.M ? r0 + kActGradRows : p.M;
+  const int r0 = b * p.rows, r1 = r0 + p.rows < p.M ? r0 + p.rows : p.M;
   if (r0 >= r1 || nv <= 0) return;
   // The group of the first row: the last one that starts at or before it.
   int g = 0, lo = 0, end = p.M;
@@ -51,20 +51,30 @@ __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p
     }
     if (g >= p.G) break;  // rows of no group
     const int stop = end < r1 ? end : r1;
-#pragma unroll 4
-    for (; r < stop; ++r) {
-      float d[8];
-      layer_load8_16<Tag>(dY + ((int64_t)r * p.lddy + c) * 2, p.wide, nv, d);
-      if constexpr (ACT != ACT_NONE) {
-        float z[8];
-        layer_load8_16<Tag>(Z + ((int64_t)r * p.ldz + c) * 2, p.wide, nv, z);
+    // Rows in batches whose loads are all requested before the first store
+    // (dZ may be dY or Z, so the compiler would not move them across).
+    auto batch = [&](auto count) {
+      constexpr int R = count.value;
+      float d[R][8], z[R][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] *= layer_slope<ACT>(z[e]);
+      for (int u = 0; u < R; ++u) {
+        layer_load8_16<Tag>(dY + ((int64_t)(r + u) * p.lddy + c) * 2, p.wide, nv, d[u]);
+        if constexpr (ACT != ACT_NONE)
+          layer_load8_16<Tag>(Z + ((int64_t)(r + u) * p.ldz + c) * 2, p.wide, nv, z[u]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += d[e];
-      if (dZ) layer_store8_16<Tag>(dZ + ((int64_t)r * p.lddz + c) * 2, p.wide, nv, d);
-    }
+      for (int u = 0; u < R; ++u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (ACT != ACT_NONE) d[u][e] *= layer_slope<ACT>(z[u][e]);
+          sum[e] += d[u][e];
+        }
+        if (dZ) layer_store8_16<Tag>(dZ + ((int64_t)(r + u) * p.lddz + c) * 2, p.wide, nv, d[u]);
+      }
+      r += R;
+    };
+    while (r + 4 <= stop) batch(LayerConst<4>{});
+    while (r < stop) batch(LayerConst<1>{});
     if (p.db) {
       float* out = p.part + (int64_t)(b + g) * p.N + c;
 #pragma unroll
@@ -76,32 +86,37 @@ __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p
   }
 }
 
-// db[g][n]: the group's partial sums, a quarter of them for each wave, joined
-// in wave order.
-__global__ void __launch_bounds__(256) layer_bias_sum_kernel(const ActGradArgs p) {
-  __shared__ float x[4][64];
+// db[g][n]: the group's partial sums, every kSumWaves-th of them for each wave,
+// joined in wave order.
+constexpr int kSumWaves = 16;
+__global__ void __launch_bounds__(64 * kSumWaves) layer_bias_sum_kernel(const ActGradArgs p) {
+  __shared__ float x[kSumWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = blockIdx.y, n = blockIdx.x * 64 + lane;
   int first = 0, count = p.M;
   if (p.offsets) layer_group(p.offsets, g, p.M, first, count);
   float s = 0.0f;
   if (count > 0 && n < p.N) {
-    const int b0 = first / kActGradRows, b1 = (first + count - 1) / kActGradRows;
+    const int b0 = first / p.rows, b1 = (first + count - 1) / p.rows;
     const float* part = p.part + (int64_t)g * p.N + n;
     int b = b0 + w;
-    for (; b + 28 <= b1; b += 32) {
+    for (; b + 7 * kSumWaves <= b1; b += 8 * kSumWaves) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(b + 4 * u) * p.N];
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(b + u * kSumWaves) * p.N];
 #pragma unroll
       for (int u = 0; u < 8; ++u) s += v[u];
     }
-    for (; b <= b1; b += 4) s += part[(int64_t)b * p.N];
+    for (; b <= b1; b += kSumWaves) s += part[(int64_t)b * p.N];
   }
   x[w][lane] = s;
   __syncthreads();
-  if (w == 0 && n < p.N)
-    p.db[(int64_t)g * p.N + n] = (x[0][lane] + x[1][lane]) + (x[2][lane] + x[3][lane]);
+  if (w == 0 && n < p.N) {
+    s = x[0][lane];
+#pragma unroll
+    for (int u = 1; u < kSumWaves; ++u) s += x[u][lane];
+    p.db[(int64_t)g * p.N + n] = s;
+  }
 }
 
 template <class Tag>
@@ -194,14 +209,18 @@ struct RowIo<RowF32, E> {
   }
 };
 
-// A wave takes one token and E columns a lane; four of the token's rows are
-// in flight at a time, added in the order of its choices.
+// A wave takes E columns a lane of one token, and neighbouring waves the
+// token's other columns, so that whole rows are read at about the same time
+// (one 1 KiB piece of every token first: MEASURE). Four of the
+// token's rows are in flight at a time, added in the order of its choices.
 template <class Row, int E>
 __global__ void __launch_bounds__(256) layer_combine_kernel(const CombineArgs p) {
   using Io = RowIo<Row, E>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + w;
-  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * E;
+  const int wid = blockIdx.x * 4 + w;
+  const int across = (p.H + 64 * E - 1) / (64 * E);
+  const int t = wid / across;
+  const int64_t c = ((int64_t)(wid - t * across) * 64 + lane) * E;
   if (t >= p.T || c >= p.H) return;
   const int rows = p.T * p.top;
   const int64_t t0 = (int64_t)t * p.top;
@@ -298,8 +317,8 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
 
 template <class Row, int E>
 hipError_t combine(const CombineArgs& a, hipStream_t s) {
-  const dim3 grid((a.T + 3) / 4, (unsigned)combine_column_blocks(a));
-  return launch_kernel(layer_combine_kernel<Row, E>, grid, dim3(256), s, a);
+  return launch_kernel(layer_combine_kernel<Row, E>, dim3((unsigned)((combine_waves(a) + 3) / 4)),
+                       dim3(256), s, a);
 }
 template <class Row, int E>
 hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
@@ -310,13 +329,14 @@ hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
 
 hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s) {
   if (a.M > 0) {
-    const int blocks = (a.M + kActGradRows - 1) / kActGradRows;
+    const int blocks = (a.M + a.rows - 1) / a.rows;
     const dim3 grid((blocks + 3) / 4, act_grad_column_blocks(a.N));
     const hipError_t e = dtype == 0 ? launch_act<TagF16>(a, grid, s) : launch_act<TagBF16>(a, grid, s);
     if (e != hipSuccess) return e;
   }
   if (!a.db) return hipSuccess;
-  return launch_kernel(layer_bias_sum_kernel, dim3((a.N + 63) / 64, a.G), dim3(256), s, a);
+  return launch_kernel(layer_bias_sum_kernel, dim3((a.N + 63) / 64, a.G), dim3(64 * kSumWaves),
+                       s, a);
 }
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
