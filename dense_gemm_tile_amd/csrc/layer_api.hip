@@ -170,8 +170,7 @@ bool kernel_runs(const LayerPlan& pl, int k) {
   if (!pl.direct || pl.a.K == 0) return false;
   if (k < LK_SKINNY16) return true;
   if (pl.ta || pl.a.mode == LAYER_SUM) return false;
-  // B stored [K][N] is laid out for 32 columns and 16, 32 or 64 rows.
-  return pl.tb || (k != LK_SKINNY16N16 && k != LK_SKINNY48);
+  return pl.tb || k != LK_SKINNY16N16;  // 16 columns of B stored [K][N] are half a line
 }
 
 int choose_kernel(const LayerPlan& pl) {
@@ -181,23 +180,24 @@ int choose_kernel(const LayerPlan& pl) {
     // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
     return tiles(LK_GENERAL128) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
   const int64_t rows = a.mode == LAYER_ROWS ? (a.M + a.G - 1) / a.G : a.M;
+  const bool split = kernel_runs(pl, LK_SKINNY64N64);
   // Few rows: the weights' bytes count, and a wave's loads in flight. Groups'
   // sizes are only known on average, and a group that needs a second row tile
-  // reads its weights twice (64 groups of 2048x2048, us, 16-row tiles against
-  // 64x64 ones: 94 and 108 at 2 rows a group, 182 and 133 at 16).
-  if (kernel_runs(pl, LK_SKINNY16) && rows <= (a.mode == LAYER_ROWS ? 8 : 64)) {
-    if (rows <= 16)
-      return pl.tb && a.mode == LAYER_DENSE && a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY16;
-    if (rows <= 32) return LK_SKINNY32;
-    return rows <= 48 && pl.tb ? LK_SKINNY48 : LK_SKINNY64;
+  // reads its weights twice.
+  if (split && rows <= (a.mode == LAYER_ROWS ? 8 : 64)) {
+    if (rows <= 16) {
+      if (a.mode == LAYER_ROWS || !pl.tb) return LK_SKINNY16;
+      return a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY32;
+    }
+    return rows <= 32 ? LK_SKINNY32 : rows <= 48 ? LK_SKINNY48 : LK_SKINNY64;
   }
   const int64_t n256 = tiles(LK_PP256);
   if (n256 >= 256 || (n256 >= 192 && a.K >= 1024) || (n256 >= 128 && a.K >= 2048)) return LK_PP256;
-  // One round of 64-row tiles with the sum split over waves.
-  if (kernel_runs(pl, LK_SKINNY64) && a.mode == LAYER_DENSE) {
-    if (tiles(LK_SKINNY64) <= 256) return LK_SKINNY64;
-    if (tiles(LK_SKINNY64N64) <= 256) return LK_SKINNY64N64;
-  }
+  // One round of small tiles with the sum split over waves: the smallest that
+  // fits the CUs.
+  if (split && a.mode == LAYER_DENSE)
+    for (int k : {LK_SKINNY32, LK_SKINNY64, LK_SKINNY64N64})
+      if (tiles(k) <= 256) return k;
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
@@ -240,7 +240,8 @@ hipError_t launch_product(const LayerPlan& pl, hipStream_t s) {
                                   pl.ntiles, s);
     default: {
       const LayerKernelInfo& k = kLayerKernels[pl.kernel];
-      return launch_layer_skinny(pl.dtype, pl.tb, k.bm / 16, k.bn / 16, pl.a, pl.ntiles, s);
+      if (k.bm == 16 && pl.tb) return launch_layer_skinny(pl.dtype, k.bn / 16, pl.a, pl.ntiles, s);
+      return launch_layer_split(pl.dtype, pl.tb, k.bm / 16, k.bn / 16, pl.a, pl.ntiles, s);
     }
   }
 }

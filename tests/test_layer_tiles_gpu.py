@@ -15,10 +15,10 @@ pytestmark = pytest.mark.gpu
 LAYOUTS = [(0, 1), (0, 0), (1, 0), (1, 1)]
 TILES = {"g128x128": (128, 128), "g64x64": (64, 64), "pp256x256": (256, 256), "pp128x128": (128, 128),
          "pp128x128deep": (128, 128)}
-# A stored [M][K]; the last two with B stored [N][K] only.
+# A stored [M][K]; s16x16 with B stored [N][K] only.
 SKINNY = {"s16x32": (16, 32), "s32x32": (32, 32), "s64x32": (64, 32), "s64x64": (64, 64),
           "s16x16": (16, 16), "s48x32": (48, 32)}
-NT_ONLY = ("s16x16", "s48x32")
+NT_ONLY = ("s16x16",)
 
 
 @contextmanager
