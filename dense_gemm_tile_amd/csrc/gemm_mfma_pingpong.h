@@ -141,10 +141,15 @@ typedef short pp_i16x4 __attribute__((ext_vector_type(4)));
 // out-of-range offset, so they read as zeros; the contiguous dimension must
 // fill whole 16-byte pieces (the M/N-contiguous form: 16-bit elements, a
 // multiple of 8).
-template <bool MN, int NFRAG, int ATOM = 32, bool MASK = false>
+// PP_RECORDS: the resource's record count alone masks the rows past the operand
+// (rows past the last one have larger offsets), so a piece costs one addition
+// and no comparison; its contiguous dimension must fill whole tiles (K-contiguous:
+// K a multiple of 64; M/N-contiguous: M or N of 256).
+enum PpMask : int { PP_WHOLE = 0, PP_MASKED = 1, PP_RECORDS = 2 };
+template <bool MN, int NFRAG, int ATOM = 32, int MASK = PP_WHOLE>
 struct PpOperand;
 
-template <int NFRAG, int ATOM, bool MASK>
+template <int NFRAG, int ATOM, int MASK>
 struct PpOperand<false, NFRAG, ATOM, MASK> {
   using C = PingPongCfgT<ATOM>;
   using At = typename C::At;
@@ -201,6 +206,11 @@ struct PpOperand<false, NFRAG, ATOM, MASK> {
       const int soff = slice * 128 + i * 8 * ld2;  // a slice is 128 bytes of each row
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base), (pp_lds_ptr_t)(slot + (lw * 8 + i) * 1024),
                                                16, voff, soff, 0, 0);
+    } else if constexpr (MASK == PP_RECORDS) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc_n(base, nrec),
+                                               (pp_lds_ptr_t)(slot + (lw * 8 + i) * 1024), 16,
+                                               row + (chunk << 4) + (slice * 128 + i * 8 * ld2), 0,
+                                               0, 0);
     } else {
       const int kb = slice * 128 + (chunk << 4);  // the piece's first byte in its row
       const int voff = ((rmask >> i) & 1) && kb < kbytes ? row + i * 8 * ld2 + kb : kOutOfRange;
@@ -223,7 +233,7 @@ struct PpOperand<false, NFRAG, ATOM, MASK> {
   }
 };
 
-template <int NFRAG, int ATOM, bool MASK>
+template <int NFRAG, int ATOM, int MASK>
 struct PpOperand<true, NFRAG, ATOM, MASK> {
   using C = PingPongCfgT<ATOM>;
   static constexpr int NV = ATOM == 16 ? 4 : 2;  // distinct load offsets
@@ -276,6 +286,10 @@ struct PpOperand<true, NFRAG, ATOM, MASK> {
     if constexpr (!MASK) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(b), (pp_lds_ptr_t)(slot + (lw * 8 + i) * 1024),
                                                16, voff[q], (int)(2 * i * ld * 2), 0, 0);
+    } else if constexpr (MASK == PP_RECORDS) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc_n(b, nrec_slice(slice)),
+                                               (pp_lds_ptr_t)(slot + (lw * 8 + i) * 1024), 16,
+                                               voff[q] + (int)(2 * i * ld * 2), 0, 0, 0);
     } else {
       // This lane's K row is slice*64 + 16 lw + 2 i + l/32.
       const int krem = krem0 - slice * C::BK - 2 * i;
@@ -348,7 +362,7 @@ __device__ __forceinline__ void pp_multiply(typename C::At::acc_t (&acc)[C::TM][
   }
 }
 
-template <bool AMN, bool BMN, int ATOM, bool MASK = false>
+template <bool AMN, bool BMN, int ATOM, int MASK = PP_WHOLE>
 struct PingPongPipe {
   using C = PingPongCfgT<ATOM>;
   char* smem;
@@ -410,11 +424,11 @@ struct PingPongPipe {
     if constexpr (MN) {
 #pragma unroll
       for (int q = 0; q < Op::NV; ++q) asm volatile("" : "+v"(x.voff[q]));
-      if constexpr (MASK) asm volatile("" : "+v"(x.cmask), "+v"(x.krem0));
+      if constexpr (MASK == PP_MASKED) asm volatile("" : "+v"(x.cmask), "+v"(x.krem0));
     } else {
       asm volatile("" : "+v"(x.row), "+v"(x.c0));
       if constexpr (ATOM == 16) asm volatile("" : "+v"(x.c1));
-      if constexpr (MASK) asm volatile("" : "+v"(x.rmask));
+      if constexpr (MASK == PP_MASKED) asm volatile("" : "+v"(x.rmask));
     }
   }
 };
@@ -428,7 +442,7 @@ struct PingPongPipe {
 // this compiler's host pass rejects a second kernel (same Tag, other
 // epilogue) calling a device function template specialization already
 // instantiated for the first one.
-template <class C, class Tag, int EPI, bool AMN, bool BMN, bool MASK>
+template <class C, class Tag, int EPI, bool AMN, bool BMN, int MASK>
 __device__ __forceinline__ void pp_mainloop(typename C::At::acc_t (&acc)[C::TM][C::TN],
                                             const PingPongPipe<AMN, BMN, C::At::M, MASK>& pipe,
                                             int K, int group) {

@@ -12,7 +12,7 @@ namespace dgt {
 
 namespace {
 
-template <class Tag, int MODE, bool AMN, bool BMN>
+template <class Tag, int MODE, bool AMN, bool BMN, int MASK>
 __global__ void __launch_bounds__(PingPongCfg::THREADS) layer_pp256_kernel(const LayerArgs p) {
   using C = PingPongCfgT<AMN ? 32 : 16>;  // the atom: see gemm_mfma_pingpong.h
   using At = typename C::At;
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(PingPongCfg::THREADS) layer_pp256_kernel(const
   ga.M = q.M;
   ga.N = q.N;
   ga.K = q.K;
-  PingPongPipe<AMN, BMN, At::M, true> pipe;
+  PingPongPipe<AMN, BMN, At::M, MASK> pipe;
   pipe.init(ga, smem, q.m0, q.n0, group, wave, lane, wm, wn);
   acc_t acc[C::TM][C::TN];
 #pragma unroll
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(PingPongCfg::THREADS) layer_pp256_kernel(const
     for (int j = 0; j < C::TN; ++j)
 #pragma unroll
       for (int v = 0; v < At::NACC; ++v) acc[i][j][v] = 0.0f;
-  pp_mainloop<C, Tag, MODE, AMN, BMN, true>(acc, pipe, q.K, group);
+  pp_mainloop<C, Tag, MODE, AMN, BMN, MASK>(acc, pipe, q.K, group);
   // The tile is found again rather than kept in scalar registers, which the
   // loop has none to spare of.
   asm volatile("" : "+s"(t));
@@ -54,20 +54,28 @@ __global__ void __launch_bounds__(PingPongCfg::THREADS) layer_pp256_kernel(const
                       reinterpret_cast<float*>(smem + wave * layer_lds_bytes<C>()));
 }
 
-template <class Tag>
+template <class Tag, int MASK>
 hipError_t launch(bool ta, bool tb, const LayerArgs& a, int ntiles, hipStream_t s) {
   return layer_for_layout(a, ta, tb, [&](auto mode, auto la, auto lb) {
-    return launch_kernel(layer_pp256_kernel<Tag, mode.value, la.value != 0, lb.value == 0>,
+    return launch_kernel(layer_pp256_kernel<Tag, mode.value, la.value != 0, lb.value == 0, MASK>,
                          dim3(ntiles), dim3(PingPongCfg::THREADS), s, a);
   });
+}
+template <class Tag>
+hipError_t launch_mask(bool ta, bool tb, const LayerArgs& a, int ntiles, hipStream_t s) {
+  // By sum, K is a group's rows: any number of them will do there, as for every
+  // operand not stored along K.
+  const bool records = (ta ? a.M % 256 == 0 : a.K % 64 == 0) && (tb ? a.K % 64 == 0 : a.N % 256 == 0);
+  return records ? launch<Tag, PP_RECORDS>(ta, tb, a, ntiles, s)
+                 : launch<Tag, PP_MASKED>(ta, tb, a, ntiles, s);
 }
 
 }  // namespace
 
 hipError_t launch_layer_pp256(int dtype, bool ta, bool tb, const LayerArgs& a, int ntiles,
                               hipStream_t s) {
-  if (dtype == 0) return launch<TagF16>(ta, tb, a, ntiles, s);
-  return launch<TagBF16>(ta, tb, a, ntiles, s);
+  if (dtype == 0) return launch_mask<TagF16>(ta, tb, a, ntiles, s);
+  return launch_mask<TagBF16>(ta, tb, a, ntiles, s);
 }
 
 }  // namespace dgt
