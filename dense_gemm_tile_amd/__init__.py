@@ -88,6 +88,10 @@ def _load():
 
 
 _lib = _load()
+try:
+    from . import _binding as _fast  # calls of the layer operators that enqueue work
+except ImportError as e:
+    raise ImportError(f"{e}: build the package with `python dense_gemm_tile_amd/build.py`") from e
 
 
 class GemmError(RuntimeError):
@@ -179,9 +183,8 @@ def gemm_linear(M, N, K, dtype, transA, transB, A, lda, B, ldb, bias, act, R, ld
                 out_dtype, Z=None, ldz=0, stream=None):
     """Enqueue Z = op(A)@op(B) + bias, Y = act(Z) + R (bias, R and Z may be None); act is one of
     "none", "relu", "gelu", "gelu_erf", "silu"; raises GemmError on a non-zero status."""
-    _check(_lib.gemm_linear(M, N, K, _dtype(dtype), int(transA), int(transB), _ptr(A), lda,
-                            _ptr(B), ldb, _ptr(bias), _act(act), _ptr(R), ldr, _ptr(Y), ldy,
-                            _dtype(out_dtype), _ptr(Z), ldz, _stream(stream)))
+    _check(_fast.gemm_linear(M, N, K, dtype, transA, transB, A, lda, B, ldb, bias, act, R, ldr, Y,
+                             ldy, out_dtype, Z, ldz, stream))
 
 
 def gemm_linear_validate(M, N, K, dtype, transA, transB, A, lda, B, ldb, bias, act, R, ldr, Y, ldy,
@@ -195,9 +198,8 @@ def gemm_linear_validate(M, N, K, dtype, transA, transB, A, lda, B, ldb, bias, a
 def gemm_grouped(G, M, N, K, dtype, transB, offsets, A, lda, B, ldb, stride_b, bias, act, R, ldr,
                  Y, ldy, out_dtype, Z=None, ldz=0, stream=None):
     """Enqueue gemm_linear() with one B and bias per group of rows offsets[g] .. offsets[g+1]-1."""
-    _check(_lib.gemm_grouped(G, M, N, K, _dtype(dtype), int(transB), _ptr(offsets), _ptr(A), lda,
-                             _ptr(B), ldb, stride_b, _ptr(bias), _act(act), _ptr(R), ldr, _ptr(Y),
-                             ldy, _dtype(out_dtype), _ptr(Z), ldz, _stream(stream)))
+    _check(_fast.gemm_grouped(G, M, N, K, dtype, transB, offsets, A, lda, B, ldb, stride_b, bias,
+                              act, R, ldr, Y, ldy, out_dtype, Z, ldz, stream))
 
 
 def gemm_grouped_validate(G, M, N, K, dtype, transB, offsets, A, lda, B, ldb, stride_b, bias, act,
@@ -211,9 +213,8 @@ def gemm_grouped_validate(G, M, N, K, dtype, transB, offsets, A, lda, B, ldb, st
 def gemm_grouped_grad_weight(G, M, N, K, dtype, offsets, A, lda, B, ldb, D, ldd, stride_d,
                              out_dtype, accumulate=False, stream=None):
     """Enqueue D_g = A_g^T @ B_g (+ D_g when accumulate) over the rows of each group."""
-    _check(_lib.gemm_grouped_grad_weight(G, M, N, K, _dtype(dtype), _ptr(offsets), _ptr(A), lda,
-                                         _ptr(B), ldb, _ptr(D), ldd, stride_d, _dtype(out_dtype),
-                                         int(accumulate), _stream(stream)))
+    _check(_fast.gemm_grouped_grad_weight(G, M, N, K, dtype, offsets, A, lda, B, ldb, D, ldd,
+                                          stride_d, out_dtype, accumulate, stream))
 
 
 def gemm_grouped_grad_weight_validate(G, M, N, K, dtype, offsets, A, lda, B, ldb, D, ldd, stride_d,
@@ -228,47 +229,43 @@ def gemm_act_grad(G, M, N, dtype, act, offsets, dY, lddy, Z, ldz, dZ, lddz, db, 
                   workspace_bytes, stream=None):
     """Enqueue dZ = dY * act'(Z) and db[g] = the sum of dZ over each group's rows (float32).
     offsets None: one group. workspace: gemm_act_grad_workspace(G, M, N) bytes on the device."""
-    _check(_lib.gemm_act_grad(G, M, N, _dtype(dtype), _act(act), _ptr(offsets), _ptr(dY), lddy,
-                              _ptr(Z), ldz, _ptr(dZ), lddz, _ptr(db), _ptr(workspace),
-                              workspace_bytes, _stream(stream)))
+    _check(_fast.gemm_act_grad(G, M, N, dtype, act, offsets, dY, lddy, Z, ldz, dZ, lddz, db,
+                               workspace, workspace_bytes, stream))
 
 
 def gemm_act_grad_workspace(G, M, N) -> int:
     """Bytes of workspace that gemm_act_grad() needs."""
-    return _lib.gemm_act_grad_workspace(G, M, N)
+    return _fast.gemm_act_grad_workspace(G, M, N)
 
 
 def gemm_route(T, top, E, ids, offsets, order, slot, workspace, workspace_bytes, stream=None):
     """Enqueue the stable sort of T x top int32 expert ids: offsets[E + 1], order[T * top] and
     slot[T * top] (int32). workspace: gemm_route_workspace(T, top, E) bytes on the device."""
-    _check(_lib.gemm_route(T, top, E, _ptr(ids), _ptr(offsets), _ptr(order), _ptr(slot),
-                           _ptr(workspace), workspace_bytes, _stream(stream)))
+    _check(_fast.gemm_route(T, top, E, ids, offsets, order, slot, workspace, workspace_bytes,
+                            stream))
 
 
 def gemm_route_workspace(T, top, E) -> int:
     """Bytes of workspace that gemm_route() needs."""
-    return _lib.gemm_route_workspace(T, top, E)
+    return _fast.gemm_route_workspace(T, top, E)
 
 
 def gemm_dispatch(T, top, H, dtype, X, ldx, slot, Xs, ldxs, stream=None):
     """Enqueue Xs[slot[t][j]] = X[t] ("f16", "bf16" or "f32" rows of H values)."""
-    _check(_lib.gemm_dispatch(T, top, H, _dtype(dtype), _ptr(X), ldx, _ptr(slot), _ptr(Xs), ldxs,
-                              _stream(stream)))
+    _check(_fast.gemm_dispatch(T, top, H, dtype, X, ldx, slot, Xs, ldxs, stream))
 
 
 def gemm_combine(T, top, H, dtype, Ys, ldys, slot, weights, R, ldr, Y, ldy, stream=None):
     """Enqueue Y[t] = sum_j weights[t][j] * Ys[slot[t][j]] + R[t] (weights float32 or None for
     ones, R may be None)."""
-    _check(_lib.gemm_combine(T, top, H, _dtype(dtype), _ptr(Ys), ldys, _ptr(slot), _ptr(weights),
-                             _ptr(R), ldr, _ptr(Y), ldy, _stream(stream)))
+    _check(_fast.gemm_combine(T, top, H, dtype, Ys, ldys, slot, weights, R, ldr, Y, ldy, stream))
 
 
 def gemm_combine_grad(T, top, H, dtype, dY, lddy, Ys, ldys, slot, weights, dYs, lddys, dweights,
                       stream=None):
     """Enqueue dYs[slot[t][j]] = weights[t][j] * dY[t] and dweights[t][j] = <dY[t], Ys[slot]>."""
-    _check(_lib.gemm_combine_grad(T, top, H, _dtype(dtype), _ptr(dY), lddy, _ptr(Ys), ldys,
-                                  _ptr(slot), _ptr(weights), _ptr(dYs), lddys, _ptr(dweights),
-                                  _stream(stream)))
+    _check(_fast.gemm_combine_grad(T, top, H, dtype, dY, lddy, Ys, ldys, slot, weights, dYs, lddys,
+                                   dweights, stream))
 
 
 def gemm_last_error() -> str:

@@ -4,8 +4,9 @@ Usage: python dense_gemm_tile_amd/build.py [--incremental]
 (or __graft_entry__.build(), which always compiles everything). It is
 run as a script, not imported through the package, because importing the
 package requires the library this script builds.
-Objects go to _build/ at the repository root; the shared library lands next to
-this file so the Python binding finds it.
+Objects go to _build/ at the repository root; the shared library and the
+extension module that calls it (csrc/binding.cpp) land next to this file so the
+Python binding finds them.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libdense_gemm_tile_amd.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+BINDING_PATH = os.path.join(PKG_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = "gfx950"
 
 
@@ -68,6 +71,20 @@ def _compile(src: str, extra, incremental: bool = False) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """The extension module: host code only, linked to the library beside it."""
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           "-no-hip-rt",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", PKG_DIR, f"-l:{LIB_NAME}",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(verbose: bool = False, jobs: int | None = None, extra_flags=(),
           incremental: bool = False) -> str:
     """Compile every source (or, with incremental, those whose object is older
@@ -85,6 +102,7 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=(),
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _build_binding()
     if verbose:
         print(f"built {LIB_PATH} from {len(srcs)} sources", file=sys.stderr)
     return LIB_PATH

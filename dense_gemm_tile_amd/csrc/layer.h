@@ -316,21 +316,57 @@ __device__ __forceinline__ void layer_store8_32(char* p, bool wide, int nv, cons
   }
 }
 
-// Z, activation, residual and Y of 8 columns of one row, from the sums x.
+// 8 columns of the residual, requested ahead of their use: whole pieces as they
+// are stored, others converted at once.
+struct LayerResidual {
+  f32x4 lo, hi;
+};
+template <class Tag>
+__device__ __forceinline__ LayerResidual layer_request_r(const LayerArgs& p, const LayerTile& q,
+                                                         int r, int c, int nv) {
+  LayerResidual v;
+  const bool wide = (p.vec & VEC_R) && nv == 8;
+  const char* const at = q.R + ((int64_t)r * p.ldr + c) * (p.out32 ? 4 : 2);
+  if (wide) {
+    v.lo = *reinterpret_cast<const f32x4*>(at);
+    if (p.out32) v.hi = *reinterpret_cast<const f32x4*>(at + 16);
+  } else {
+    float f[8];
+    if (p.out32) layer_load8_32(at, false, nv, f);
+    else layer_load8_16<Tag>(at, false, nv, f);
+    v.lo = f32x4{f[0], f[1], f[2], f[3]};
+    v.hi = f32x4{f[4], f[5], f[6], f[7]};
+  }
+  return v;
+}
+template <class Tag>
+__device__ __forceinline__ void layer_add_r(const LayerArgs& p, const LayerResidual& v, int nv,
+                                            float (&x)[8]) {
+  if ((p.vec & VEC_R) && nv == 8 && !p.out32) {
+    float f[8];
+    layer_unpack8<Tag>(__builtin_bit_cast(u32x4, v.lo), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += f[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] += v.lo[e];
+      x[e + 4] += v.hi[e];
+    }
+  }
+}
+
+// Z, activation, residual and Y of 8 columns of one row, from the sums x. res:
+// what layer_request_r gave for them (not used without a residual).
 template <class Tag>
 __device__ __forceinline__ void layer_finish8(const LayerArgs& p, const LayerTile& q, int r, int c,
-                                              int nv, const float (&bias)[8], float (&x)[8]) {
+                                              int nv, const float (&bias)[8],
+                                              const LayerResidual& res, float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] += bias[e];
   if (q.Z) layer_store8_16<Tag>(q.Z + ((int64_t)r * p.ldz + c) * 2, p.vec & VEC_Z, nv, x);
   layer_act8(x, p.act);
-  if (q.R) {
-    float rv[8];
-    if (p.out32) layer_load8_32(q.R + ((int64_t)r * p.ldr + c) * 4, p.vec & VEC_R, nv, rv);
-    else layer_load8_16<Tag>(q.R + ((int64_t)r * p.ldr + c) * 2, p.vec & VEC_R, nv, rv);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += rv[e];
-  }
+  if (q.R) layer_add_r<Tag>(p, res, nv, x);
   if (p.out32) layer_store8_32(q.Y + ((int64_t)r * p.ldy + c) * 4, p.vec & VEC_Y, nv, x);
   else layer_store8_16<Tag>(q.Y + ((int64_t)r * p.ldy + c) * 2, p.vec & VEC_Y, nv, x);
 }
@@ -367,8 +403,21 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
 #pragma unroll
   for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
   if (q.bias && nv > 0) layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
+  // The residual of a row of atoms is requested before its sums go through LDS.
+  // (R may be Y: every element is read before the same lane writes it.)
+  constexpr int PASSES = At::M / RPP;
+  LayerResidual res[PASSES];
+  auto request = [&](int i) {
+    if (!q.R || nv <= 0) return;
+#pragma unroll
+    for (int s = 0; s < PASSES; ++s) {
+      const int r = r0 + i * At::M + s * RPP + rl;
+      if (r < q.M) res[s] = layer_request_r<Tag>(p, q, r, c, nv);
+    }
+  };
 #pragma unroll
   for (int i = 0; i < C::TM; ++i) {
+    request(i);
 #pragma unroll
     for (int j = 0; j < C::TN; ++j)
 #pragma unroll
@@ -376,12 +425,12 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
         lds[At::acc_row(lane, v) * P + j * At::N + At::acc_col(lane)] = acc[i][j][v];
     layer_wave_order();
 #pragma unroll
-    for (int s = 0; s < At::M / RPP; ++s) {
+    for (int s = 0; s < PASSES; ++s) {
       const int rr = s * RPP + rl, r = r0 + i * At::M + rr;
       const f32x4 lo = *reinterpret_cast<const f32x4*>(lds + rr * P + cl);
       const f32x4 hi = *reinterpret_cast<const f32x4*>(lds + rr * P + cl + 4);
       float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      if (r < q.M && nv > 0) layer_finish8<Tag>(p, q, r, c, nv, bias, x);
+      if (r < q.M && nv > 0) layer_finish8<Tag>(p, q, r, c, nv, bias, res[s], x);
     }
     layer_wave_order();
   }

@@ -173,31 +173,55 @@ bool kernel_runs(const LayerPlan& pl, int k) {
   return pl.tb || k != LK_SKINNY16N16;  // 16 columns of B stored [K][N] are half a line
 }
 
+// By rows, the groups' sizes are only known on average. Measured on weights of
+// 2048 x 2048, 64 groups, us by average rows a group:
+//            2    8    16   32   64   128  (1024)
+//   s16x32   81  110  156  247
+//   s64x64  100  118  121  133  166  257
+//   pp128   109  127  129  131  164  163   742
+//   pp256   122  137  139  141  149  207   551
+int choose_grouped(const LayerPlan& pl) {
+  const LayerArgs& a = pl.a;
+  const int64_t used = a.G < a.M ? a.G : a.M, rows = (a.M + a.G - 1) / a.G;
+  // Tiles to expect: whole ones, and one cut short for every other group.
+  auto tiles = [&](int k) {
+    const LayerKernelInfo& i = kLayerKernels[k];
+    const int64_t m = a.M / i.bm + (used + 1) / 2;
+    return (m > used ? m : used) * ((a.N + i.bn - 1) / i.bn);
+  };
+  if (rows >= 256 && tiles(LK_PP256) >= 256) return LK_PP256;
+  if (rows <= 48 || tiles(LK_SKINNY64N64) <= 512) {
+    if (rows <= 32 && tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
+    return rows <= 8 ? LK_SKINNY16 : LK_SKINNY64N64;
+  }
+  return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
+}
+
 int choose_kernel(const LayerPlan& pl) {
   const LayerArgs& a = pl.a;
   auto tiles = [&](int k) { return count_tiles(a, kLayerKernels[k]); };
   if (!kernel_runs(pl, LK_PP256))
     // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
     return tiles(LK_GENERAL128) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
-  const int64_t rows = a.mode == LAYER_ROWS ? (a.M + a.G - 1) / a.G : a.M;
+  if (a.mode == LAYER_ROWS) return choose_grouped(pl);
   const bool split = kernel_runs(pl, LK_SKINNY64N64);
-  // Few rows: the weights' bytes count, and a wave's loads in flight. Groups'
-  // sizes are only known on average, and a group that needs a second row tile
-  // reads its weights twice.
-  if (split && rows <= (a.mode == LAYER_ROWS ? 8 : 64)) {
-    if (rows <= 16) {
-      if (a.mode == LAYER_ROWS || !pl.tb) return LK_SKINNY16;
-      return a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY32;
-    }
-    return rows <= 32 ? LK_SKINNY32 : rows <= 48 ? LK_SKINNY48 : LK_SKINNY64;
+  // Few rows: the weights' bytes count.
+  if (split && a.M <= 64) {
+    // (16 columns of B stored [K][N] would be a quarter of a line.)
+    if (a.M <= 16) return !pl.tb ? LK_SKINNY16 : a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY32;
+    return a.M <= 32 ? LK_SKINNY32 : a.M <= 48 ? LK_SKINNY48 : LK_SKINNY64;
   }
   const int64_t n256 = tiles(LK_PP256);
   if (n256 >= 256 || (n256 >= 192 && a.K >= 1024) || (n256 >= 128 && a.K >= 2048)) return LK_PP256;
-  // One round of small tiles with the sum split over waves: the smallest that
-  // fits the CUs.
-  if (split && a.mode == LAYER_DENSE)
-    for (int k : {LK_SKINNY32, LK_SKINNY64, LK_SKINNY64N64})
+  // Small grids: tiles with the sum split over waves, the smallest that fit the
+  // CUs in one round, or two rounds of 64 x 64 ones (512x4096x4096 41 us against
+  // 52 on 128 x 128 tiles, 1024x2048x2048 26 against 30; four rounds, 2048^3, 49
+  // against 32).
+  if (split) {
+    for (int k : {LK_SKINNY32, LK_SKINNY64})
       if (tiles(k) <= 256) return k;
+    if (tiles(LK_SKINNY64N64) <= 512) return LK_SKINNY64N64;
+  }
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
