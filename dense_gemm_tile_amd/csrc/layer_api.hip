@@ -179,20 +179,28 @@ bool kernel_runs(const LayerPlan& pl, int k) {
 //   s16x32   81  110  156  247
 //   s64x64  100  118  121  133  166  257
 //   pp128   109  127  129  131  164  163   742
-//   pp256   122  137  139  141  149  207   551
+//   pp256   122  137  139  141  149  207   515
+// and with B stored [K][N], where pieces of 32 or 64 columns cost the small tiles
+// as much as whole lines: s16x32 119 at 2 rows, pp128 89.
 int choose_grouped(const LayerPlan& pl) {
   const LayerArgs& a = pl.a;
   const int64_t used = a.G < a.M ? a.G : a.M, rows = (a.M + a.G - 1) / a.G;
   // Tiles to expect: whole ones, and one cut short for every other group.
   auto tiles = [&](int k) {
     const LayerKernelInfo& i = kLayerKernels[k];
-    const int64_t m = a.M / i.bm + (used + 1) / 2;
-    return (m > used ? m : used) * ((a.N + i.bn - 1) / i.bn);
+    int64_t m = a.M / i.bm + (used + 1) / 2;
+    m = (m > used ? m : used) + used / 20;
+    return m * ((a.N + i.bn - 1) / i.bn);
   };
-  if (rows >= 256 && tiles(LK_PP256) >= 256) return LK_PP256;
-  if (rows <= 48 || tiles(LK_SKINNY64N64) <= 512) {
+  // One wave of workgroups takes 1.4 times as long on 256 x 256 tiles (one to a
+  // CU) as on 128 x 128 ones (two to a CU).
+  const int64_t rounds256 = (tiles(LK_PP256) + 255) / 256, rounds128 = (tiles(LK_PP128) + 511) / 512;
+  if (rows >= 96 && tiles(LK_PP256) >= 192 && 14 * rounds256 < 10 * rounds128 + 4) return LK_PP256;
+  if (pl.tb) {
     if (rows <= 32 && tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
-    return rows <= 8 ? LK_SKINNY16 : LK_SKINNY64N64;
+    if (tiles(LK_SKINNY64N64) <= 512) return LK_SKINNY64N64;
+    // (A K that leaves a wave less than two slices is too short to split.)
+    if (a.K >= 1024 && rows <= 48) return rows <= 8 ? LK_SKINNY16 : LK_SKINNY64N64;
   }
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
@@ -776,6 +784,7 @@ int gemm_combine(int64_t T, int64_t top, int64_t H, int dtype, const void* Ys, i
     a.H = (int)H;
     const Mat* mats[] = {&mi, &mr, &my};
     a.piece = common_piece(H, elem, mats);
+    a.once = n * H * elem >= (int64_t{128} << 20);
     if (combine_waves(a) > 0x7ffffff0)
       return fail(GEMM_ERR_UNSUPPORTED, "too many pieces of rows for one launch");
     set_path("combine in pieces of " + std::to_string(a.piece * elem) + " bytes");

@@ -74,10 +74,16 @@ struct CombineArgs {
   int64_t ldys, ldr, ldy;  // elements
   int T, top, H;
   int piece;  // elements per access
+  int once;   // the rows read fill half of the last cache (256 MiB) or more
 };
+// Pieces a lane: two once that leaves 16 waves to a CU.
+inline int combine_span(const CombineArgs& a) {
+  return a.once || (int64_t)a.T * a.H >= (int64_t)2 * 64 * a.piece * 16 * 256 ? 2 : 1;
+}
 // Waves that a call's rows are cut into.
 inline int64_t combine_waves(const CombineArgs& a) {
-  return a.T * (((int64_t)a.H + 64 * a.piece - 1) / (64 * a.piece));
+  const int64_t span = (int64_t)combine_span(a) * 64 * a.piece;
+  return a.T * ((a.H + span - 1) / span);
 }
 hipError_t launch_combine(int rowtype, const CombineArgs& a, hipStream_t s);
 

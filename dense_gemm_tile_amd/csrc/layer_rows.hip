@@ -176,67 +176,83 @@ __global__ void __launch_bounds__(256) layer_dispatch_kernel(const DispatchArgs 
 // ------------------------------------------------------------------ combine --
 // Elements of rows: loads and stores of E consecutive ones, as float32.
 struct RowF32 {};
+// ONCE: with the hint not to keep the bytes in the caches.
 template <class Row, int E>
 struct RowIo {  // 16-bit types
+  using V = typename RowPiece<2 * E>::type;
+  template <bool ONCE = false>
   __device__ static __forceinline__ void load(const void* base, int64_t at, float (&f)[E]) {
-    using V = typename RowPiece<2 * E>::type;
-    const V v = *reinterpret_cast<const V*>(static_cast<const unsigned short*>(base) + at);
+    const V* p = reinterpret_cast<const V*>(static_cast<const unsigned short*>(base) + at);
+    const V v = ONCE ? __builtin_nontemporal_load(p) : *p;
     const unsigned short* s = reinterpret_cast<const unsigned short*>(&v);
 #pragma unroll
     for (int e = 0; e < E; ++e) f[e] = layer_f32(Row{}, s[e]);
   }
+  template <bool ONCE = false>
   __device__ static __forceinline__ void store(void* base, int64_t at, const float (&f)[E]) {
-    using V = typename RowPiece<2 * E>::type;
     V v;
     unsigned short* s = reinterpret_cast<unsigned short*>(&v);
 #pragma unroll
     for (int e = 0; e < E; ++e) s[e] = layer_16(Row{}, f[e]);
-    *reinterpret_cast<V*>(static_cast<unsigned short*>(base) + at) = v;
+    V* p = reinterpret_cast<V*>(static_cast<unsigned short*>(base) + at);
+    if constexpr (ONCE) __builtin_nontemporal_store(v, p);
+    else *p = v;
   }
 };
 template <int E>
 struct RowIo<RowF32, E> {
+  using V = typename RowPiece<4 * E>::type;
+  template <bool ONCE = false>
   __device__ static __forceinline__ void load(const void* base, int64_t at, float (&f)[E]) {
-    using V = typename RowPiece<4 * E>::type;
-    const V v = *reinterpret_cast<const V*>(static_cast<const float*>(base) + at);
+    const V* p = reinterpret_cast<const V*>(static_cast<const float*>(base) + at);
+    const V v = ONCE ? __builtin_nontemporal_load(p) : *p;
     __builtin_memcpy(f, &v, 4 * E);
   }
+  template <bool ONCE = false>
   __device__ static __forceinline__ void store(void* base, int64_t at, const float (&f)[E]) {
-    using V = typename RowPiece<4 * E>::type;
     V v;
     __builtin_memcpy(&v, f, 4 * E);
-    *reinterpret_cast<V*>(static_cast<float*>(base) + at) = v;
+    V* p = reinterpret_cast<V*>(static_cast<float*>(base) + at);
+    if constexpr (ONCE) __builtin_nontemporal_store(v, p);
+    else *p = v;
   }
 };
 
-// A wave takes E columns a lane of one token, and neighbouring waves the
-// token's other columns, so that whole rows are read at about the same time
-// (one 1 KiB piece of every token first: MEASURE). Four of the
-// token's rows are in flight at a time, added in the order of its choices.
-template <class Row, int E>
+// A wave takes SPAN pieces of E columns a lane of one token, and neighbouring
+// waves the token's other columns, so that whole rows are read at about the same
+// time. Four of the token's rows are in flight at a time, added in the order of
+// its choices. ONCE: calls that move more than the caches hold ask them not to
+// keep anything (16384 tokens of 4 rows of 4096: 158 us without, 127 for the
+// rows that are read alone, 111 for all).
+template <class Row, int E, int SPAN, bool ONCE>
 __global__ void __launch_bounds__(256) layer_combine_kernel(const CombineArgs p) {
   using Io = RowIo<Row, E>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int wid = blockIdx.x * 4 + w;
-  const int across = (p.H + 64 * E - 1) / (64 * E);
-  const int t = wid / across;
-  const int64_t c = ((int64_t)(wid - t * across) * 64 + lane) * E;
-  if (t >= p.T || c >= p.H) return;
+  const int across = (p.H + SPAN * 64 * E - 1) / (SPAN * 64 * E);
+  const int t = __builtin_amdgcn_readfirstlane(wid / across);
+  if (t >= p.T) return;
+  const int c0 = ((wid - t * across) * SPAN * 64 + lane) * E;  // piece s: c0 + s * 64 * E
   const int rows = p.T * p.top;
   const int64_t t0 = (int64_t)t * p.top;
-  float sum[E];
+  float sum[SPAN][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+  for (int s = 0; s < SPAN; ++s)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[s][e] = 0.0f;
   for (int j0 = 0; j0 < p.top; j0 += 4) {
-    float f[4][E], wt[4];
-    bool in[4];
+    float f[4][SPAN][E], wt[4];
+    bool in[4];  // uniform
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = j0 + u;
       const int at = j < p.top ? p.slot[t0 + j] : -1;
       in[u] = (unsigned)at < (unsigned)rows;
       if (in[u]) {
-        Io::load(p.Ys, (int64_t)at * p.ldys + c, f[u]);
+#pragma unroll
+        for (int s = 0; s < SPAN; ++s)
+          if (c0 + s * 64 * E < p.H)
+            Io::template load<ONCE>(p.Ys, (int64_t)at * p.ldys + c0 + s * 64 * E, f[u][s]);
         wt[u] = p.weights ? p.weights[t0 + j] : 1.0f;
       }
     }
@@ -244,16 +260,23 @@ __global__ void __launch_bounds__(256) layer_combine_kernel(const CombineArgs p)
     for (int u = 0; u < 4; ++u)
       if (in[u]) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] = __builtin_fmaf(wt[u], f[u][e], sum[e]);
+        for (int s = 0; s < SPAN; ++s)
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[s][e] = __builtin_fmaf(wt[u], f[u][s][e], sum[s][e]);
       }
   }
-  if (p.R) {
-    float r[E];
-    Io::load(p.R, (int64_t)t * p.ldr + c, r);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] += r[e];
+  for (int s = 0; s < SPAN; ++s) {
+    const int64_t c = c0 + s * 64 * E;
+    if (c >= p.H) continue;
+    if (p.R) {
+      float r[E];
+      Io::template load<ONCE>(p.R, (int64_t)t * p.ldr + c, r);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[s][e] += r[e];
+    }
+    Io::template store<ONCE>(p.Y, (int64_t)t * p.ldy + c, sum[s]);
   }
-  Io::store(p.Y, (int64_t)t * p.ldy + c, sum);
 }
 
 // A workgroup takes one token; its threads share the columns, and their
@@ -279,11 +302,11 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
     }
     for (int64_t c = (int64_t)tid * E; c < p.H; c += 256 * E) {
       float d[E], y[4][E];
-      Io::load(p.dY, (int64_t)t * p.lddy + c, d);
+      Io::template load<true>(p.dY, (int64_t)t * p.lddy + c, d);
       if (p.dw) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (at[u] >= 0) Io::load(p.Ys, (int64_t)at[u] * p.ldys + c, y[u]);
+          if (at[u] >= 0) Io::template load<true>(p.Ys, (int64_t)at[u] * p.ldys + c, y[u]);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -317,8 +340,10 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
 
 template <class Row, int E>
 hipError_t combine(const CombineArgs& a, hipStream_t s) {
-  return launch_kernel(layer_combine_kernel<Row, E>, dim3((unsigned)((combine_waves(a) + 3) / 4)),
-                       dim3(256), s, a);
+  const dim3 grid((unsigned)((combine_waves(a) + 3) / 4)), block(256);
+  if (a.once) return launch_kernel(layer_combine_kernel<Row, E, 2, true>, grid, block, s, a);
+  if (combine_span(a) == 2) return launch_kernel(layer_combine_kernel<Row, E, 2, false>, grid, block, s, a);
+  return launch_kernel(layer_combine_kernel<Row, E, 1, false>, grid, block, s, a);
 }
 template <class Row, int E>
 hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
