@@ -29,12 +29,13 @@ struct LayerArgs {
   int M, N, K;       // by rows: M counts all rows; by sum: K does
   int G, mode, act;
   int out32;         // Y (and R) hold float32, else the operands' 16-bit type
-  int vec;           // bits 0-3: bias, R, Y, Z allow 16-byte accesses of 8 columns
+  int vec;           // LayerVec: what allows 16-byte accesses of 8 columns
   int a_vw, b_vw;    // staging vector widths of A and B (general kernel)
   int tiles_m, tiles_n;  // of one group (by sum, dense); by rows: tiles_m is not used
   int group_m;
 };
-enum LayerVec : int { VEC_BIAS = 1, VEC_R = 2, VEC_Y = 4, VEC_Z = 8 };
+// VEC_ALL: everything that the call has, and N is a multiple of 8.
+enum LayerVec : int { VEC_BIAS = 1, VEC_R = 2, VEC_Y = 4, VEC_Z = 8, VEC_ALL = 16 };
 
 // One group's product and one tile of it. Pointers and sizes are uniform.
 struct LayerTile {
@@ -316,71 +317,50 @@ __device__ __forceinline__ void layer_store8_32(char* p, bool wide, int nv, cons
   }
 }
 
-// 8 columns of the residual, requested ahead of their use: whole pieces as they
-// are stored, others converted at once.
-struct LayerResidual {
-  f32x4 lo, hi;
-};
-template <class Tag>
-__device__ __forceinline__ LayerResidual layer_request_r(const LayerArgs& p, const LayerTile& q,
-                                                         int r, int c, int nv) {
-  LayerResidual v;
-  const bool wide = (p.vec & VEC_R) && nv == 8;
-  const char* const at = q.R + ((int64_t)r * p.ldr + c) * (p.out32 ? 4 : 2);
-  if (wide) {
-    v.lo = *reinterpret_cast<const f32x4*>(at);
-    if (p.out32) v.hi = *reinterpret_cast<const f32x4*>(at + 16);
-  } else {
-    float f[8];
-    if (p.out32) layer_load8_32(at, false, nv, f);
-    else layer_load8_16<Tag>(at, false, nv, f);
-    v.lo = f32x4{f[0], f[1], f[2], f[3]};
-    v.hi = f32x4{f[4], f[5], f[6], f[7]};
-  }
-  return v;
-}
-template <class Tag>
-__device__ __forceinline__ void layer_add_r(const LayerArgs& p, const LayerResidual& v, int nv,
-                                            float (&x)[8]) {
-  if ((p.vec & VEC_R) && nv == 8 && !p.out32) {
-    float f[8];
-    layer_unpack8<Tag>(__builtin_bit_cast(u32x4, v.lo), f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += f[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] += v.lo[e];
-      x[e + 4] += v.hi[e];
-    }
-  }
-}
-
-// Z, activation, residual and Y of 8 columns of one row, from the sums x. res:
-// what layer_request_r gave for them (not used without a residual).
+// Z, activation, residual and Y of 8 columns of one row, from the sums x.
 template <class Tag>
 __device__ __forceinline__ void layer_finish8(const LayerArgs& p, const LayerTile& q, int r, int c,
-                                              int nv, const float (&bias)[8],
-                                              const LayerResidual& res, float (&x)[8]) {
+                                              int nv, const float (&bias)[8], float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] += bias[e];
   if (q.Z) layer_store8_16<Tag>(q.Z + ((int64_t)r * p.ldz + c) * 2, p.vec & VEC_Z, nv, x);
   layer_act8(x, p.act);
-  if (q.R) layer_add_r<Tag>(p, res, nv, x);
+  if (q.R) {
+    float rv[8];
+    if (p.out32) layer_load8_32(q.R + ((int64_t)r * p.ldr + c) * 4, p.vec & VEC_R, nv, rv);
+    else layer_load8_16<Tag>(q.R + ((int64_t)r * p.ldr + c) * 2, p.vec & VEC_R, nv, rv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += rv[e];
+  }
   if (p.out32) layer_store8_32(q.Y + ((int64_t)r * p.ldy + c) * 4, p.vec & VEC_Y, nv, x);
   else layer_store8_16<Tag>(q.Y + ((int64_t)r * p.ldy + c) * 2, p.vec & VEC_Y, nv, x);
 }
 
 // The epilogue of one wave's TM x TN atoms, whose first output is (r0, c0).
 // The accumulators of a 16- or 32-wide atom hold 4 rows of one column per
-// lane; a row of atoms goes through LDS so that each lane gets 8 consecutive
-// columns of one row, and a wave's stores of 16-bit outputs are 16 bytes a
-// lane, whole 128-byte lines where the wave is 64 columns wide. lds: this
+// lane; batches of up to 64 rows go through LDS so that each lane gets 8
+// consecutive columns of one row, and a wave's stores of 16-bit outputs are 16
+// bytes a lane, whole 128-byte lines where the wave is 64 columns wide. lds: this
 // wave's own layer_lds_bytes<C>(); no other wave touches it.
+//
+// The rows of a batch are finished in a loop that is not unrolled past four
+// passes: with all of it unrolled, the epilogue outgrew the instruction cache
+// (32768x4096x2048 on 256x256 tiles, us: MEASURE).
 template <class C>
-constexpr int layer_pitch() { return C::TN * C::At::N + 4; }  // floats; 4 apart in banks per row
+struct LayerEpi {
+  using At = typename C::At;
+  static constexpr int W = C::TN * At::N, P = W + 4;  // columns; pitch in floats, 4 apart in banks
+  static constexpr int ROWS = C::TM * At::M;
+  static constexpr int BATCH = ROWS < 64 ? ROWS : 64;     // rows
+  static constexpr int LPR = W / 8, RPP = 64 / LPR;       // lanes a row, rows a pass
+  static constexpr int PASSES = BATCH / RPP;
+  static constexpr int GROUP = PASSES < 4 ? PASSES : 4;   // passes unrolled
+  static_assert(W % 8 == 0 && 64 % LPR == 0 && BATCH % RPP == 0 && PASSES % GROUP == 0 &&
+                    ROWS % BATCH == 0 && BATCH % At::M == 0,
+                "whole passes");
+};
 template <class C>
-constexpr int layer_lds_bytes() { return C::At::M * layer_pitch<C>() * 4; }
+constexpr int layer_lds_bytes() { return LayerEpi<C>::BATCH * LayerEpi<C>::P * 4; }
 
 // LDS written by some lanes of a wave is read by others: LDS operations of one
 // wave complete in order, so only the compiler has to keep theirs.
@@ -389,48 +369,120 @@ __device__ __forceinline__ void layer_wave_order() {
   asm volatile("" ::: "memory");
 }
 
+// The residual of one group of passes, as it is stored (16-bit: lo alone).
+template <int GROUP>
+struct LayerGroupR {
+  u32x4 lo[GROUP], hi[GROUP];
+};
+// Requests it for the passes whose first row is r (RPP rows a pass).
+template <int GROUP, int RPP>
+__device__ __forceinline__ void layer_group_r(LayerGroupR<GROUP>& v, const LayerArgs& p,
+                                              const LayerTile& q, int r, int c) {
+  if (!q.R || c >= q.N) return;
+#pragma unroll
+  for (int s = 0; s < GROUP; ++s) {
+    const int row = r + s * RPP;
+    if (row >= q.M) continue;
+    const char* const at = q.R + ((int64_t)row * p.ldr + c) * (p.out32 ? 4 : 2);
+    v.lo[s] = *reinterpret_cast<const u32x4*>(at);
+    if (p.out32) v.hi[s] = *reinterpret_cast<const u32x4*>(at + 16);
+  }
+}
+// The passes of a batch whose first row is r, all of its columns in whole
+// 16-byte pieces: lds is this lane's first piece, c its first column. The
+// residual is requested a group of passes ahead. (R may be Y: a lane reads each
+// of its pieces before it writes it.)
+template <class E, class Tag, int ACT>
+__device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile& q, int r, int c,
+                                             const float* lds, const float (&bias)[8],
+                                             LayerGroupR<E::GROUP>& res) {
+#pragma unroll 1
+  for (int g = 0; g < E::PASSES; g += E::GROUP) {
+    LayerGroupR<E::GROUP> next;
+    if (g + E::GROUP < E::PASSES)
+      layer_group_r<E::GROUP, E::RPP>(next, p, q, r + (g + E::GROUP) * E::RPP, c);
+#pragma unroll
+    for (int s = 0; s < E::GROUP; ++s) {
+      const int row = r + (g + s) * E::RPP;
+      const float* const from = lds + (g + s) * E::RPP * E::P;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(from);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(from + 4);
+      float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += bias[e];
+      if (row < q.M && c < q.N) {
+        if (q.Z)
+          *reinterpret_cast<u32x4*>(q.Z + ((int64_t)row * p.ldz + c) * 2) = layer_pack8<Tag>(x);
+        layer_act8_of<ACT>(x);
+        if (q.R) {
+          float f[8];
+          if (p.out32) {
+            const f32x4 a = __builtin_bit_cast(f32x4, res.lo[s]), b = __builtin_bit_cast(f32x4, res.hi[s]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = a[e], f[e + 4] = b[e];
+          } else {
+            layer_unpack8<Tag>(res.lo[s], f);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += f[e];
+        }
+        if (p.out32) layer_store8_32(q.Y + ((int64_t)row * p.ldy + c) * 4, true, 8, x);
+        else *reinterpret_cast<u32x4*>(q.Y + ((int64_t)row * p.ldy + c) * 2) = layer_pack8<Tag>(x);
+      }
+    }
+    res = next;
+  }
+}
+
 template <class C, class Tag>
 __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][C::TN],
                                             const LayerArgs& p, const LayerTile& q, int r0, int c0,
                                             int lane, float* lds) {
   using At = typename C::At;
-  constexpr int W = C::TN * At::N, P = layer_pitch<C>();
-  constexpr int LPR = W / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
-  static_assert(W % 8 == 0 && 64 % LPR == 0 && At::M % RPP == 0, "whole passes");
-  const int cl = 8 * (lane % LPR), rl = lane / LPR;
+  using E = LayerEpi<C>;
+  constexpr int P = E::P, AR = E::BATCH / At::M;  // atom rows of a batch
+  const int cl = 8 * (lane % E::LPR), rl = lane / E::LPR;
   const int c = c0 + cl, nv = q.N - c >= 8 ? 8 : q.N - c;
   float bias[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
-  if (q.bias && nv > 0) layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
-  // The residual of a row of atoms is requested before its sums go through LDS.
-  // (R may be Y: every element is read before the same lane writes it.)
-  constexpr int PASSES = At::M / RPP;
-  LayerResidual res[PASSES];
-  auto request = [&](int i) {
-    if (!q.R || nv <= 0) return;
+  if (q.bias && nv > 0) {
+    if (p.vec & VEC_ALL) layer_unpack8<Tag>(*reinterpret_cast<const u32x4*>(q.bias + (int64_t)c * 2), bias);
+    else layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
+  }
 #pragma unroll
-    for (int s = 0; s < PASSES; ++s) {
-      const int r = r0 + i * At::M + s * RPP + rl;
-      if (r < q.M) res[s] = layer_request_r<Tag>(p, q, r, c, nv);
-    }
-  };
+  for (int b = 0; b < C::TM / AR; ++b) {
+    const int r = r0 + b * E::BATCH;  // (uniform) the batch's first row
+    if (r >= q.M) break;
+    LayerGroupR<E::GROUP> res;
+    if (p.vec & VEC_ALL) layer_group_r<E::GROUP, E::RPP>(res, p, q, r + rl, c);
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
-    request(i);
+    for (int i = 0; i < AR; ++i)
 #pragma unroll
-    for (int j = 0; j < C::TN; ++j)
+      for (int j = 0; j < C::TN; ++j)
 #pragma unroll
-      for (int v = 0; v < At::NACC; ++v)
-        lds[At::acc_row(lane, v) * P + j * At::N + At::acc_col(lane)] = acc[i][j][v];
+        for (int v = 0; v < At::NACC; ++v)
+          lds[(i * At::M + At::acc_row(lane, v)) * P + j * At::N + At::acc_col(lane)] =
+              acc[b * AR + i][j][v];
     layer_wave_order();
+    const float* const from = lds + rl * P + cl;
+    if (p.vec & VEC_ALL) {
+      switch (p.act) {
+        case ACT_RELU: layer_passes<E, Tag, ACT_RELU>(p, q, r + rl, c, from, bias, res); break;
+        case ACT_GELU: layer_passes<E, Tag, ACT_GELU>(p, q, r + rl, c, from, bias, res); break;
+        case ACT_GELU_ERF: layer_passes<E, Tag, ACT_GELU_ERF>(p, q, r + rl, c, from, bias, res); break;
+        case ACT_SILU: layer_passes<E, Tag, ACT_SILU>(p, q, r + rl, c, from, bias, res); break;
+        default: layer_passes<E, Tag, ACT_NONE>(p, q, r + rl, c, from, bias, res); break;
+      }
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < E::PASSES; ++s) {
+        const int row = r + s * E::RPP + rl;
+        float x[8];
 #pragma unroll
-    for (int s = 0; s < PASSES; ++s) {
-      const int rr = s * RPP + rl, r = r0 + i * At::M + rr;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(lds + rr * P + cl);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(lds + rr * P + cl + 4);
-      float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      if (r < q.M && nv > 0) layer_finish8<Tag>(p, q, r, c, nv, bias, res[s], x);
+        for (int e = 0; e < 8; ++e) x[e] = from[s * E::RPP * P + e];
+        if (row < q.M && nv > 0) layer_finish8<Tag>(p, q, row, c, nv, bias, x);
+      }
     }
     layer_wave_order();
   }

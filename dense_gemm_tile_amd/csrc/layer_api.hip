@@ -254,6 +254,8 @@ int plan_tiles(LayerPlan& pl, const char* op) {
   a.group_m = 8;
   pl.ntiles = (int)n;
   static const char* const ops[4] = {"NN", "NT", "TN", "TT"};
+  const int need = (a.bias ? VEC_BIAS : 0) | (a.R ? VEC_R : 0) | VEC_Y | (a.Z ? VEC_Z : 0);
+  if ((a.vec & need) == need && a.N % 8 == 0) a.vec |= VEC_ALL;
   g_layer_path = {op, ops[pl.ta * 2 + pl.tb], pl.kernel, a.act, a.bias != nullptr,
                   a.R != nullptr, a.Z != nullptr, a.out32 != 0};
   set_path_writer(write_layer_path);

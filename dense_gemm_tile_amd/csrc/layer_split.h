@@ -80,10 +80,8 @@ struct SplitSum {
           bias[e] = 0.0f;
           v[e] = outs[rr * PITCH + cl + e];
         }
-        LayerResidual res;
-        if (q.R) res = layer_request_r<Tag>(p, q, r, c, nv);
         if (q.bias) layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
-        layer_finish8<Tag>(p, q, r, c, nv, bias, res, v);
+        layer_finish8<Tag>(p, q, r, c, nv, bias, v);
       }
     }
   }
