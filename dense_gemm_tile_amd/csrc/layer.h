@@ -206,21 +206,32 @@ __device__ __forceinline__ void layer_unpack8(u32x4 v, float (&f)[8]) {
     f[2 * d + 1] = layer_f32(Tag{}, (unsigned short)(v[d] >> 16));
   }
 }
+// Two at a time: one instruction for bf16.
+typedef float layer_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 layer_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 layer_f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ unsigned layer_pack2(TagF16, float lo, float hi) {
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(layer_f32x2{lo, hi}, layer_f16x2));
+}
+__device__ __forceinline__ unsigned layer_pack2(TagBF16, float lo, float hi) {
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(layer_f32x2{lo, hi}, layer_bf16x2));
+}
 template <class Tag>
 __device__ __forceinline__ u32x4 layer_pack8(const float (&f)[8]) {
   u32x4 v;
 #pragma unroll
-  for (int d = 0; d < 4; ++d)
-    v[d] = (unsigned)layer_16(Tag{}, f[2 * d]) | ((unsigned)layer_16(Tag{}, f[2 * d + 1]) << 16);
+  for (int d = 0; d < 4; ++d) v[d] = layer_pack2(Tag{}, f[2 * d], f[2 * d + 1]);
   return v;
 }
 
 // --------------------------------------------------------------- activations --
-// 1 / (1 + exp(-v)): exp overflows to infinity and the reciprocal of that is
-// 0, so both ends come out right without a branch.
-__device__ __forceinline__ float layer_sigmoid(float v) {
-  return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+// 1 / (1 + 2^u), the logistic function of -u ln 2: 2^u overflows to infinity and
+// the reciprocal of that is 0, so both ends come out right without a branch.
+__device__ __forceinline__ float layer_logistic2(float u) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u));
 }
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float layer_sigmoid(float v) { return layer_logistic2(-kLog2e * v); }
 constexpr float kGeluA = 1.5957691216057308f;       // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
@@ -229,7 +240,10 @@ constexpr float kGeluB = 0.044715f;
 template <int ACT>
 __device__ __forceinline__ float layer_act(float z) {
   if constexpr (ACT == ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
-  if constexpr (ACT == ACT_GELU) return z * layer_sigmoid(kGeluA * (z + kGeluB * z * z * z));
+  if constexpr (ACT == ACT_GELU) {
+    const float w = __builtin_fmaf(z * z, -kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA);
+    return z * layer_logistic2(z * w);
+  }
   if constexpr (ACT == ACT_GELU_ERF) return 0.5f * z * erfcf(-0.70710678118654752f * z);
   if constexpr (ACT == ACT_SILU) return z * layer_sigmoid(z);
   return z;
@@ -379,11 +393,12 @@ template <int GROUP, int RPP>
 __device__ __forceinline__ void layer_group_r(LayerGroupR<GROUP>& v, const LayerArgs& p,
                                               const LayerTile& q, int r, int c) {
   if (!q.R || c >= q.N) return;
+  const int osz = p.out32 ? 4 : 2;
+  const int64_t step = RPP * p.ldr * osz;
+  const char* at = q.R + ((int64_t)r * p.ldr + c) * osz;
 #pragma unroll
-  for (int s = 0; s < GROUP; ++s) {
-    const int row = r + s * RPP;
-    if (row >= q.M) continue;
-    const char* const at = q.R + ((int64_t)row * p.ldr + c) * (p.out32 ? 4 : 2);
+  for (int s = 0; s < GROUP; ++s, at += step) {
+    if (r + s * RPP >= q.M) continue;
     v.lo[s] = *reinterpret_cast<const u32x4*>(at);
     if (p.out32) v.hi[s] = *reinterpret_cast<const u32x4*>(at + 16);
   }
@@ -396,6 +411,10 @@ template <class E, class Tag, int ACT>
 __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile& q, int r, int c,
                                              const float* lds, const float (&bias)[8],
                                              LayerGroupR<E::GROUP>& res) {
+  const int osz = p.out32 ? 4 : 2;
+  const int64_t ystep = E::RPP * p.ldy * osz, zstep = E::RPP * p.ldz * 2;
+  char* y = q.Y + ((int64_t)r * p.ldy + c) * osz;
+  char* z = q.Z + ((int64_t)r * p.ldz + c) * 2;
 #pragma unroll 1
   for (int g = 0; g < E::PASSES; g += E::GROUP) {
     LayerGroupR<E::GROUP> next;
@@ -411,8 +430,7 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] += bias[e];
       if (row < q.M && c < q.N) {
-        if (q.Z)
-          *reinterpret_cast<u32x4*>(q.Z + ((int64_t)row * p.ldz + c) * 2) = layer_pack8<Tag>(x);
+        if (q.Z) *reinterpret_cast<u32x4*>(z) = layer_pack8<Tag>(x);
         layer_act8_of<ACT>(x);
         if (q.R) {
           float f[8];
@@ -426,9 +444,11 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] += f[e];
         }
-        if (p.out32) layer_store8_32(q.Y + ((int64_t)row * p.ldy + c) * 4, true, 8, x);
-        else *reinterpret_cast<u32x4*>(q.Y + ((int64_t)row * p.ldy + c) * 2) = layer_pack8<Tag>(x);
+        if (p.out32) layer_store8_32(y, true, 8, x);
+        else *reinterpret_cast<u32x4*>(y) = layer_pack8<Tag>(x);
       }
+      y += ystep;
+      z += zstep;
     }
     res = next;
   }
