@@ -540,9 +540,10 @@ hipError_t launch_layer_pp256(int dtype, bool ta, bool tb, const LayerArgs& a, i
                               hipStream_t s);
 hipError_t launch_layer_pp128(int dtype, bool ta, bool tb, bool deep, const LayerArgs& a,
                               int ntiles, hipStream_t s);
-// 16 mt x 16 nt outputs a workgroup, A stored [M][K]; dense and by rows. The
-// first: 16 rows, B stored [N][K].
-hipError_t launch_layer_skinny(int dtype, int nt, const LayerArgs& a, int ntiles, hipStream_t s);
+// 16 mt x 32 (16 nt) outputs a workgroup, A stored [M][K]; dense and by rows. The
+// first: B stored [N][K], by rows and mt = 1, or (any) at any alignment.
+hipError_t launch_layer_skinny(int dtype, bool any, int mt, const LayerArgs& a, int ntiles,
+                               hipStream_t s);
 hipError_t launch_layer_split(int dtype, bool tb, int mt, int nt, const LayerArgs& a, int ntiles,
                               hipStream_t s);
 

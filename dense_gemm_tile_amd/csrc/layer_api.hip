@@ -105,7 +105,7 @@ bool wide16(const Mat& m) {
 enum LayerKernel : int {
   LK_GENERAL128 = 0, LK_GENERAL64, LK_PP256, LK_PP128, LK_PP128_DEEP,
   LK_SKINNY16, LK_SKINNY16N16, LK_SKINNY32, LK_SKINNY48, LK_SKINNY64, LK_SKINNY64N64,
-  NUM_LAYER_KERNELS
+  LK_ANY16, LK_ANY32, LK_ANY64, LK_ROWS16, NUM_LAYER_KERNELS
 };
 struct LayerKernelInfo {
   const char* name;
@@ -116,14 +116,16 @@ const LayerKernelInfo kLayerKernels[NUM_LAYER_KERNELS] = {
     {"pp128x128", 128, 128}, {"pp128x128deep", 128, 128},
     {"s16x32", 16, 32},     {"s16x16", 16, 16},     {"s32x32", 32, 32},
     {"s48x32", 48, 32},     {"s64x32", 64, 32},
-    {"s64x64", 64, 64},
+    {"s64x64", 64, 64},     {"u16x32", 16, 32},     {"u32x32", 32, 32},
+    {"u64x32", 64, 32},     {"r16x32", 16, 32},
 };
 
 struct LayerPlan {
   LayerArgs a{};
   int dtype = 0;
   bool ta = false, tb = false;
-  bool direct = false;  // both operands load in whole 16-byte pieces
+  bool reach = false;   // 32-bit offsets reach a tile's rows of both operands
+  bool direct = false;  // and both load in whole 16-byte pieces
   int kernel = LK_GENERAL128;
   int ntiles = 0;  // workgroups that cover every tile (by rows: at least)
 };
@@ -158,16 +160,21 @@ int64_t count_tiles(const LayerArgs& a, const LayerKernelInfo& k) {
          (a.mode == LAYER_SUM ? a.G : 1);
 }
 
-// Whether an operand loads in whole 16-byte pieces with 32-bit offsets over the
-// 257 rows that a tile of any kernel spans. `along` is its contiguous dimension.
+// Whether 32-bit offsets reach the 257 rows that a tile of any kernel spans, and
+// whether an operand loads in whole 16-byte pieces as well. `along` is its
+// contiguous dimension.
+bool layer_reach(const Mat& m) { return m.ptr && m.ld < (int64_t{1} << 31) / (2 * 257) - 4096; }
 bool layer_direct(const Mat& m, int64_t along) {
-  return wide16(m) && along % 8 == 0 && m.ld < (int64_t{1} << 31) / (2 * 257) - 4096;
+  return layer_reach(m) && wide16(m) && along % 8 == 0;
 }
 
 // Whether kernel k can run the call at all.
 bool kernel_runs(const LayerPlan& pl, int k) {
   if (k == LK_GENERAL128 || k == LK_GENERAL64) return true;
-  if (!pl.direct || pl.a.K == 0) return false;
+  if (pl.a.K == 0) return false;
+  if (k == LK_ROWS16) return pl.direct && pl.tb && pl.a.mode == LAYER_ROWS;
+  if (k >= LK_ANY16) return pl.reach && !pl.ta && pl.tb && pl.a.mode != LAYER_SUM;
+  if (!pl.direct) return false;
   if (k < LK_SKINNY16) return true;
   if (pl.ta || pl.a.mode == LAYER_SUM) return false;
   return pl.tb || k != LK_SKINNY16N16;  // 16 columns of B stored [K][N] are half a line
@@ -176,7 +183,7 @@ bool kernel_runs(const LayerPlan& pl, int k) {
 // By rows, the groups' sizes are only known on average. Measured on weights of
 // 2048 x 2048, 64 groups, us by average rows a group:
 //            2    8    16   32   64   128  (1024)
-//   s16x32   81  110  156  247
+//   r16x32   81  110  156  247
 //   s64x64  100  118  121  133  166  257
 //   pp128   109  127  129  131  164  163   742
 //   pp256   122  137  139  141  149  207   515
@@ -195,12 +202,12 @@ int choose_grouped(const LayerPlan& pl) {
   // One wave of workgroups takes 1.4 times as long on 256 x 256 tiles (one to a
   // CU) as on 128 x 128 ones (two to a CU).
   const int64_t rounds256 = (tiles(LK_PP256) + 255) / 256, rounds128 = (tiles(LK_PP128) + 511) / 512;
-  if (rows >= 96 && tiles(LK_PP256) >= 192 && 14 * rounds256 < 10 * rounds128 + 4) return LK_PP256;
+  if (rows >= 96 && tiles(LK_PP256) >= 192 && 14 * rounds256 < 10 * rounds128) return LK_PP256;
   if (pl.tb) {
     if (rows <= 32 && tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
     if (tiles(LK_SKINNY64N64) <= 512) return LK_SKINNY64N64;
     // (A K that leaves a wave less than two slices is too short to split.)
-    if (a.K >= 1024 && rows <= 48) return rows <= 8 ? LK_SKINNY16 : LK_SKINNY64N64;
+    if (a.K >= 1024 && rows <= 48) return rows <= 8 ? LK_ROWS16 : LK_SKINNY64N64;
   }
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
@@ -208,16 +215,29 @@ int choose_grouped(const LayerPlan& pl) {
 int choose_kernel(const LayerPlan& pl) {
   const LayerArgs& a = pl.a;
   auto tiles = [&](int k) { return count_tiles(a, kLayerKernels[k]); };
-  if (!kernel_runs(pl, LK_PP256))
+  if (!kernel_runs(pl, LK_PP256)) {
+    if (kernel_runs(pl, LK_ANY16)) {
+      if (a.mode == LAYER_ROWS) {
+        if (a.M <= 4 * (int64_t)a.G) return LK_ANY16;  // (16 rows a group: 197 us, 135 on 64 x 64)
+      } else if (a.M <= 64 || tiles(LK_ANY64) <= 256) {
+        // The most rows a tile that still give every CU one (64x4096x4095:
+        // 128 tiles of 64 rows 43 us, 256 of 32 rows 29).
+        for (int k : {LK_ANY64, LK_ANY32})
+          if (a.M > kLayerKernels[k].bm / 2 && tiles(k) >= 224) return k;
+        return a.M <= 32 ? LK_ANY16 : LK_ANY32;
+      }
+    }
     // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
     return tiles(LK_GENERAL128) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
+  }
   if (a.mode == LAYER_ROWS) return choose_grouped(pl);
   const bool split = kernel_runs(pl, LK_SKINNY64N64);
   // Few rows: the weights' bytes count.
   if (split && a.M <= 64) {
     // (16 columns of B stored [K][N] would be a quarter of a line.)
-    if (a.M <= 16) return !pl.tb ? LK_SKINNY16 : a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY32;
-    return a.M <= 32 ? LK_SKINNY32 : a.M <= 48 ? LK_SKINNY48 : LK_SKINNY64;
+    if (a.M <= 16) return pl.tb && a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY16;
+    if (a.M <= 32 || tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
+    return a.M <= 48 ? LK_SKINNY48 : LK_SKINNY64;
   }
   const int64_t n256 = tiles(LK_PP256);
   if (n256 >= 256 || (n256 >= 192 && a.K >= 1024) || (n256 >= 128 && a.K >= 2048)) return LK_PP256;
@@ -274,7 +294,8 @@ hipError_t launch_product(const LayerPlan& pl, hipStream_t s) {
                                   pl.ntiles, s);
     default: {
       const LayerKernelInfo& k = kLayerKernels[pl.kernel];
-      if (k.bm == 16 && pl.tb) return launch_layer_skinny(pl.dtype, k.bn / 16, pl.a, pl.ntiles, s);
+      if (pl.kernel >= LK_ANY16)
+        return launch_layer_skinny(pl.dtype, pl.kernel != LK_ROWS16, k.bm / 16, pl.a, pl.ntiles, s);
       return launch_layer_split(pl.dtype, pl.tb, k.bm / 16, k.bn / 16, pl.a, pl.ntiles, s);
     }
   }
@@ -365,6 +386,7 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
   pl.dtype = dtype;
   pl.ta = ta;
   pl.tb = tb;
+  pl.reach = layer_reach(ma) && layer_reach(mb);
   pl.direct = layer_direct(ma, ta ? M : K) && layer_direct(mb, tb ? K : N);
   return plan_tiles(pl, dense ? "linear" : "grouped");
 }
@@ -425,6 +447,7 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
   pl.dtype = dtype;
   pl.ta = true;
   pl.tb = false;
+  pl.reach = M > 0 && layer_reach(ma) && layer_reach(mb);
   pl.direct = M > 0 && layer_direct(ma, N) && layer_direct(mb, K);
   return plan_tiles(pl, "grad_weight");
 }

@@ -1,6 +1,6 @@
 // The layer operators' product on tiles of up to 64 rows, A stored [M][K], the
-// sum split over the workgroup's waves: decoding batches of more than 16 rows,
-// and grids too small for larger tiles.
+// sum split over the workgroup's waves: decoding batches, and grids too small
+// for larger tiles.
 //
 // A workgroup owns 16 MT rows and 16 NT columns; wave w takes slices w, w + KW,
 // ... of 64 and loads their pieces of both operands straight into LDS of its
@@ -96,12 +96,12 @@ __global__ void __launch_bounds__(KW * 64) layer_split_kernel(const LayerArgs p)
   using Sum = SplitSum<MT, NT, KW>;
   using SA = SplitAlong<MT>;
   using SB = SplitAlong<NT>;
-  using RB = SplitRows<NT>;
+  using RB = SplitRows<NT == 1 ? 2 : NT>;  // (B stored [K][N]: not 16 columns)
   constexpr int A_SLICE = 2048 * MT, SLICE = A_SLICE + 2048 * NT;
   constexpr int LOADS = 2 * MT + 2 * NT;
   constexpr int BYTES = KW * D * SLICE > Sum::LDS_BYTES ? KW * D * SLICE : Sum::LDS_BYTES;
   static_assert(BYTES <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
-  static_assert(SB::LOADS == 2 * NT && RB::LOADS == 2 * NT, "both forms of B take as many loads");
+  static_assert(!BMN || (NT > 1 && RB::LOADS == SB::LOADS), "both forms of B take as many loads");
   static_assert(D <= 4, "split_wait tells at most three slices apart");
   __shared__ __attribute__((aligned(1024))) char smem[BYTES];
 
@@ -186,9 +186,9 @@ hipError_t launch(const LayerArgs& a, int ntiles, hipStream_t s) {
 // D and KW: as many slices as the LDS holds, for eight waves while two fit.
 template <class Tag, int MODE, bool BMN>
 hipError_t launch_form(int mt, int nt, const LayerArgs& a, int ntiles, hipStream_t s) {
-  if constexpr (BMN) {
-    if (mt == 1) return launch<Tag, MODE, BMN, 1, 2, 3, 8>(a, ntiles, s);
-  }
+  if constexpr (!BMN)
+    if (mt == 1 && nt == 1) return launch<Tag, MODE, BMN, 1, 1, 4, 8>(a, ntiles, s);
+  if (mt == 1) return launch<Tag, MODE, BMN, 1, 2, 3, 8>(a, ntiles, s);
   if (mt == 2) return launch<Tag, MODE, BMN, 2, 2, 2, 8>(a, ntiles, s);
   if (mt == 3) return launch<Tag, MODE, BMN, 3, 2, 2, 8>(a, ntiles, s);
   if (nt == 2) return launch<Tag, MODE, BMN, 4, 2, 3, 4>(a, ntiles, s);

@@ -18,7 +18,9 @@ TILES = {"g128x128": (128, 128), "g64x64": (64, 64), "pp256x256": (256, 256), "p
 # A stored [M][K]; s16x16 with B stored [N][K] only.
 SKINNY = {"s16x32": (16, 32), "s32x32": (32, 32), "s64x32": (64, 32), "s64x64": (64, 64),
           "s16x16": (16, 16), "s48x32": (48, 32)}
-NT_ONLY = ("s16x16",)
+NT_ONLY = ("s16x16", "r16x32")
+# Any alignment and K, A stored [M][K], B stored [N][K].
+ANY = {"u16x32": (16, 32), "u32x32": (32, 32), "u64x32": (64, 32)}
 
 
 @contextmanager
@@ -56,10 +58,10 @@ def test_dense_forced(name):
                     i += 1
 
 
-@pytest.mark.parametrize("name", [*TILES, *SKINNY])
+@pytest.mark.parametrize("name", [*TILES, *SKINNY, "r16x32"])
 def test_grouped_forced(name):
     need_gpu()
-    bm, bn = {**TILES, **SKINNY}[name]
+    bm, bn = {**TILES, **SKINNY, "r16x32": (16, 32)}[name]
     gen = torch.Generator().manual_seed(bm * 3 + bn)
     sizes = [[1], [0, 0, bm, 0], [bm - 1, 1, bm + 1, 0, 3 * bm + 5], [1, 0, 2] * 30, [0], [7] * 67, [bm] * 3]
     with tile(name):
@@ -72,6 +74,51 @@ def test_grouped_forced(name):
                                    residual=i % 3 == 0, keep_z=i % 4 == 1, spare=(i * 7) % 20,
                                    out_dtype="f32" if i % 3 == 1 else None, shared=i == 3)
                     assert f" {name} " in path, path
+
+
+@pytest.mark.parametrize("name", list(ANY))
+def test_any_alignment_forced(name):
+    need_gpu()
+    bm, bn = ANY[name]
+    gen = torch.Generator().manual_seed(bm * 11 + bn)
+    i = 0
+    with tile(name):
+        for pads in ((0, 0, 0), (1, 0, 3), (0, 1, 0), (3, 5, 1), (2, 4, 6)):
+            for M, N in ((1, 1), (bm, bn), (bm - 3, bn + 3), (2 * bm + 1, 3 * bn - 5)):
+                for K in (1, 2, 7, 8, 9, 63, 64, 65, 129, 520, 701, 1033, 2055):
+                    dtype = ("f16", "bf16")[i % 2]
+                    path = linear(gen, M, N, K, dtype, 0, 1, act=ACTS[i % 5], bias=i % 2 == 0, residual=i % 3 == 0,
+                                  keep_z=i % 4 == 1, out_dtype="f32" if i % 3 == 1 else dtype, pads=pads)
+                    assert f" {name} " in path, path
+                    i += 1
+        for i, s in enumerate([[1], [0, 0, bm, 0], [bm - 1, 1, bm + 1, 0, 3 * bm + 5], [1, 0, 2] * 30]):
+            for N, K in ((bn + 1, 65), (7, 701), (bn, 128)):
+                path = grouped(gen, s, N, K, ("f16", "bf16")[i % 2], 1, act=ACTS[i % 5], bias=i % 2 == 0,
+                               keep_z=i % 4 == 1, spare=(i * 7) % 20, pads=(i % 3, i % 2, 0))
+                assert f" {name} " in path, path
+
+
+def test_any_alignment_of_the_first_element():
+    """Operands that start 2, 4, 6 ... bytes into an allocation, odd pitches."""
+    need_gpu()
+    import dense_gemm_tile_amd as dgt
+    from layer_helpers import linear_want
+    gen = torch.Generator().manual_seed(12)
+    for name, (bm, _) in ANY.items():
+        with tile(name):
+            for ao in range(4):
+                for bo in range(4):
+                    M, N, K, lda, ldb = bm + 1, 37, 203, 203 + ao, 203 + bo
+                    x = randn(gen, (M + 1) * lda, dtype="bf16")[ao:]
+                    w = randn(gen, (N + 1) * ldb, dtype="bf16")[bo:]
+                    xs = torch.as_strided(x, (M, K), (lda, 1), x.storage_offset())
+                    ws = torch.as_strided(w, (N, K), (ldb, 1), w.storage_offset())
+                    y = out(M, N, dtype="f32")
+                    say(f"{name} starts {2 * ao} and {2 * bo} bytes in")
+                    dgt.gemm_linear(M, N, K, "bf16", 0, 1, xs, lda, ws, ldb, None, "none", None, 0, y, N, "f32",
+                                    stream=torch.cuda.current_stream())
+                    wy, _, ty, _ = linear_want(xs, ws.T, None, None, "none", "bf16", "f32")
+                    close(y, wy, ty, dgt.gemm_last_path())
 
 
 @pytest.mark.parametrize("name", list(TILES))
