@@ -235,6 +235,37 @@ __device__ __forceinline__ float layer_sigmoid(float v) { return layer_logistic2
 constexpr float kGeluA = 1.5957691216057308f;       // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
+// The normal distribution's function Phi(z) and exp(-z^2 / 2). With x = |z| /
+// sqrt(2) and t = 1 / (1 + x / 2), erfc(x) exp(x^2) / t is smooth on t in (0, 1]: a
+// polynomial of degree 8 fitted to it for x up to 9.4 by least squares weighted
+// toward the largest relative error (4e-8; 1.4e-7 in float32 arithmetic). The
+// exponent z^2 / 2 log2(e) is held in two floats, so that the exponential keeps
+// its relative accuracy far out: Phi of a negative z is not a difference. (The
+// library's erfc: 4096x4096x1024 48 us, 42 so, 32 without an activation.)
+struct LayerNormal {
+  float phi, e;
+};
+__device__ __forceinline__ LayerNormal layer_normal(float z) {
+  const float c = __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f);  // both are 0 or 1 past that
+  constexpr float kHi = 0.7213475108146667f, kLo = 9.629815e-09f;  // log2(e) / 2
+  const float h = c * kHi, hl = __builtin_fmaf(c, kLo, __builtin_fmaf(c, kHi, -h));
+  const float hi = h * c, lo = __builtin_fmaf(hl, c, __builtin_fmaf(h, c, -hi));
+  const float e0 = __builtin_amdgcn_exp2f(-hi);
+  const float e = __builtin_fmaf(-0.6931471805599453f * lo, e0, e0);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(c), 0.3535533905932738f, 1.0f));
+  float g = -0.0588473342359066f;
+  g = __builtin_fmaf(g, t, 0.2834887206554413f);
+  g = __builtin_fmaf(g, t, -0.4849390983581543f);
+  g = __builtin_fmaf(g, t, 0.2754654288291931f);
+  g = __builtin_fmaf(g, t, -0.024821195751428604f);
+  g = __builtin_fmaf(g, t, 0.201917365193367f);
+  g = __builtin_fmaf(g, t, 0.24330003559589386f);
+  g = __builtin_fmaf(g, t, 0.28234803676605225f);
+  g = __builtin_fmaf(g, t, 0.2820879817008972f);
+  const float q = 0.5f * t * g * e;  // Phi(-|z|)
+  return {c < 0.0f ? q : 1.0f - q, e};
+}
+
 // GELU's tanh form, z (1 + tanh(u)) / 2, is z * sigmoid(2 u): no difference
 // of nearly equal numbers for negative z.
 template <int ACT>
@@ -244,7 +275,7 @@ __device__ __forceinline__ float layer_act(float z) {
     const float w = __builtin_fmaf(z * z, -kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA);
     return z * layer_logistic2(z * w);
   }
-  if constexpr (ACT == ACT_GELU_ERF) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+  if constexpr (ACT == ACT_GELU_ERF) return z * layer_normal(z).phi;
   if constexpr (ACT == ACT_SILU) return z * layer_sigmoid(z);
   return z;
 }
@@ -259,9 +290,9 @@ __device__ __forceinline__ float layer_slope(float z) {
     return s + c * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * c * c);
   }
   if constexpr (ACT == ACT_GELU_ERF) {
+    const LayerNormal n = layer_normal(z);
     const float c = z > 16.0f ? 16.0f : (z < -16.0f ? -16.0f : z);
-    return 0.5f * erfcf(-0.70710678118654752f * c) +
-           c * 0.3989422804014327f * __expf(-0.5f * c * c);
+    return __builtin_fmaf(c * 0.3989422804014327f, n.e, n.phi);
   }
   if constexpr (ACT == ACT_SILU) {
     const float s = layer_sigmoid(z);
@@ -273,6 +304,15 @@ template <int ACT>
 __device__ __forceinline__ void layer_act8_of(float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = layer_act<ACT>(f[e]);
+}
+__device__ __forceinline__ float layer_act1(float z, int act) {
+  switch (act) {  // uniform over the launch
+    case ACT_RELU: return layer_act<ACT_RELU>(z);
+    case ACT_GELU: return layer_act<ACT_GELU>(z);
+    case ACT_GELU_ERF: return layer_act<ACT_GELU_ERF>(z);
+    case ACT_SILU: return layer_act<ACT_SILU>(z);
+    default: return z;
+  }
 }
 __device__ __forceinline__ void layer_act8(float (&f)[8], int act) {
   switch (act) {  // uniform over the launch
@@ -369,6 +409,13 @@ struct LayerEpi {
   static constexpr int LPR = W / 8, RPP = 64 / LPR;       // lanes a row, rows a pass
   static constexpr int PASSES = BATCH / RPP;
   static constexpr int GROUP = PASSES < 4 ? PASSES : 4;   // passes unrolled
+  // Outputs that are not 16-byte pieces go one column a lane, so that the lanes'
+  // accesses are consecutive at any alignment, from the waves of 64 x 32 outputs
+  // (8192x1001x1024: 43 us with 8 columns a lane, 37 so). The others keep 8
+  // columns a lane: on 64 x 64 outputs the general kernel takes 16 us instead of
+  // 28 for 2000x701x300, and the masked 256x256 kernel, compiled with the loop
+  // over columns, spends 28 us more on every tile, taken or not.
+  static constexpr bool COLUMNS = ROWS == 64 && W == 32;
   static_assert(W % 8 == 0 && 64 % LPR == 0 && BATCH % RPP == 0 && PASSES % GROUP == 0 &&
                     ROWS % BATCH == 0 && BATCH % At::M == 0,
                 "whole passes");
@@ -454,6 +501,43 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
   }
 }
 
+// The same where some rows are not 16-byte pieces: one column a lane.
+template <class E, class Tag>
+__device__ __forceinline__ void layer_columns(const LayerArgs& p, const LayerTile& q, int r0, int c0,
+                                              int lane, const float* lds) {
+  constexpr int RPS = 64 / E::W, STEPS = E::BATCH / RPS, U = 4;  // rows a step; steps at once
+  static_assert(E::W <= 64 && STEPS % U == 0, "whole steps");
+  const int col = lane % E::W, c = c0 + col, rl = lane / E::W;
+  if (c >= q.N) return;
+  auto load16 = [&](const char* at) { return layer_f32(Tag{}, *reinterpret_cast<const unsigned short*>(at)); };
+  const float bias = q.bias ? load16(q.bias + (int64_t)c * 2) : 0.0f;
+#pragma unroll 1
+  for (int s = 0; s < STEPS; s += U) {
+    float x[U], res[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int in = (s + u) * RPS + rl, row = r0 + in;
+      x[u] = lds[in * E::P + col] + bias;
+      res[u] = 0.0f;
+      if (q.R && row < q.M) {
+        const int64_t at = (int64_t)row * p.ldr + c;
+        res[u] = p.out32 ? reinterpret_cast<const float*>(q.R)[at] : load16(q.R + at * 2);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = r0 + (s + u) * RPS + rl;
+      if (row >= q.M) continue;
+      if (q.Z)
+        reinterpret_cast<unsigned short*>(q.Z)[(int64_t)row * p.ldz + c] = layer_16(Tag{}, x[u]);
+      const float y = layer_act1(x[u], p.act) + res[u];
+      const int64_t at = (int64_t)row * p.ldy + c;
+      if (p.out32) reinterpret_cast<float*>(q.Y)[at] = y;
+      else reinterpret_cast<unsigned short*>(q.Y)[at] = layer_16(Tag{}, y);
+    }
+  }
+}
+
 template <class C, class Tag>
 __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][C::TN],
                                             const LayerArgs& p, const LayerTile& q, int r0, int c0,
@@ -495,13 +579,17 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
         default: layer_passes<E, Tag, ACT_NONE>(p, q, r + rl, c, from, bias, res); break;
       }
     } else {
+      if constexpr (E::COLUMNS) {
+        layer_columns<E, Tag>(p, q, r, c0, lane, lds);
+      } else {
 #pragma unroll 1
-      for (int s = 0; s < E::PASSES; ++s) {
-        const int row = r + s * E::RPP + rl;
-        float x[8];
+        for (int s = 0; s < E::PASSES; ++s) {
+          const int row = r + s * E::RPP + rl;
+          float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = from[s * E::RPP * P + e];
-        if (row < q.M && nv > 0) layer_finish8<Tag>(p, q, row, c, nv, bias, x);
+          for (int e = 0; e < 8; ++e) x[e] = from[s * E::RPP * P + e];
+          if (row < q.M && nv > 0) layer_finish8<Tag>(p, q, row, c, nv, bias, x);
+        }
       }
     }
     layer_wave_order();
@@ -532,7 +620,8 @@ hipError_t layer_for_layout(const LayerArgs& a, bool ta, bool tb, F f) {
 
 // The kernels of the products, each next to its definition. dtype: 0 f16, 1
 // bf16. They return the HIP status of the launch.
-hipError_t launch_layer_general(int dtype, bool ta, bool tb, bool small, const LayerArgs& a,
+// tile: 0 128x128, 1 64x64, 2 64x64 with the sum split over four wave groups.
+hipError_t launch_layer_general(int dtype, bool ta, bool tb, int tile, const LayerArgs& a,
                                 int ntiles, hipStream_t s);
 // Operands in whole 16-byte pieces (layer_direct in layer_api.hip). deep: ten
 // half-slots of LDS instead of five.
@@ -540,11 +629,11 @@ hipError_t launch_layer_pp256(int dtype, bool ta, bool tb, const LayerArgs& a, i
                               hipStream_t s);
 hipError_t launch_layer_pp128(int dtype, bool ta, bool tb, bool deep, const LayerArgs& a,
                               int ntiles, hipStream_t s);
-// 16 mt x 32 (16 nt) outputs a workgroup, A stored [M][K]; dense and by rows. The
-// first: B stored [N][K], by rows and mt = 1, or (any) at any alignment.
+// 16 mt x 32 (16 nt) outputs a workgroup. The first: A stored [M][K], B stored
+// [N][K], by rows and mt = 1, or (any) dense and by rows at any alignment.
 hipError_t launch_layer_skinny(int dtype, bool any, int mt, const LayerArgs& a, int ntiles,
                                hipStream_t s);
-hipError_t launch_layer_split(int dtype, bool tb, int mt, int nt, const LayerArgs& a, int ntiles,
+hipError_t launch_layer_split(int dtype, bool ta, bool tb, int mt, int nt, const LayerArgs& a, int ntiles,
                               hipStream_t s);
 
 }  // namespace dgt

@@ -105,7 +105,8 @@ bool wide16(const Mat& m) {
 enum LayerKernel : int {
   LK_GENERAL128 = 0, LK_GENERAL64, LK_PP256, LK_PP128, LK_PP128_DEEP,
   LK_SKINNY16, LK_SKINNY16N16, LK_SKINNY32, LK_SKINNY48, LK_SKINNY64, LK_SKINNY64N64,
-  LK_ANY16, LK_ANY32, LK_ANY64, LK_ROWS16, NUM_LAYER_KERNELS
+  LK_ANY16, LK_ANY32, LK_ANY64, LK_ROWS16, LK_GENERAL64K4,
+  NUM_LAYER_KERNELS
 };
 struct LayerKernelInfo {
   const char* name;
@@ -118,6 +119,7 @@ const LayerKernelInfo kLayerKernels[NUM_LAYER_KERNELS] = {
     {"s48x32", 48, 32},     {"s64x32", 64, 32},
     {"s64x64", 64, 64},     {"u16x32", 16, 32},     {"u32x32", 32, 32},
     {"u64x32", 64, 32},     {"r16x32", 16, 32},
+    {"g64x64k4", 64, 64},
 };
 
 struct LayerPlan {
@@ -170,14 +172,15 @@ bool layer_direct(const Mat& m, int64_t along) {
 
 // Whether kernel k can run the call at all.
 bool kernel_runs(const LayerPlan& pl, int k) {
-  if (k == LK_GENERAL128 || k == LK_GENERAL64) return true;
+  if (k == LK_GENERAL128 || k == LK_GENERAL64 || k == LK_GENERAL64K4) return true;
   if (pl.a.K == 0) return false;
   if (k == LK_ROWS16) return pl.direct && pl.tb && pl.a.mode == LAYER_ROWS;
   if (k >= LK_ANY16) return pl.reach && !pl.ta && pl.tb && pl.a.mode != LAYER_SUM;
   if (!pl.direct) return false;
   if (k < LK_SKINNY16) return true;
-  if (pl.ta || pl.a.mode == LAYER_SUM) return false;
-  return pl.tb || k != LK_SKINNY16N16;  // 16 columns of B stored [K][N] are half a line
+  // Operands not stored along K come in rows of 32 or 64 elements.
+  if (pl.ta) return k == LK_SKINNY32 || k == LK_SKINNY64 || k == LK_SKINNY64N64;
+  return pl.tb || k != LK_SKINNY16N16;
 }
 
 // By rows, the groups' sizes are only known on average. Measured on weights of
@@ -203,6 +206,7 @@ int choose_grouped(const LayerPlan& pl) {
   // CU) as on 128 x 128 ones (two to a CU).
   const int64_t rounds256 = (tiles(LK_PP256) + 255) / 256, rounds128 = (tiles(LK_PP128) + 511) / 512;
   if (rows >= 96 && tiles(LK_PP256) >= 192 && 14 * rounds256 < 10 * rounds128) return LK_PP256;
+  if (!pl.tb && rows <= 16 && tiles(LK_SKINNY16) <= 512) return LK_SKINNY16;
   if (pl.tb) {
     if (rows <= 32 && tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
     if (tiles(LK_SKINNY64N64) <= 512) return LK_SKINNY64N64;
@@ -227,13 +231,15 @@ int choose_kernel(const LayerPlan& pl) {
         return a.M <= 32 ? LK_ANY16 : LK_ANY32;
       }
     }
+    // The sum split over wave groups where even 64 x 64 tiles leave CUs idle.
+    if (tiles(LK_GENERAL64) <= 256 && a.K >= 512) return LK_GENERAL64K4;
     // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
     return tiles(LK_GENERAL128) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
   }
   if (a.mode == LAYER_ROWS) return choose_grouped(pl);
   const bool split = kernel_runs(pl, LK_SKINNY64N64);
   // Few rows: the weights' bytes count.
-  if (split && a.M <= 64) {
+  if (split && !pl.ta && a.M <= 64) {
     // (16 columns of B stored [K][N] would be a quarter of a line.)
     if (a.M <= 16) return pl.tb && a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY16;
     if (a.M <= 32 || tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
@@ -290,13 +296,15 @@ hipError_t launch_product(const LayerPlan& pl, hipStream_t s) {
       return launch_layer_pp128(pl.dtype, pl.ta, pl.tb, pl.kernel == LK_PP128_DEEP, pl.a, pl.ntiles, s);
     case LK_GENERAL128:
     case LK_GENERAL64:
-      return launch_layer_general(pl.dtype, pl.ta, pl.tb, pl.kernel == LK_GENERAL64, pl.a,
-                                  pl.ntiles, s);
+    case LK_GENERAL64K4:
+      return launch_layer_general(pl.dtype, pl.ta, pl.tb,
+                                  pl.kernel == LK_GENERAL128 ? 0 : pl.kernel == LK_GENERAL64 ? 1 : 2,
+                                  pl.a, pl.ntiles, s);
     default: {
       const LayerKernelInfo& k = kLayerKernels[pl.kernel];
       if (pl.kernel >= LK_ANY16)
         return launch_layer_skinny(pl.dtype, pl.kernel != LK_ROWS16, k.bm / 16, pl.a, pl.ntiles, s);
-      return launch_layer_split(pl.dtype, pl.tb, k.bm / 16, k.bn / 16, pl.a, pl.ntiles, s);
+      return launch_layer_split(pl.dtype, pl.ta, pl.tb, k.bm / 16, k.bn / 16, pl.a, pl.ntiles, s);
     }
   }
 }

@@ -300,26 +300,38 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
       wt[u] = at[u] >= 0 && p.weights ? p.weights[t0 + j] : 1.0f;
       dot[u] = 0.0f;
     }
-    for (int64_t c = (int64_t)tid * E; c < p.H; c += 256 * E) {
-      float d[E], y[4][E];
-      Io::template load<true>(p.dY, (int64_t)t * p.lddy + c, d);
-      if (p.dw) {
+    // S pieces of every row at once, 16 bytes or so a lane and row.
+    constexpr int S = E >= 4 ? 1 : 4 / E;
+    for (int64_t c0 = (int64_t)tid * E; c0 < p.H; c0 += 256 * E * S) {
+      float d[S][E], y[4][S][E];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (at[u] >= 0) Io::template load<true>(p.Ys, (int64_t)at[u] * p.ldys + c, y[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (at[u] < 0) continue;
+      for (int s = 0; s < S; ++s) {
+        const int64_t c = c0 + s * 256 * E;
+        if (c >= p.H) continue;
+        Io::template load<true>(p.dY, (int64_t)t * p.lddy + c, d[s]);
         if (p.dw) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) dot[u] = __builtin_fmaf(d[e], y[u][e], dot[u]);
+          for (int u = 0; u < 4; ++u)
+            if (at[u] >= 0) Io::template load<true>(p.Ys, (int64_t)at[u] * p.ldys + c, y[u][s]);
         }
-        if (p.dYs) {
-          float o[E];
+      }
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = wt[u] * d[e];
-          Io::store(p.dYs, (int64_t)at[u] * p.lddys + c, o);
+      for (int s = 0; s < S; ++s) {
+        const int64_t c = c0 + s * 256 * E;
+        if (c >= p.H) continue;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (at[u] < 0) continue;
+          if (p.dw) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot[u] = __builtin_fmaf(d[s][e], y[u][s][e], dot[u]);
+          }
+          if (p.dYs) {
+            float o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = wt[u] * d[s][e];
+            Io::store(p.dYs, (int64_t)at[u] * p.lddys + c, o);
+          }
         }
       }
     }

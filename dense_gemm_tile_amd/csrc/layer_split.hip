@@ -1,5 +1,4 @@
-// The layer operators' product on tiles of up to 64 rows, A stored [M][K], the
-// sum split over the workgroup's waves: decoding batches, and grids too small
+// The layer operators' product on tiles of up to 64 rows, the sum split over the workgroup's waves: decoding batches, and grids too small
 // for larger tiles.
 //
 // A workgroup owns 16 MT rows and 16 NT columns; wave w takes slices w, w + KW,
@@ -90,18 +89,20 @@ struct SplitRows {
   }
 };
 
-template <class Tag, int MODE, bool BMN, int MT, int NT, int D, int KW>
+template <class Tag, int MODE, bool AMN, bool BMN, int MT, int NT, int D, int KW>
 __global__ void __launch_bounds__(KW * 64) layer_split_kernel(const LayerArgs p) {
   using At = SplitAtom;
   using Sum = SplitSum<MT, NT, KW>;
   using SA = SplitAlong<MT>;
   using SB = SplitAlong<NT>;
+  using RA = SplitRows<MT == 2 ? 2 : 4>;  // (A stored [K][M]: 32 or 64 rows)
   using RB = SplitRows<NT == 1 ? 2 : NT>;  // (B stored [K][N]: not 16 columns)
   constexpr int A_SLICE = 2048 * MT, SLICE = A_SLICE + 2048 * NT;
   constexpr int LOADS = 2 * MT + 2 * NT;
   constexpr int BYTES = KW * D * SLICE > Sum::LDS_BYTES ? KW * D * SLICE : Sum::LDS_BYTES;
   static_assert(BYTES <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
   static_assert(!BMN || (NT > 1 && RB::LOADS == SB::LOADS), "both forms of B take as many loads");
+  static_assert(!AMN || MT == 2 || MT == 4, "A stored [K][M] is laid out in 64- or 128-byte rows");
   static_assert(D <= 4, "split_wait tells at most three slices apart");
   __shared__ __attribute__((aligned(1024))) char smem[BYTES];
 
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(KW * 64) layer_split_kernel(const LayerArgs p)
 
   // Resources end at the last byte of the operand's last row here, so no offset
   // below 2^31 reads past it.
-  const auto ra = make_rsrc_n(q.A + (int64_t)q.m0 * p.lda * 2, split_records(q.M - q.m0, p.lda, q.K));
+  const char* const Ab = AMN ? q.A + (int64_t)q.m0 * 2 : q.A + (int64_t)q.m0 * p.lda * 2;
+  const auto ra = make_rsrc_n(Ab, split_records(q.M - q.m0, p.lda, q.K));  // (not AMN)
   const char* const Bb = BMN ? q.B + (int64_t)q.n0 * 2 : q.B + (int64_t)q.n0 * p.ldb * 2;
   const auto rb = make_rsrc_n(Bb, split_records(q.N - q.n0, p.ldb, q.K));  // (not BMN)
 
@@ -127,13 +129,16 @@ __global__ void __launch_bounds__(KW * 64) layer_split_kernel(const LayerArgs p)
 
   const int KT = (q.K + 63) / 64;
   // (B stored [K][N]: neighbouring column tiles share lines, so all walk alike.)
-  const int start = BMN ? 0 : split_start(q.n0 / Sum::BN, KT);
+  const int start = AMN || BMN ? 0 : split_start(q.n0 / Sum::BN, KT);
   const int NJ = KT > w ? (KT - w + KW - 1) / KW : 0;  // this wave's slices
   char* const mine = smem + w * D * SLICE;
   auto request = [&](int d, int j) {
     const int s = j * KW + w + start, slice = s >= KT ? s - KT : s;
     char* const lds = mine + d * SLICE;
-    SA::request(ra, (int)(p.lda * 2), q.M - q.m0, q.K, slice, lds, lane);
+    if constexpr (AMN)
+      RA::request(Ab, p.lda, q.K - slice * 64, q.M - q.m0, slice, lds, lane);
+    else
+      SA::request(ra, (int)(p.lda * 2), q.M - q.m0, q.K, slice, lds, lane);
     if constexpr (BMN)
       RB::request(Bb, p.ldb, q.K - slice * 64, q.N - q.n0, slice, lds + A_SLICE, lane);
     else
@@ -148,7 +153,8 @@ __global__ void __launch_bounds__(KW * 64) layer_split_kernel(const LayerArgs p)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) a[i][h] = SA::read(lds, i, h, lane);
+      for (int i = 0; i < MT; ++i)
+        a[i][h] = AMN ? RA::read(lds, i, h, lane) : SA::read(lds, i, h, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         b[n][h] = BMN ? RB::read(lds + A_SLICE, n, h, lane) : SB::read(lds + A_SLICE, n, h, lane);
@@ -178,37 +184,38 @@ __global__ void __launch_bounds__(KW * 64) layer_split_kernel(const LayerArgs p)
   Sum::template finish<Tag>(acc, p, q, smem, tid, w);
 }
 
-template <class Tag, int MODE, bool BMN, int MT, int NT, int D, int KW>
+template <class Tag, int MODE, bool AMN, bool BMN, int MT, int NT, int D, int KW>
 hipError_t launch(const LayerArgs& a, int ntiles, hipStream_t s) {
-  return launch_kernel(layer_split_kernel<Tag, MODE, BMN, MT, NT, D, KW>, dim3(ntiles),
+  return launch_kernel(layer_split_kernel<Tag, MODE, AMN, BMN, MT, NT, D, KW>, dim3(ntiles),
                        dim3(KW * 64), s, a);
 }
 // D and KW: as many slices as the LDS holds, for eight waves while two fit.
-template <class Tag, int MODE, bool BMN>
+template <class Tag, int MODE, bool AMN, bool BMN>
 hipError_t launch_form(int mt, int nt, const LayerArgs& a, int ntiles, hipStream_t s) {
-  if constexpr (!BMN)
-    if (mt == 1 && nt == 1) return launch<Tag, MODE, BMN, 1, 1, 4, 8>(a, ntiles, s);
-  if (mt == 1) return launch<Tag, MODE, BMN, 1, 2, 3, 8>(a, ntiles, s);
-  if (mt == 2) return launch<Tag, MODE, BMN, 2, 2, 2, 8>(a, ntiles, s);
-  if (mt == 3) return launch<Tag, MODE, BMN, 3, 2, 2, 8>(a, ntiles, s);
-  if (nt == 2) return launch<Tag, MODE, BMN, 4, 2, 3, 4>(a, ntiles, s);
-  return launch<Tag, MODE, BMN, 4, 4, 2, 4>(a, ntiles, s);
+  if constexpr (!AMN) {
+    if constexpr (!BMN)
+      if (mt == 1 && nt == 1) return launch<Tag, MODE, AMN, BMN, 1, 1, 4, 8>(a, ntiles, s);
+    if (mt == 1) return launch<Tag, MODE, AMN, BMN, 1, 2, 3, 8>(a, ntiles, s);
+    if (mt == 3) return launch<Tag, MODE, AMN, BMN, 3, 2, 2, 8>(a, ntiles, s);
+  }
+  if (mt == 2) return launch<Tag, MODE, AMN, BMN, 2, 2, 2, 8>(a, ntiles, s);
+  if (nt == 2) return launch<Tag, MODE, AMN, BMN, 4, 2, 3, 4>(a, ntiles, s);
+  return launch<Tag, MODE, AMN, BMN, 4, 4, 2, 4>(a, ntiles, s);
 }
 template <class Tag>
-hipError_t launch_mode(bool tb, int mt, int nt, const LayerArgs& a, int ntiles, hipStream_t s) {
-  if (a.mode == LAYER_ROWS)
-    return tb ? launch_form<Tag, LAYER_ROWS, false>(mt, nt, a, ntiles, s)
-              : launch_form<Tag, LAYER_ROWS, true>(mt, nt, a, ntiles, s);
-  return tb ? launch_form<Tag, LAYER_DENSE, false>(mt, nt, a, ntiles, s)
-            : launch_form<Tag, LAYER_DENSE, true>(mt, nt, a, ntiles, s);
+hipError_t launch_layout(bool ta, bool tb, int mt, int nt, const LayerArgs& a, int ntiles,
+                         hipStream_t s) {
+  return layer_for_layout(a, ta, tb, [&](auto mode, auto la, auto lb) {
+    return launch_form<Tag, mode.value, la.value != 0, lb.value == 0>(mt, nt, a, ntiles, s);
+  });
 }
 
 }  // namespace
 
-hipError_t launch_layer_split(int dtype, bool tb, int mt, int nt, const LayerArgs& a, int ntiles,
-                              hipStream_t s) {
-  if (dtype == 0) return launch_mode<TagF16>(tb, mt, nt, a, ntiles, s);
-  return launch_mode<TagBF16>(tb, mt, nt, a, ntiles, s);
+hipError_t launch_layer_split(int dtype, bool ta, bool tb, int mt, int nt, const LayerArgs& a,
+                              int ntiles, hipStream_t s) {
+  if (dtype == 0) return launch_layout<TagF16>(ta, tb, mt, nt, a, ntiles, s);
+  return launch_layout<TagBF16>(ta, tb, mt, nt, a, ntiles, s);
 }
 
 }  // namespace dgt

@@ -13,11 +13,12 @@ from test_layer_product_gpu import grouped, linear
 pytestmark = pytest.mark.gpu
 
 LAYOUTS = [(0, 1), (0, 0), (1, 0), (1, 1)]
-TILES = {"g128x128": (128, 128), "g64x64": (64, 64), "pp256x256": (256, 256), "pp128x128": (128, 128),
+TILES = {"g128x128": (128, 128), "g64x64": (64, 64), "g64x64k4": (64, 64), "pp256x256": (256, 256), "pp128x128": (128, 128),
          "pp128x128deep": (128, 128)}
-# A stored [M][K]; s16x16 with B stored [N][K] only.
+# A stored [M][K], those of ALL in any layout; s16x16 with B stored [N][K] only.
 SKINNY = {"s16x32": (16, 32), "s32x32": (32, 32), "s64x32": (64, 32), "s64x64": (64, 64),
           "s16x16": (16, 16), "s48x32": (48, 32)}
+ALL = ("s32x32", "s64x32", "s64x64")
 NT_ONLY = ("s16x16", "r16x32")
 # Any alignment and K, A stored [M][K], B stored [N][K].
 ANY = {"u16x32": (16, 32), "u32x32": (32, 32), "u64x32": (64, 32)}
@@ -34,7 +35,7 @@ def tile(name):
 
 
 def layouts(name):
-    return [la for la in LAYOUTS if name in TILES or (not la[0] and (la[1] or name not in NT_ONLY))]
+    return [la for la in LAYOUTS if name in TILES or name in ALL or (not la[0] and (la[1] or name not in NT_ONLY))]
 
 
 @pytest.mark.parametrize("name", [*TILES, *SKINNY])
@@ -121,11 +122,11 @@ def test_any_alignment_of_the_first_element():
                     close(y, wy, ty, dgt.gemm_last_path())
 
 
-@pytest.mark.parametrize("name", list(TILES))
+@pytest.mark.parametrize("name", [*TILES, *ALL])
 def test_grad_weight_forced(name):
     need_gpu()
     import dense_gemm_tile_amd as dgt
-    bm, bn = TILES[name]
+    bm, bn = {**TILES, **SKINNY}[name]
     gen = torch.Generator().manual_seed(bm + bn)
     with tile(name):
         for i, sizes in enumerate([[1], [0], [64, 0, 65], [200, 1, 0, 63, 330], [3, 0] * 20]):
