@@ -15,6 +15,14 @@ from __future__ import annotations
 import ctypes
 import os
 
+# PyTorch brings a HIP runtime of its own, and of two runtimes in a process only
+# the one that is loaded first finds the device: so PyTorch's comes first, in
+# whichever order a program imports the two.
+try:
+    import torch as _torch  # noqa: F401
+except ImportError:
+    pass  # raw device addresses need no PyTorch
+
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_NAME = "libdense_gemm_tile_amd.so"
 LIB_PATH = os.path.join(_PKG_DIR, LIB_NAME)

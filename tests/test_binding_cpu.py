@@ -5,8 +5,8 @@ import ctypes
 
 import pytest
 
-dgt = pytest.importorskip("dense_gemm_tile_amd")
-from dense_gemm_tile_amd import _binding  # noqa: E402
+import dense_gemm_tile_amd as dgt
+from dense_gemm_tile_amd import _binding
 
 A0, B0, Y0 = 0x10000000, 0x20000000, 0x30000000
 
@@ -95,3 +95,14 @@ def test_every_enqueueing_entry_point_of_the_header_is_there():
     layer = names - {"gemm_i8", "gemm_last_error", "gemm_last_path", "gemm_tile_order"}
     assert layer <= {n for n in dir(_binding) if n.startswith("gemm_")}
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_the_package_may_be_imported_first():
+    """PyTorch's HIP runtime is loaded before the library's, whichever the program imports first."""
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", "import dense_gemm_tile_amd, sys; print('torch' in sys.modules); "
+                          "import torch; m = [l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l]; "
+                          "print(len(set(m)))"], capture_output=True, text=True, check=True,
+                         cwd=__file__.rsplit("/tests/", 1)[0])
+    assert out.stdout.split()[0] == "True", out.stdout
