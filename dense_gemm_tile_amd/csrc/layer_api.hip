@@ -105,7 +105,7 @@ bool wide16(const Mat& m) {
 enum LayerKernel : int {
   LK_GENERAL128 = 0, LK_GENERAL64, LK_PP256, LK_PP128, LK_PP128_DEEP,
   LK_SKINNY16, LK_SKINNY16N16, LK_SKINNY32, LK_SKINNY48, LK_SKINNY64, LK_SKINNY64N64,
-  LK_ANY16, LK_ANY32, LK_ANY64, LK_ROWS16, LK_GENERAL64K4,
+  LK_ANY16, LK_ANY32, LK_ANY64, LK_ROWS16, LK_GENERAL64K4, LK_RING128,
   NUM_LAYER_KERNELS
 };
 struct LayerKernelInfo {
@@ -119,7 +119,7 @@ const LayerKernelInfo kLayerKernels[NUM_LAYER_KERNELS] = {
     {"s48x32", 48, 32},     {"s64x32", 64, 32},
     {"s64x64", 64, 64},     {"u16x32", 16, 32},     {"u32x32", 32, 32},
     {"u64x32", 64, 32},     {"r16x32", 16, 32},
-    {"g64x64k4", 64, 64},
+    {"g64x64k4", 64, 64},   {"r128x128", 128, 128},
 };
 
 struct LayerPlan {
@@ -174,6 +174,9 @@ bool layer_direct(const Mat& m, int64_t along) {
 bool kernel_runs(const LayerPlan& pl, int k) {
   if (k == LK_GENERAL128 || k == LK_GENERAL64 || k == LK_GENERAL64K4) return true;
   if (pl.a.K == 0) return false;
+  // Operands stored along K are not staged there.
+  if (k == LK_RING128)
+    return pl.reach && (pl.ta || !pl.tb) && (pl.a.a_direct || pl.ta) && (pl.a.b_direct || !pl.tb);
   if (k == LK_ROWS16) return pl.direct && pl.tb && pl.a.mode == LAYER_ROWS;
   if (k >= LK_ANY16) return pl.reach && !pl.ta && pl.tb && pl.a.mode != LAYER_SUM;
   if (!pl.direct) return false;
@@ -231,10 +234,17 @@ int choose_kernel(const LayerPlan& pl) {
         return a.M <= 32 ? LK_ANY16 : LK_ANY32;
       }
     }
-    // The sum split over wave groups where even 64 x 64 tiles leave CUs idle.
-    if (tiles(LK_GENERAL64) <= 256 && a.K >= 512) return LK_GENERAL64K4;
+    // The sum split over wave groups where 64 x 64 tiles leave CUs idle, or a long
+    // sum dominates (300x5001x3001: 87 us on 64 x 64 tiles, 65 split).
+    const int64_t n64 = tiles(LK_GENERAL64);
+    if ((n64 <= 256 && a.K >= 512) || (n64 <= 512 && a.K >= 2048)) return LK_GENERAL64K4;
     // 64 x 64 tiles where 128 x 128 ones would leave CUs without work.
-    return tiles(LK_GENERAL128) >= 256 ? LK_GENERAL128 : LK_GENERAL64;
+    if (tiles(LK_GENERAL128) < 256) return LK_GENERAL64;
+    // The general kernel transposes operands not stored along K in registers; the
+    // ring reads them transposed from LDS, and pays for staging the others (4096^3,
+    // us: one of the former 336-357 against 246-282, one of the latter 185 against
+    // 209, one of each 104 against 112 at 4000x4001x1023).
+    return kernel_runs(pl, LK_RING128) ? LK_RING128 : LK_GENERAL128;
   }
   if (a.mode == LAYER_ROWS) return choose_grouped(pl);
   const bool split = kernel_runs(pl, LK_SKINNY64N64);
@@ -294,6 +304,7 @@ hipError_t launch_product(const LayerPlan& pl, hipStream_t s) {
     case LK_PP128:
     case LK_PP128_DEEP:
       return launch_layer_pp128(pl.dtype, pl.ta, pl.tb, pl.kernel == LK_PP128_DEEP, pl.a, pl.ntiles, s);
+    case LK_RING128: return launch_layer_ring(pl.dtype, pl.ta, pl.tb, pl.a, pl.ntiles, s);
     case LK_GENERAL128:
     case LK_GENERAL64:
     case LK_GENERAL64K4:
@@ -395,7 +406,9 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
   pl.ta = ta;
   pl.tb = tb;
   pl.reach = layer_reach(ma) && layer_reach(mb);
-  pl.direct = layer_direct(ma, ta ? M : K) && layer_direct(mb, tb ? K : N);
+  a.a_direct = layer_direct(ma, ta ? M : K);
+  a.b_direct = layer_direct(mb, tb ? K : N);
+  pl.direct = a.a_direct && a.b_direct;
   return plan_tiles(pl, dense ? "linear" : "grouped");
 }
 
@@ -456,7 +469,9 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
   pl.ta = true;
   pl.tb = false;
   pl.reach = M > 0 && layer_reach(ma) && layer_reach(mb);
-  pl.direct = M > 0 && layer_direct(ma, N) && layer_direct(mb, K);
+  a.a_direct = M > 0 && layer_direct(ma, N);
+  a.b_direct = M > 0 && layer_direct(mb, K);
+  pl.direct = a.a_direct && a.b_direct;
   return plan_tiles(pl, "grad_weight");
 }
 

@@ -1,5 +1,5 @@
-// The layer operators' product on tiles of up to 64 rows, the sum split over the workgroup's waves: decoding batches, and grids too small
-// for larger tiles.
+// The layer operators' product on tiles of up to 64 rows, the sum split over the
+// workgroup's waves: decoding batches, and grids too small for larger tiles.
 //
 // A workgroup owns 16 MT rows and 16 NT columns; wave w takes slices w, w + KW,
 // ... of 64 and loads their pieces of both operands straight into LDS of its
@@ -7,7 +7,8 @@
 // byte. Consecutive lanes load consecutive bytes (8 rows of 128 bytes of an
 // operand stored along K, whole rows of the tile of B stored [K][N]); loading
 // fragments into registers as layer_skinny.hip does puts neighbouring lanes into
-// different rows, which takes the address units four times as long: MEASURE.
+// different rows, which takes the address units four times as long (48x8192x8192
+// 44 us, 30 here).
 #include "layer_split.h"
 
 namespace dgt {

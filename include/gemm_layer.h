@@ -110,9 +110,11 @@ GEMM_API int gemm_grouped_grad_weight_validate(int64_t G, int64_t M, int64_t N, 
                  const void* D, int64_t ldd, int64_t stride_d, int out_dtype, int accumulate);
 
 /*
- * gemm_act_grad: dZ = dY * act'(Z) (all M x N of `dtype`), and per group the
- * bias gradient db[g][n] = sum over the group's rows of the unrounded dZ, in
- * float32, the rows in an order that does not depend on the run.
+ * gemm_act_grad: dZ = dY * act'(Z) (all M x N of `dtype`: the operand of the
+ * products that follow, dX = dZ W and dW = dZ^T X, which therefore see it rounded
+ * once), and per group the bias gradient db[g][n] = sum over the group's rows of
+ * the unrounded dZ, in float32, the rows in an order that does not depend on the
+ * run.
  *
  * offsets   as in gemm_grouped, or NULL for one group of all M rows (G == 1).
  * Z         not read when act is GEMM_ACT_NONE (may be NULL).

@@ -99,6 +99,33 @@ def test_any_alignment_forced(name):
                 assert f" {name} " in path, path
 
 
+@pytest.mark.parametrize("tA,tB", [(0, 0), (1, 0), (1, 1)])
+def test_staged_ring_forced(tA, tB):
+    """Operands not stored along K with odd widths, pitches and starts; the others aligned."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(21 + 2 * tA + tB)
+    along_k = not tA or tB  # some operand is stored along K: whole pieces of it
+    i = 0
+    with tile("r128x128"):
+        for pad in (0, 1, 2, 5, 8):
+            pads = (pad if tA else 8 * (pad % 2), 8 * (pad % 2) if tB else pad, (0, 3, 8)[i % 3])
+            for M, N in ((1, 1), (128, 128), (125, 131), (259, 391), (7, 300)):
+                for K in (1, 8, 63, 64, 65, 72, 200, 333, 1096):
+                    if along_k and K % 8:
+                        continue
+                    dtype = ("f16", "bf16")[i % 2]
+                    path = linear(gen, M, N, K, dtype, tA, tB, act=ACTS[i % 5], bias=i % 2 == 0, residual=i % 3 == 0,
+                                  keep_z=i % 4 == 1, out_dtype="f32" if i % 3 == 1 else dtype, pads=pads)
+                    assert " r128x128 " in path, path
+                    i += 1
+        if not tA:
+            for i, s in enumerate([[1], [0, 0, 128, 0], [127, 1, 129, 0, 389], [1, 0, 2] * 30]):
+                for N, K in ((129, 72), (7, 704), (128, 128)):
+                    path = grouped(gen, s, N, K, ("f16", "bf16")[i % 2], 0, act=ACTS[i % 5], bias=i % 2 == 0,
+                                   keep_z=i % 4 == 1, spare=(i * 7) % 20, pads=(0, i % 4, i % 3))
+                    assert " r128x128 " in path, path
+
+
 def test_any_alignment_of_the_first_element():
     """Operands that start 2, 4, 6 ... bytes into an allocation, odd pitches."""
     need_gpu()
@@ -122,11 +149,11 @@ def test_any_alignment_of_the_first_element():
                     close(y, wy, ty, dgt.gemm_last_path())
 
 
-@pytest.mark.parametrize("name", [*TILES, *ALL])
+@pytest.mark.parametrize("name", [*TILES, *ALL, "r128x128"])
 def test_grad_weight_forced(name):
     need_gpu()
     import dense_gemm_tile_amd as dgt
-    bm, bn = {**TILES, **SKINNY}[name]
+    bm, bn = {**TILES, **SKINNY, "r128x128": (125, 131)}[name]
     gen = torch.Generator().manual_seed(bm + bn)
     with tile(name):
         for i, sizes in enumerate([[1], [0], [64, 0, 65], [200, 1, 0, 63, 330], [3, 0] * 20]):
