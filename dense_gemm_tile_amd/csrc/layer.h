@@ -29,14 +29,12 @@ struct LayerArgs {
   int M, N, K;       // by rows: M counts all rows; by sum: K does
   int G, mode, act;
   int out32;         // Y (and R) hold float32, else the operands' 16-bit type
-  int vec;           // LayerVec: what allows 16-byte accesses of 8 columns
+  int whole8;        // N is a multiple of 8
   int a_vw, b_vw;    // staging vector widths of A and B (general kernel)
   int a_direct, b_direct;  // A, B in whole 16-byte pieces (ring kernel)
   int tiles_m, tiles_n;  // of one group (by sum, dense); by rows: tiles_m is not used
   int group_m;
 };
-// VEC_ALL: everything that the call has, and N is a multiple of 8.
-enum LayerVec : int { VEC_BIAS = 1, VEC_R = 2, VEC_Y = 4, VEC_Z = 8, VEC_ALL = 16 };
 
 // One group's product and one tile of it. Pointers and sizes are uniform.
 struct LayerTile {
@@ -334,32 +332,50 @@ __device__ __forceinline__ void layer_act8(float (&f)[8], int act) {
 
 // ------------------------------------------------------------------ epilogue --
 // Row-wise accesses of up to 8 columns of a 16-bit or float32 matrix; nv of
-// the 8 lie inside it. wide: 16-byte accesses are allowed.
+// the 8 lie inside it. Whole pieces go 16 bytes at a time at whatever address
+// they have, which this target's memory unit serves: 4096 x 4096 activation
+// gradients at an odd pitch 73 us element by element, 32 so; a product of
+// 8192x2047x1024 with bias and GELU 58, 42 so.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+typedef unsigned u32_at2 __attribute__((aligned(2)));
 template <class Tag>
-__device__ __forceinline__ void layer_load8_16(const char* p, bool wide, int nv, float (&f)[8]) {
-  if (wide && nv == 8) {
-    layer_unpack8<Tag>(*reinterpret_cast<const u32x4*>(p), f);
-  } else {
-    const unsigned short* s = reinterpret_cast<const unsigned short*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e < nv ? layer_f32(Tag{}, s[e]) : 0.0f;
+__device__ __forceinline__ void layer_load8_16(const char* p, int nv, float (&f)[8]) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (nv == 8) {
+    v = *reinterpret_cast<const u32x4_at2*>(p);
+  } else {  // 4, 2 and 1 columns: shorter code than one after the other
+    u32x2 four = {0u, 0u};
+    unsigned two = 0u, one = 0u;
+    if (nv & 4) four = *reinterpret_cast<const u32x2_at2*>(p);
+    if (nv & 2) two = *reinterpret_cast<const u32_at2*>(p + (nv & 4) * 2);
+    if (nv & 1) one = *reinterpret_cast<const unsigned short*>(p + (nv & 6) * 2);
+    const unsigned x = nv & 2 ? two : one, y = nv & 2 ? one : 0u;
+    v.x = nv & 4 ? four.x : x;
+    v.y = nv & 4 ? four.y : y;
+    v.z = nv & 4 ? x : 0u;
+    v.w = nv & 4 ? y : 0u;
   }
+  layer_unpack8<Tag>(v, f);
 }
 template <class Tag>
-__device__ __forceinline__ void layer_store8_16(char* p, bool wide, int nv, const float (&f)[8]) {
-  if (wide && nv == 8) {
-    *reinterpret_cast<u32x4*>(p) = layer_pack8<Tag>(f);
+__device__ __forceinline__ void layer_store8_16(char* p, int nv, const float (&f)[8]) {
+  const u32x4 v = layer_pack8<Tag>(f);
+  if (nv == 8) {
+    *reinterpret_cast<u32x4_at2*>(p) = v;
   } else {
-    unsigned short* s = reinterpret_cast<unsigned short*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < nv) s[e] = layer_16(Tag{}, f[e]);
+    const unsigned x = nv & 4 ? v.z : v.x, y = nv & 4 ? v.w : v.y;
+    if (nv & 4) *reinterpret_cast<u32x2_at2*>(p) = u32x2{v.x, v.y};
+    if (nv & 2) *reinterpret_cast<u32_at2*>(p + (nv & 4) * 2) = x;
+    if (nv & 1) *reinterpret_cast<unsigned short*>(p + (nv & 6) * 2) = (unsigned short)(nv & 2 ? y : x);
   }
 }
-__device__ __forceinline__ void layer_load8_32(const char* p, bool wide, int nv, float (&f)[8]) {
+__device__ __forceinline__ void layer_load8_32(const char* p, int nv, float (&f)[8]) {
   const float* s = reinterpret_cast<const float*>(p);
-  if (wide && nv == 8) {
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(s), hi = *reinterpret_cast<const f32x4*>(s + 4);
+  if (nv == 8) {
+    const u32x4_at4* v = reinterpret_cast<const u32x4_at4*>(p);
+    const f32x4 lo = __builtin_bit_cast(f32x4, u32x4(v[0])), hi = __builtin_bit_cast(f32x4, u32x4(v[1]));
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = lo[e], f[e + 4] = hi[e];
   } else {
@@ -367,11 +383,12 @@ __device__ __forceinline__ void layer_load8_32(const char* p, bool wide, int nv,
     for (int e = 0; e < 8; ++e) f[e] = e < nv ? s[e] : 0.0f;
   }
 }
-__device__ __forceinline__ void layer_store8_32(char* p, bool wide, int nv, const float (&f)[8]) {
+__device__ __forceinline__ void layer_store8_32(char* p, int nv, const float (&f)[8]) {
   float* s = reinterpret_cast<float*>(p);
-  if (wide && nv == 8) {
-    *reinterpret_cast<f32x4*>(s) = f32x4{f[0], f[1], f[2], f[3]};
-    *reinterpret_cast<f32x4*>(s + 4) = f32x4{f[4], f[5], f[6], f[7]};
+  if (nv == 8) {
+    u32x4_at4* v = reinterpret_cast<u32x4_at4*>(p);
+    v[0] = __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]});
+    v[1] = __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]});
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -385,17 +402,17 @@ __device__ __forceinline__ void layer_finish8(const LayerArgs& p, const LayerTil
                                               int nv, const float (&bias)[8], float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] += bias[e];
-  if (q.Z) layer_store8_16<Tag>(q.Z + ((int64_t)r * p.ldz + c) * 2, p.vec & VEC_Z, nv, x);
+  if (q.Z) layer_store8_16<Tag>(q.Z + ((int64_t)r * p.ldz + c) * 2, nv, x);
   layer_act8(x, p.act);
   if (q.R) {
     float rv[8];
-    if (p.out32) layer_load8_32(q.R + ((int64_t)r * p.ldr + c) * 4, p.vec & VEC_R, nv, rv);
-    else layer_load8_16<Tag>(q.R + ((int64_t)r * p.ldr + c) * 2, p.vec & VEC_R, nv, rv);
+    if (p.out32) layer_load8_32(q.R + ((int64_t)r * p.ldr + c) * 4, nv, rv);
+    else layer_load8_16<Tag>(q.R + ((int64_t)r * p.ldr + c) * 2, nv, rv);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] += rv[e];
   }
-  if (p.out32) layer_store8_32(q.Y + ((int64_t)r * p.ldy + c) * 4, p.vec & VEC_Y, nv, x);
-  else layer_store8_16<Tag>(q.Y + ((int64_t)r * p.ldy + c) * 2, p.vec & VEC_Y, nv, x);
+  if (p.out32) layer_store8_32(q.Y + ((int64_t)r * p.ldy + c) * 4, nv, x);
+  else layer_store8_16<Tag>(q.Y + ((int64_t)r * p.ldy + c) * 2, nv, x);
 }
 
 // The epilogue of one wave's TM x TN atoms, whose first output is (r0, c0).
@@ -418,13 +435,6 @@ struct LayerEpi {
   static constexpr int LPR = W / 8, RPP = 64 / LPR;       // lanes a row, rows a pass
   static constexpr int PASSES = BATCH / RPP;
   static constexpr int GROUP = PASSES < 4 ? PASSES : 4;   // passes unrolled
-  // Outputs that are not 16-byte pieces go one column a lane, so that the lanes'
-  // accesses are consecutive at any alignment, from the waves of 64 x 32 outputs
-  // (8192x1001x1024: 43 us with 8 columns a lane, 37 so). The others keep 8
-  // columns a lane: on 64 x 64 outputs the general kernel takes 16 us instead of
-  // 28 for 2000x701x300, and the masked 256x256 kernel, compiled with the loop
-  // over columns, spends 28 us more on every tile, taken or not.
-  static constexpr bool COLUMNS = ROWS == 64 && W == 32;
   static_assert(W % 8 == 0 && 64 % LPR == 0 && BATCH % RPP == 0 && PASSES % GROUP == 0 &&
                     ROWS % BATCH == 0 && BATCH % At::M == 0,
                 "whole passes");
@@ -455,8 +465,8 @@ __device__ __forceinline__ void layer_group_r(LayerGroupR<GROUP>& v, const Layer
 #pragma unroll
   for (int s = 0; s < GROUP; ++s, at += step) {
     if (r + s * RPP >= q.M) continue;
-    v.lo[s] = *reinterpret_cast<const u32x4*>(at);
-    if (p.out32) v.hi[s] = *reinterpret_cast<const u32x4*>(at + 16);
+    v.lo[s] = *reinterpret_cast<const u32x4_at2*>(at);
+    if (p.out32) v.hi[s] = *reinterpret_cast<const u32x4_at4*>(at + 16);
   }
 }
 // The passes of a batch whose first row is r, all of its columns in whole
@@ -486,7 +496,7 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] += bias[e];
       if (row < q.M && c < q.N) {
-        if (q.Z) *reinterpret_cast<u32x4*>(z) = layer_pack8<Tag>(x);
+        if (q.Z) *reinterpret_cast<u32x4_at2*>(z) = layer_pack8<Tag>(x);
         layer_act8_of<ACT>(x);
         if (q.R) {
           float f[8];
@@ -500,50 +510,13 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] += f[e];
         }
-        if (p.out32) layer_store8_32(y, true, 8, x);
-        else *reinterpret_cast<u32x4*>(y) = layer_pack8<Tag>(x);
+        if (p.out32) layer_store8_32(y, 8, x);
+        else *reinterpret_cast<u32x4_at2*>(y) = layer_pack8<Tag>(x);
       }
       y += ystep;
       z += zstep;
     }
     res = next;
-  }
-}
-
-// The same where some rows are not 16-byte pieces: one column a lane.
-template <class E, class Tag>
-__device__ __forceinline__ void layer_columns(const LayerArgs& p, const LayerTile& q, int r0, int c0,
-                                              int lane, const float* lds) {
-  constexpr int RPS = 64 / E::W, STEPS = E::BATCH / RPS, U = 4;  // rows a step; steps at once
-  static_assert(E::W <= 64 && STEPS % U == 0, "whole steps");
-  const int col = lane % E::W, c = c0 + col, rl = lane / E::W;
-  if (c >= q.N) return;
-  auto load16 = [&](const char* at) { return layer_f32(Tag{}, *reinterpret_cast<const unsigned short*>(at)); };
-  const float bias = q.bias ? load16(q.bias + (int64_t)c * 2) : 0.0f;
-#pragma unroll 1
-  for (int s = 0; s < STEPS; s += U) {
-    float x[U], res[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int in = (s + u) * RPS + rl, row = r0 + in;
-      x[u] = lds[in * E::P + col] + bias;
-      res[u] = 0.0f;
-      if (q.R && row < q.M) {
-        const int64_t at = (int64_t)row * p.ldr + c;
-        res[u] = p.out32 ? reinterpret_cast<const float*>(q.R)[at] : load16(q.R + at * 2);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = r0 + (s + u) * RPS + rl;
-      if (row >= q.M) continue;
-      if (q.Z)
-        reinterpret_cast<unsigned short*>(q.Z)[(int64_t)row * p.ldz + c] = layer_16(Tag{}, x[u]);
-      const float y = layer_act1(x[u], p.act) + res[u];
-      const int64_t at = (int64_t)row * p.ldy + c;
-      if (p.out32) reinterpret_cast<float*>(q.Y)[at] = y;
-      else reinterpret_cast<unsigned short*>(q.Y)[at] = layer_16(Tag{}, y);
-    }
   }
 }
 
@@ -560,15 +533,15 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
 #pragma unroll
   for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
   if (q.bias && nv > 0) {
-    if (p.vec & VEC_ALL) layer_unpack8<Tag>(*reinterpret_cast<const u32x4*>(q.bias + (int64_t)c * 2), bias);
-    else layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
+    if (p.whole8) layer_unpack8<Tag>(*reinterpret_cast<const u32x4_at2*>(q.bias + (int64_t)c * 2), bias);
+    else layer_load8_16<Tag>(q.bias + (int64_t)c * 2, nv, bias);
   }
 #pragma unroll
   for (int b = 0; b < C::TM / AR; ++b) {
     const int r = r0 + b * E::BATCH;  // (uniform) the batch's first row
     if (r >= q.M) break;
     LayerGroupR<E::GROUP> res;
-    if (p.vec & VEC_ALL) layer_group_r<E::GROUP, E::RPP>(res, p, q, r + rl, c);
+    if (p.whole8) layer_group_r<E::GROUP, E::RPP>(res, p, q, r + rl, c);
 #pragma unroll
     for (int i = 0; i < AR; ++i)
 #pragma unroll
@@ -579,7 +552,7 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
               acc[b * AR + i][j][v];
     layer_wave_order();
     const float* const from = lds + rl * P + cl;
-    if (p.vec & VEC_ALL) {
+    if (p.whole8) {
       switch (p.act) {
         case ACT_RELU: layer_passes<E, Tag, ACT_RELU>(p, q, r + rl, c, from, bias, res); break;
         case ACT_GELU: layer_passes<E, Tag, ACT_GELU>(p, q, r + rl, c, from, bias, res); break;
@@ -588,17 +561,13 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
         default: layer_passes<E, Tag, ACT_NONE>(p, q, r + rl, c, from, bias, res); break;
       }
     } else {
-      if constexpr (E::COLUMNS) {
-        layer_columns<E, Tag>(p, q, r, c0, lane, lds);
-      } else {
 #pragma unroll 1
-        for (int s = 0; s < E::PASSES; ++s) {
-          const int row = r + s * E::RPP + rl;
-          float x[8];
+      for (int s = 0; s < E::PASSES; ++s) {
+        const int row = r + s * E::RPP + rl;
+        float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = from[s * E::RPP * P + e];
-          if (row < q.M && nv > 0) layer_finish8<Tag>(p, q, row, c, nv, bias, x);
-        }
+        for (int e = 0; e < 8; ++e) x[e] = from[s * E::RPP * P + e];
+        if (row < q.M && nv > 0) layer_finish8<Tag>(p, q, row, c, nv, bias, x);
       }
     }
     layer_wave_order();

@@ -290,8 +290,7 @@ int plan_tiles(LayerPlan& pl, const char* op) {
   a.group_m = 8;
   pl.ntiles = (int)n;
   static const char* const ops[4] = {"NN", "NT", "TN", "TT"};
-  const int need = (a.bias ? VEC_BIAS : 0) | (a.R ? VEC_R : 0) | VEC_Y | (a.Z ? VEC_Z : 0);
-  if ((a.vec & need) == need && a.N % 8 == 0) a.vec |= VEC_ALL;
+  a.whole8 = a.N % 8 == 0;
   g_layer_path = {op, ops[pl.ta * 2 + pl.tb], pl.kernel, a.act, a.bias != nullptr,
                   a.R != nullptr, a.Z != nullptr, a.out32 != 0};
   set_path_writer(write_layer_path);
@@ -396,8 +395,6 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
   a.mode = dense ? LAYER_DENSE : LAYER_ROWS;
   a.act = act;
   a.out32 = osz == 4;
-  a.vec = (wide16(mbias) ? VEC_BIAS : 0) | (wide16(mr) ? VEC_R : 0) | (wide16(my) ? VEC_Y : 0) |
-          (wide16(mz) ? VEC_Z : 0);
   a.a_vw = vector_width16(A, lda);
   a.b_vw = vector_width16(B, ldb);
   if (g > 1)
@@ -462,7 +459,6 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
   a.G = (int)G;
   a.mode = LAYER_SUM;
   a.out32 = osz == 4;
-  a.vec = wide16(md) ? VEC_Y | VEC_R : 0;
   a.a_vw = vector_width16(A, lda);
   a.b_vw = vector_width16(B, ldb);
   pl.dtype = dtype;
@@ -707,7 +703,6 @@ int gemm_act_grad(int64_t G, int64_t M, int64_t N, int dtype, int act, const int
     a.N = (int)N;
     a.act = act;
     a.rows = act_grad_rows(M, N);
-    a.wide = wide16(my) && (!Z || wide16(mz)) && (!dZ || wide16(md));
     set_path(std::string("act_grad act=") + kActNames[act] + (dZ ? " dz" : "") + (db ? " db" : ""));
     return launched(launch_act_grad(dtype, a, static_cast<hipStream_t>(stream)));
   });

@@ -20,15 +20,19 @@ struct ActGradArgs {
   int64_t lddy, ldz, lddz;
   int G, M, N, act;
   int rows;            // act_grad_rows(M, N)
-  int wide;            // rows of all three allow 16-byte accesses
 };
 // Rows that one wave sums by itself (a partial sum is kept for each): 32, fewer
 // where that would leave less than 16 waves to a CU. At 4096 x 4096 with GELU,
-// 32 rows a wave (4 waves a CU) take 51 us, 4 rows a wave (32) 28 us.
+// 32 rows a wave (4 waves a CU) take 51 us, 4 rows a wave (32) 28 us. Fewer
+// than 4 where waves are fewer than SIMDs, as a row then costs its arithmetic's
+// latency (76 x 2622: 12 us, 7 so), but not for more than 256 partial sums a
+// column, whose joining costs as much (613 x 1536: 9 us, 12 so).
 inline int act_grad_rows(int64_t m, int64_t n) {
   const int64_t blocks = (n + 511) / 512;
   int rows = 32;
   while (rows > 4 && (m + rows - 1) / rows * blocks < 16 * 256) rows /= 2;
+  while (rows > 1 && (m + rows - 1) / rows <= 128 && (m + rows - 1) / rows * blocks < 4 * 256)
+    rows /= 2;
   return rows;
 }
 inline unsigned act_grad_column_blocks(int64_t n) { return (unsigned)((n + 511) / 512); }

@@ -17,6 +17,7 @@ namespace {
 // number for each run (each next run has the next b or the next g), so the
 // sums go to row b + g of the workspace. A second kernel adds each group's
 // runs in order.
+constexpr int kActRows = 4;
 template <class Tag, int ACT>
 __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -51,30 +52,30 @@ __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p
     }
     if (g >= p.G) break;  // rows of no group
     const int stop = end < r1 ? end : r1;
-    // Rows in batches whose loads are all requested before the first store
-    // (dZ may be dY or Z, so the compiler would not move them across).
-    auto batch = [&](auto count) {
-      constexpr int R = count.value;
-      float d[R][8], z[R][8];
+    // kActRows rows at once, all of their loads requested before the first store
+    // (dZ may be dY or Z, so the compiler would not move them across). Not more:
+    // a short call's time is the fetching of its instructions.
+    for (; r < stop; r += kActRows) {
+      float d[kActRows][8], z[kActRows][8];
 #pragma unroll
-      for (int u = 0; u < R; ++u) {
-        layer_load8_16<Tag>(dY + ((int64_t)(r + u) * p.lddy + c) * 2, p.wide, nv, d[u]);
+      for (int u = 0; u < kActRows; ++u) {
+        if (r + u >= stop) break;
+        layer_load8_16<Tag>(dY + ((int64_t)(r + u) * p.lddy + c) * 2, nv, d[u]);
         if constexpr (ACT != ACT_NONE)
-          layer_load8_16<Tag>(Z + ((int64_t)(r + u) * p.ldz + c) * 2, p.wide, nv, z[u]);
+          layer_load8_16<Tag>(Z + ((int64_t)(r + u) * p.ldz + c) * 2, nv, z[u]);
       }
 #pragma unroll
-      for (int u = 0; u < R; ++u) {
+      for (int u = 0; u < kActRows; ++u) {
+        if (r + u >= stop) break;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if constexpr (ACT != ACT_NONE) d[u][e] *= layer_slope<ACT>(z[u][e]);
           sum[e] += d[u][e];
         }
-        if (dZ) layer_store8_16<Tag>(dZ + ((int64_t)(r + u) * p.lddz + c) * 2, p.wide, nv, d[u]);
+        if (dZ) layer_store8_16<Tag>(dZ + ((int64_t)(r + u) * p.lddz + c) * 2, nv, d[u]);
       }
-      r += R;
-    };
-    while (r + 4 <= stop) batch(LayerConst<4>{});
-    while (r < stop) batch(LayerConst<1>{});
+    }
+    r = stop;
     if (p.db) {
       float* out = p.part + (int64_t)(b + g) * p.N + c;
 #pragma unroll

@@ -80,7 +80,7 @@ struct SplitSum {
           bias[e] = 0.0f;
           v[e] = outs[rr * PITCH + cl + e];
         }
-        if (q.bias) layer_load8_16<Tag>(q.bias + (int64_t)c * 2, p.vec & VEC_BIAS, nv, bias);
+        if (q.bias) layer_load8_16<Tag>(q.bias + (int64_t)c * 2, nv, bias);
         layer_finish8<Tag>(p, q, r, c, nv, bias, v);
       }
     }
