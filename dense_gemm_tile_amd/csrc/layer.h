@@ -334,7 +334,7 @@ __device__ __forceinline__ void layer_act8(float (&f)[8], int act) {
 // Row-wise accesses of up to 8 columns of a 16-bit or float32 matrix; nv of
 // the 8 lie inside it. Whole pieces go 16 bytes at a time at whatever address
 // they have, which this target's memory unit serves: 4096 x 4096 activation
-// gradients at an odd pitch 73 us element by element, 32 so; a product of
+// gradients at an odd pitch 73 us element by element, 31 so; a product of
 // 8192x2047x1024 with bias and GELU 58, 42 so.
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));

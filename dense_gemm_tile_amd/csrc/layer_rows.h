@@ -23,7 +23,7 @@ struct ActGradArgs {
 };
 // Rows that one wave sums by itself (a partial sum is kept for each): 32, fewer
 // where that would leave less than 16 waves to a CU. At 4096 x 4096 with GELU,
-// 32 rows a wave (4 waves a CU) take 51 us, 4 rows a wave (32) 28 us. Fewer
+// 32 rows a wave (4 waves a CU) take 51 us, 4 rows a wave (32) 26 us. Fewer
 // than 4 where waves are fewer than SIMDs, as a row then costs its arithmetic's
 // latency (76 x 2622: 12 us, 7 so), but not for more than 256 partial sums a
 // column, whose joining costs as much (613 x 1536: 9 us, 12 so).
