@@ -311,15 +311,6 @@ __device__ __forceinline__ void layer_act8_of(float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = layer_act<ACT>(f[e]);
 }
-__device__ __forceinline__ float layer_act1(float z, int act) {
-  switch (act) {  // uniform over the launch
-    case ACT_RELU: return layer_act<ACT_RELU>(z);
-    case ACT_GELU: return layer_act<ACT_GELU>(z);
-    case ACT_GELU_ERF: return layer_act<ACT_GELU_ERF>(z);
-    case ACT_SILU: return layer_act<ACT_SILU>(z);
-    default: return z;
-  }
-}
 __device__ __forceinline__ void layer_act8(float (&f)[8], int act) {
   switch (act) {  // uniform over the launch
     case ACT_RELU: layer_act8_of<ACT_RELU>(f); break;

@@ -67,6 +67,27 @@ def test_act_grad_groups(sizes):
         act_grad(gen, 0, N, "f16", "none", sizes=sizes, spare=spare, want=("db",))
 
 
+def test_act_grad_row_ends_and_starts():
+    """Every number of columns past the last whole piece, at pitches that put rows at any 2-byte
+    address; padding stays as it was."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(3)
+    for i in range(16):
+        for base in (0, 512):
+            N = base + i + 1
+            act_grad(gen, 9, N, ("f16", "bf16")[i % 2], ACTS[i % 5], pad=i % 4)
+            act_grad(gen, 9, N, ("bf16", "f16")[i % 2], ACTS[(i + 1) % 5], pad=(i + 1) % 3, inplace=True)
+
+
+@pytest.mark.parametrize("M,N", [(128, 1030), (300, 1030), (520, 4099), (5000, 2050), (20000, 2056)])
+def test_act_grad_rows_of_a_wave(M, N):
+    """Sizes at which a wave takes 1, 2, 4 and more rows, with groups that end inside its rows."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(4)
+    act_grad(gen, M, N, "bf16", "gelu", pad=1)
+    act_grad(gen, 0, N, "f16", "silu", sizes=[M // 3, 0, 1, M // 2 - 1, 5], spare=7, inplace=True)
+
+
 def test_act_grad_no_rows_gives_zero_sums():
     need_gpu()
     import dense_gemm_tile_amd as dgt
