@@ -3,8 +3,10 @@
 // whole 16-byte pieces. Dense, by rows and by sum; pieces outside a group's
 // rows, columns or sum read as zeros.
 //
-// One tile a workgroup: the grid may be an upper bound (groups held on the
-// GPU), and a workgroup past the last tile ends at once.
+// By rows, and where pieces are masked one by one, a workgroup has one tile: by
+// rows the grid is an upper bound (groups held on the GPU), and a workgroup past
+// the last tile ends at once. Dense and by sum with the record count as the mask
+// (PP_RECORDS), 256 workgroups walk the tiles of a larger call.
 #include "gemm_mfma_pingpong.h"
 #include "layer.h"
 
@@ -63,7 +65,11 @@ __global__ void __launch_bounds__(PingPongCfg::THREADS) layer_pp256_kernel(const
     layer_store<C, Tag>(acc, p, q, q.m0 + wm * C::WTM, q.n0 + wn * C::WTN, lane,
                         reinterpret_cast<float*>(smem + wave * layer_lds_bytes<C>()));
     if constexpr (!WALK) break;
-    pp_barrier();  // the next tile's loads overwrite the epilogue's rows
+    // The next tile's loads overwrite the epilogue's rows, those of other waves
+    // too, so every wave's own LDS operations end here. (A wave whose columns lie
+    // past N writes rows that it never uses: nothing else waits for them.)
+    pp_wait_lgkm0();
+    pp_barrier();
   }
 }
 
