@@ -71,23 +71,30 @@ __device__ __forceinline__ void layer_group(const int* offsets, int g, int rows,
 // of one group of 64; a scan over the wave places them. Every wave of a
 // workgroup does this for itself: the offsets stay in its caches, and no LDS
 // has to be kept for it.
+//
+// Offsets that decrease can make groups overlap and their tiles add up past 32
+// bits (65535 groups of up to 2^27 tiles). Sums then wrap, as unsigned numbers,
+// and a tile finds some group below G or none.
 template <int BM>
 struct LayerRows {
-  __device__ static inline int tiles_of(const LayerArgs& p, int g, int& first, int& count) {
-    if (g >= p.G) return first = count = 0;
+  __device__ static inline unsigned tiles_of(const LayerArgs& p, int g, int& first, int& count) {
+    if (g >= p.G) {
+      first = count = 0;
+      return 0u;
+    }
     layer_group(p.offsets, g, p.M, first, count);
-    return (count + BM - 1) / BM;
+    return (unsigned)(count + BM - 1) / BM;
   }
-  __device__ static inline int wave_scan(int v, int lane) {  // inclusive
+  __device__ static inline unsigned wave_scan(unsigned v, int lane) {  // inclusive
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(v, d, 64);
+      const unsigned o = __shfl_up(v, d, 64);
       if (lane >= d) v += o;
     }
     return v;
   }
-  __device__ static inline int total(const LayerArgs& p, int lane) {
-    int sum = 0;
+  __device__ static inline unsigned total(const LayerArgs& p, int lane) {
+    unsigned sum = 0;
     for (int g0 = 0; g0 < p.G; g0 += 64) {
       int f, c;
       sum += tiles_of(p, g0 + lane, f, c);
@@ -100,20 +107,22 @@ struct LayerRows {
   // group, its rows, and the tile's index within the group.
   __device__ static inline int find(const LayerArgs& p, int t, int tiles_n, int lane, int& first,
                                     int& count, int& in) {
-    int base = 0;
+    int64_t base = 0;
     for (int g0 = 0; g0 < p.G; g0 += 64) {
       int f, c;
-      const int n = tiles_of(p, g0 + lane, f, c);
-      const int incl = wave_scan(n, lane);
-      const int chunk = __builtin_amdgcn_readlane(incl, 63);
+      const unsigned n = tiles_of(p, g0 + lane, f, c);
+      const unsigned incl = wave_scan(n, lane);
+      const unsigned chunk = __builtin_amdgcn_readlane(incl, 63);
       if (t < (base + chunk) * tiles_n) {
-        // the first lane whose inclusive count lies past the tile
-        const uint64_t past = __ballot((int64_t)(base + incl) * tiles_n > t);
+        // The first lane whose inclusive count lies past the tile: lane 63's does.
+        // Lanes past the last group count what the last group's lane does, so it
+        // is a group's lane.
+        const uint64_t past = __ballot((base + incl) * tiles_n > t);
         const int src = __builtin_ctzll(past);
         first = __builtin_amdgcn_readlane(f, src);
         count = __builtin_amdgcn_readlane(c, src);
-        const int before = base + __builtin_amdgcn_readlane(incl - n, src);
-        in = t - before * tiles_n;
+        const int64_t at = t - (base + (unsigned)__builtin_amdgcn_readlane(incl - n, src)) * tiles_n;
+        in = at < 0 ? -1 : (int)at;
         return g0 + src;
       }
       base += chunk;
@@ -126,7 +135,7 @@ struct LayerRows {
 // Tiles of the whole call (an exact count, uniform).
 template <int MODE, int BM>
 __device__ inline int layer_tiles(const LayerArgs& p, int lane) {
-  if constexpr (MODE == LAYER_ROWS) return LayerRows<BM>::total(p, lane) * p.tiles_n;
+  if constexpr (MODE == LAYER_ROWS) return (int)(LayerRows<BM>::total(p, lane) * (unsigned)p.tiles_n);
   return p.tiles_m * p.tiles_n * (MODE == LAYER_SUM ? p.G : 1);
 }
 
