@@ -110,16 +110,16 @@ enum LayerKernel : int {
 };
 struct LayerKernelInfo {
   const char* name;
-  int bm, bn;
+  int bm, bn, threads;
 };
 const LayerKernelInfo kLayerKernels[NUM_LAYER_KERNELS] = {
-    {"g128x128", 128, 128}, {"g64x64", 64, 64},     {"pp256x256", 256, 256},
-    {"pp128x128", 128, 128}, {"pp128x128deep", 128, 128},
-    {"s16x32", 16, 32},     {"s16x16", 16, 16},     {"s32x32", 32, 32},
-    {"s48x32", 48, 32},     {"s64x32", 64, 32},
-    {"s64x64", 64, 64},     {"u16x32", 16, 32},     {"u32x32", 32, 32},
-    {"u64x32", 64, 32},     {"r16x32", 16, 32},
-    {"g64x64k4", 64, 64},   {"r128x128", 128, 128},
+    {"g128x128", 128, 128, 256}, {"g64x64", 64, 64, 256}, {"pp256x256", 256, 256, 512},
+    {"pp128x128", 128, 128, 512}, {"pp128x128deep", 128, 128, 512},
+    {"s16x32", 16, 32, 512}, {"s16x16", 16, 16, 512}, {"s32x32", 32, 32, 512},
+    {"s48x32", 48, 32, 512}, {"s64x32", 64, 32, 256},
+    {"s64x64", 64, 64, 256}, {"u16x32", 16, 32, 512}, {"u32x32", 32, 32, 512},
+    {"u64x32", 64, 32, 512}, {"r16x32", 16, 32, 512},
+    {"g64x64k4", 64, 64, 1024}, {"r128x128", 128, 128, 256},
 };
 
 struct LayerPlan {
@@ -284,7 +284,9 @@ int plan_tiles(LayerPlan& pl, const char* op) {
   }
   const LayerKernelInfo& k = kLayerKernels[pl.kernel];
   const int64_t n = count_tiles(a, k);
-  if (n > 0x7fffffff) return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles for one launch");
+  // (A launch holds less than 2^32 threads.)
+  if (n > ((int64_t{1} << 32) - 1) / k.threads)
+    return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles for one launch");
   a.tiles_m = (a.M + k.bm - 1) / k.bm;
   a.tiles_n = (a.N + k.bn - 1) / k.bn;
   a.group_m = 8;
@@ -687,7 +689,8 @@ int gemm_act_grad(int64_t G, int64_t M, int64_t N, int dtype, int act, const int
     CHECK(check_apart(md, mb));
     CHECK(check_apart(md, mw));
     CHECK(check_apart(mb, mw));
-    CHECK(check_span(act_grad_column_blocks(N)));
+    if (act_grad_waves(M, N) > 0x7ffffff0)
+      return fail(GEMM_ERR_UNSUPPORTED, "too many pieces of rows for one launch");
     ActGradArgs a{};
     a.offsets = offsets;
     a.dY = dY;

@@ -7,6 +7,15 @@
 
 namespace dgt {
 
+// n workgroups as a grid. A launch holds less than 2^32 threads along a
+// dimension, so further workgroups go along z, the last of them in part past n
+// (layer_block() in layer_rows.hip counts them).
+inline dim3 layer_grid(int64_t n, unsigned threads, unsigned y = 1) {
+  const int64_t most = ((int64_t{1} << 32) - 1) / threads;
+  const int64_t z = (n + most - 1) / most;
+  return dim3((unsigned)((n + z - 1) / z), y, (unsigned)z);
+}
+
 // Element types of rows.
 enum RowType : int { ROW_F16 = 0, ROW_BF16 = 1, ROW_F32 = 2 };
 
@@ -35,7 +44,11 @@ inline int act_grad_rows(int64_t m, int64_t n) {
     rows /= 2;
   return rows;
 }
-inline unsigned act_grad_column_blocks(int64_t n) { return (unsigned)((n + 511) / 512); }
+// Waves that a call is cut into.
+inline int64_t act_grad_waves(int64_t m, int64_t n) {
+  const int rows = act_grad_rows(m, n);
+  return (m + rows - 1) / rows * ((n + 511) / 512);
+}
 hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s);
 
 struct RouteArgs {

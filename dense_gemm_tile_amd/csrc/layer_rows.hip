@@ -9,6 +9,9 @@ namespace dgt {
 
 namespace {
 
+// This workgroup's index in a layer_grid().
+__device__ __forceinline__ unsigned layer_block() { return blockIdx.z * gridDim.x + blockIdx.x; }
+
 // ------------------------------------------------- activation and bias grads --
 // dZ = dY * act'(Z), and sums of dZ over rows before it is rounded. A wave
 // takes p.rows rows of 512 columns (8 a lane) and keeps 8 float32 sums;
@@ -23,12 +26,12 @@ template <class Tag, int ACT>
 __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int blocks = (p.N + 511) / 512;  // of columns
-  const int id = blockIdx.x * 4 + w;
+  const unsigned id = layer_block() * 4 + w;
   const int b = id / blocks;
-  const int c = (id - b * blocks) * 512 + lane * 8;
+  const int c = (id - (unsigned)b * blocks) * 512 + lane * 8;
   const int nv = p.N - c >= 8 ? 8 : p.N - c;
+  if ((int64_t)b * p.rows >= p.M || nv <= 0) return;
   const int r0 = b * p.rows, r1 = r0 + p.rows < p.M ? r0 + p.rows : p.M;
-  if (r0 >= r1 || nv <= 0) return;
   // The group of the first row: the last one that starts at or before it.
   int g = 0, lo = 0, end = p.M;
   if (p.offsets) {
@@ -96,7 +99,7 @@ constexpr int kSumWaves = 16;
 __global__ void __launch_bounds__(64 * kSumWaves) layer_bias_sum_kernel(const ActGradArgs p) {
   __shared__ float x[kSumWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int g = blockIdx.y, n = blockIdx.x * 64 + lane;
+  const int g = blockIdx.y, n = layer_block() * 64 + lane;
   int first = 0, count = p.M;
   if (p.offsets) layer_group(p.offsets, g, p.M, first, count);
   float s = 0.0f;
@@ -158,8 +161,8 @@ template <int PIECE>
 __global__ void __launch_bounds__(256) layer_dispatch_kernel(const DispatchArgs p) {
   using V = typename RowPiece<PIECE>::type;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + w;
-  if (t >= p.T) return;
+  const unsigned t = layer_block() * 4 + w;
+  if (t >= (unsigned)p.T) return;
   const int64_t at = ((int64_t)blockIdx.y * kDispatchSpan * 64 + lane) * PIECE;
   const char* src = p.X + (int64_t)t * p.ldx + at;
   V v[kDispatchSpan];
@@ -232,10 +235,10 @@ template <class Row, int E, int SPAN, bool ONCE>
 __global__ void __launch_bounds__(256) layer_combine_kernel(const CombineArgs p) {
   using Io = RowIo<Row, E>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int wid = blockIdx.x * 4 + w;
-  const int across = (p.H + SPAN * 64 * E - 1) / (SPAN * 64 * E);
-  const int t = __builtin_amdgcn_readfirstlane(wid / across);
-  if (t >= p.T) return;
+  const unsigned wid = layer_block() * 4 + w;
+  const unsigned across = (p.H + SPAN * 64 * E - 1) / (SPAN * 64 * E);
+  const unsigned t = __builtin_amdgcn_readfirstlane(wid / across);
+  if (t >= (unsigned)p.T) return;
   const int c0 = ((wid - t * across) * SPAN * 64 + lane) * E;  // piece s: c0 + s * 64 * E
   const int rows = p.T * p.top;
   const int64_t t0 = (int64_t)t * p.top;
@@ -293,8 +296,8 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
   __shared__ float part[4][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % W;
   const int tid = w * 64 + lane;
-  const int t = W == 4 ? blockIdx.x : blockIdx.x * (4 / W) + wave / W;
-  if (W == 1 && t >= p.T) return;
+  const unsigned t = W == 4 ? layer_block() : layer_block() * (4 / W) + wave / W;
+  if (t >= (unsigned)p.T) return;  // (W == 4: the whole workgroup)
   const int rows = p.T * p.top;
   const int64_t t0 = (int64_t)t * p.top;
   for (int j0 = 0; j0 < p.top; j0 += 4) {
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
 
 template <class Row, int E>
 hipError_t combine(const CombineArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((combine_waves(a) + 3) / 4)), block(256);
+  const dim3 grid = layer_grid((combine_waves(a) + 3) / 4, 256), block(256);
   if (a.once) return launch_kernel(layer_combine_kernel<Row, E, 2, true>, grid, block, s, a);
   if (combine_span(a) == 2) return launch_kernel(layer_combine_kernel<Row, E, 2, false>, grid, block, s, a);
   return launch_kernel(layer_combine_kernel<Row, E, 1, false>, grid, block, s, a);
@@ -373,26 +376,25 @@ hipError_t combine(const CombineArgs& a, hipStream_t s) {
 template <class Row, int E>
 hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
   if (a.H <= 2 * 64 * E)
-    return launch_kernel(layer_combine_grad_kernel<Row, E, 1>, dim3((a.T + 3) / 4), dim3(256), s, a);
-  return launch_kernel(layer_combine_grad_kernel<Row, E, 4>, dim3(a.T), dim3(256), s, a);
+    return launch_kernel(layer_combine_grad_kernel<Row, E, 1>, layer_grid(((int64_t)a.T + 3) / 4, 256), dim3(256), s, a);
+  return launch_kernel(layer_combine_grad_kernel<Row, E, 4>, layer_grid(a.T, 256), dim3(256), s, a);
 }
 
 }  // namespace
 
 hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s) {
   if (a.M > 0) {
-    const int blocks = (a.M + a.rows - 1) / a.rows;
-    const dim3 grid((unsigned)(((int64_t)blocks * act_grad_column_blocks(a.N) + 3) / 4));
+    const dim3 grid = layer_grid((act_grad_waves(a.M, a.N) + 3) / 4, 256);
     const hipError_t e = dtype == 0 ? launch_act<TagF16>(a, grid, s) : launch_act<TagBF16>(a, grid, s);
     if (e != hipSuccess) return e;
   }
   if (!a.db) return hipSuccess;
-  return launch_kernel(layer_bias_sum_kernel, dim3((a.N + 63) / 64, a.G), dim3(64 * kSumWaves),
-                       s, a);
+  return launch_kernel(layer_bias_sum_kernel, layer_grid(((int64_t)a.N + 63) / 64, 64 * kSumWaves, a.G),
+                       dim3(64 * kSumWaves), s, a);
 }
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
-  const dim3 grid((a.T + 3) / 4, (unsigned)dispatch_column_blocks(a)), block(256);
+  const dim3 grid = layer_grid(((int64_t)a.T + 3) / 4, 256, (unsigned)dispatch_column_blocks(a)), block(256);
   if (a.piece == 16) return launch_kernel(layer_dispatch_kernel<16>, grid, block, s, a);
   if (a.piece == 8) return launch_kernel(layer_dispatch_kernel<8>, grid, block, s, a);
   if (a.piece == 4) return launch_kernel(layer_dispatch_kernel<4>, grid, block, s, a);
