@@ -107,22 +107,24 @@ struct LayerRows {
   // group, its rows, and the tile's index within the group.
   __device__ static inline int find(const LayerArgs& p, int t, int tiles_n, int lane, int& first,
                                     int& count, int& in) {
-    int64_t base = 0;
+    unsigned base = 0;
     for (int g0 = 0; g0 < p.G; g0 += 64) {
       int f, c;
       const unsigned n = tiles_of(p, g0 + lane, f, c);
       const unsigned incl = wave_scan(n, lane);
       const unsigned chunk = __builtin_amdgcn_readlane(incl, 63);
-      if (t < (base + chunk) * tiles_n) {
-        // The first lane whose inclusive count lies past the tile: lane 63's does.
-        // Lanes past the last group count what the last group's lane does, so it
-        // is a group's lane.
-        const uint64_t past = __ballot((base + incl) * tiles_n > t);
+      // The first lane whose inclusive count lies past the tile, if one does (sums
+      // that have wrapped may say otherwise). Lanes past the last group count what
+      // the last group's lane does, so it is a group's lane.
+      uint64_t past = 0;
+      if (t < (int)((base + chunk) * (unsigned)tiles_n))
+        past = __ballot((int64_t)(int)(base + incl) * tiles_n > t);
+      if (past) {
         const int src = __builtin_ctzll(past);
         first = __builtin_amdgcn_readlane(f, src);
         count = __builtin_amdgcn_readlane(c, src);
-        const int64_t at = t - (base + (unsigned)__builtin_amdgcn_readlane(incl - n, src)) * tiles_n;
-        in = at < 0 ? -1 : (int)at;
+        const unsigned before = base + (unsigned)__builtin_amdgcn_readlane(incl - n, src);
+        in = (int)((unsigned)t - before * (unsigned)tiles_n);
         return g0 + src;
       }
       base += chunk;
