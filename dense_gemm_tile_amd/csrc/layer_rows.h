@@ -8,12 +8,15 @@
 namespace dgt {
 
 // n workgroups as a grid. A launch holds less than 2^32 threads along a
-// dimension, so further workgroups go along z, the last of them in part past n
-// (layer_block() in layer_rows.hip counts them).
-inline dim3 layer_grid(int64_t n, unsigned threads, unsigned y = 1) {
+// dimension (and one of more computes a part without an error), so further
+// workgroups go along z, the last of them in part past n. grid_x: workgroups of
+// one z, which the kernel gets among its arguments (layer_block() in
+// layer_rows.hip): the built-in is a hidden argument more for every launch.
+inline dim3 layer_grid(int64_t n, unsigned threads, unsigned& grid_x, unsigned y = 1) {
   const int64_t most = ((int64_t{1} << 32) - 1) / threads;
   const int64_t z = (n + most - 1) / most;
-  return dim3((unsigned)((n + z - 1) / z), y, (unsigned)z);
+  grid_x = (unsigned)((n + z - 1) / z);
+  return dim3(grid_x, y, (unsigned)z);
 }
 
 // Element types of rows.
@@ -29,6 +32,7 @@ struct ActGradArgs {
   int64_t lddy, ldz, lddz;
   int G, M, N, act;
   int rows;            // act_grad_rows(M, N)
+  unsigned grid_x;     // set at the launch (layer_grid), as in the others
 };
 // Rows that one wave sums by itself (a partial sum is kept for each): 32, fewer
 // where that would leave less than 16 waves to a CU. At 4096 x 4096 with GELU,
@@ -49,7 +53,7 @@ inline int64_t act_grad_waves(int64_t m, int64_t n) {
   const int rows = act_grad_rows(m, n);
   return (m + rows - 1) / rows * ((n + 511) / 512);
 }
-hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s);
+hipError_t launch_act_grad(int dtype, ActGradArgs a, hipStream_t s);
 
 struct RouteArgs {
   const int* ids;
@@ -74,13 +78,14 @@ struct DispatchArgs {
   int T, top;
   int64_t bytes;      // of a row
   int piece;          // bytes per access: 16, 8, 4 or 2
+  unsigned grid_x;
 };
 constexpr int kDispatchSpan = 4;  // pieces a lane
 inline int64_t dispatch_column_blocks(const DispatchArgs& a) {
   const int64_t span = (int64_t)kDispatchSpan * 64 * a.piece;
   return (a.bytes + span - 1) / span;
 }
-hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s);
+hipError_t launch_dispatch(DispatchArgs a, hipStream_t s);
 
 struct CombineArgs {
   const void* Ys;
@@ -92,6 +97,7 @@ struct CombineArgs {
   int T, top, H;
   int piece;  // elements per access
   int once;   // the rows read fill half of the last cache (256 MiB) or more
+  unsigned grid_x;
 };
 // Pieces a lane: two once that leaves 16 waves to a CU.
 inline int combine_span(const CombineArgs& a) {
@@ -114,6 +120,7 @@ struct CombineGradArgs {
   int64_t lddy, ldys, lddys;
   int T, top, H;
   int piece;
+  unsigned grid_x;
 };
 hipError_t launch_combine_grad(int rowtype, const CombineGradArgs& a, hipStream_t s);
 

@@ -10,7 +10,8 @@ namespace dgt {
 namespace {
 
 // This workgroup's index in a layer_grid().
-__device__ __forceinline__ unsigned layer_block() { return blockIdx.z * gridDim.x + blockIdx.x; }
+template <class Args>
+__device__ __forceinline__ unsigned layer_block(const Args& p) { return blockIdx.z * p.grid_x + blockIdx.x; }
 
 // ------------------------------------------------- activation and bias grads --
 // dZ = dY * act'(Z), and sums of dZ over rows before it is rounded. A wave
@@ -26,7 +27,7 @@ template <class Tag, int ACT>
 __global__ void __launch_bounds__(256) layer_act_grad_kernel(const ActGradArgs p) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int blocks = (p.N + 511) / 512;  // of columns
-  const unsigned id = layer_block() * 4 + w;
+  const unsigned id = layer_block(p) * 4 + w;
   const int b = id / blocks;
   const int c = (id - (unsigned)b * blocks) * 512 + lane * 8;
   const int nv = p.N - c >= 8 ? 8 : p.N - c;
@@ -99,7 +100,7 @@ constexpr int kSumWaves = 16;
 __global__ void __launch_bounds__(64 * kSumWaves) layer_bias_sum_kernel(const ActGradArgs p) {
   __shared__ float x[kSumWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int g = blockIdx.y, n = layer_block() * 64 + lane;
+  const int g = blockIdx.y, n = layer_block(p) * 64 + lane;
   int first = 0, count = p.M;
   if (p.offsets) layer_group(p.offsets, g, p.M, first, count);
   float s = 0.0f;
@@ -161,7 +162,7 @@ template <int PIECE>
 __global__ void __launch_bounds__(256) layer_dispatch_kernel(const DispatchArgs p) {
   using V = typename RowPiece<PIECE>::type;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const unsigned t = layer_block() * 4 + w;
+  const unsigned t = layer_block(p) * 4 + w;
   if (t >= (unsigned)p.T) return;
   const int64_t at = ((int64_t)blockIdx.y * kDispatchSpan * 64 + lane) * PIECE;
   const char* src = p.X + (int64_t)t * p.ldx + at;
@@ -235,7 +236,7 @@ template <class Row, int E, int SPAN, bool ONCE>
 __global__ void __launch_bounds__(256) layer_combine_kernel(const CombineArgs p) {
   using Io = RowIo<Row, E>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const unsigned wid = layer_block() * 4 + w;
+  const unsigned wid = layer_block(p) * 4 + w;
   const unsigned across = (p.H + SPAN * 64 * E - 1) / (SPAN * 64 * E);
   const unsigned t = __builtin_amdgcn_readfirstlane(wid / across);
   if (t >= (unsigned)p.T) return;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
   __shared__ float part[4][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % W;
   const int tid = w * 64 + lane;
-  const unsigned t = W == 4 ? layer_block() : layer_block() * (4 / W) + wave / W;
+  const unsigned t = W == 4 ? layer_block(p) : layer_block(p) * (4 / W) + wave / W;
   if (t >= (unsigned)p.T) return;  // (W == 4: the whole workgroup)
   const int rows = p.T * p.top;
   const int64_t t0 = (int64_t)t * p.top;
@@ -367,34 +368,39 @@ __global__ void __launch_bounds__(256) layer_combine_grad_kernel(const CombineGr
 }
 
 template <class Row, int E>
-hipError_t combine(const CombineArgs& a, hipStream_t s) {
-  const dim3 grid = layer_grid((combine_waves(a) + 3) / 4, 256), block(256);
+hipError_t combine(CombineArgs a, hipStream_t s) {
+  const dim3 grid = layer_grid((combine_waves(a) + 3) / 4, 256, a.grid_x), block(256);
   if (a.once) return launch_kernel(layer_combine_kernel<Row, E, 2, true>, grid, block, s, a);
   if (combine_span(a) == 2) return launch_kernel(layer_combine_kernel<Row, E, 2, false>, grid, block, s, a);
   return launch_kernel(layer_combine_kernel<Row, E, 1, false>, grid, block, s, a);
 }
 template <class Row, int E>
-hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
-  if (a.H <= 2 * 64 * E)
-    return launch_kernel(layer_combine_grad_kernel<Row, E, 1>, layer_grid(((int64_t)a.T + 3) / 4, 256), dim3(256), s, a);
-  return launch_kernel(layer_combine_grad_kernel<Row, E, 4>, layer_grid(a.T, 256), dim3(256), s, a);
+hipError_t combine_grad(CombineGradArgs a, hipStream_t s) {
+  const dim3 block(256);
+  if (a.H <= 2 * 64 * E) {
+    const dim3 grid = layer_grid(((int64_t)a.T + 3) / 4, 256, a.grid_x);
+    return launch_kernel(layer_combine_grad_kernel<Row, E, 1>, grid, block, s, a);
+  }
+  const dim3 grid = layer_grid(a.T, 256, a.grid_x);
+  return launch_kernel(layer_combine_grad_kernel<Row, E, 4>, grid, block, s, a);
 }
 
 }  // namespace
 
-hipError_t launch_act_grad(int dtype, const ActGradArgs& a, hipStream_t s) {
+hipError_t launch_act_grad(int dtype, ActGradArgs a, hipStream_t s) {
   if (a.M > 0) {
-    const dim3 grid = layer_grid((act_grad_waves(a.M, a.N) + 3) / 4, 256);
+    const dim3 grid = layer_grid((act_grad_waves(a.M, a.N) + 3) / 4, 256, a.grid_x);
     const hipError_t e = dtype == 0 ? launch_act<TagF16>(a, grid, s) : launch_act<TagBF16>(a, grid, s);
     if (e != hipSuccess) return e;
   }
   if (!a.db) return hipSuccess;
-  return launch_kernel(layer_bias_sum_kernel, layer_grid(((int64_t)a.N + 63) / 64, 64 * kSumWaves, a.G),
-                       dim3(64 * kSumWaves), s, a);
+  const dim3 grid = layer_grid(((int64_t)a.N + 63) / 64, 64 * kSumWaves, a.grid_x, a.G);
+  return launch_kernel(layer_bias_sum_kernel, grid, dim3(64 * kSumWaves), s, a);
 }
 
-hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
-  const dim3 grid = layer_grid(((int64_t)a.T + 3) / 4, 256, (unsigned)dispatch_column_blocks(a)), block(256);
+hipError_t launch_dispatch(DispatchArgs a, hipStream_t s) {
+  const dim3 grid = layer_grid(((int64_t)a.T + 3) / 4, 256, a.grid_x, (unsigned)dispatch_column_blocks(a));
+  const dim3 block(256);
   if (a.piece == 16) return launch_kernel(layer_dispatch_kernel<16>, grid, block, s, a);
   if (a.piece == 8) return launch_kernel(layer_dispatch_kernel<8>, grid, block, s, a);
   if (a.piece == 4) return launch_kernel(layer_dispatch_kernel<4>, grid, block, s, a);
