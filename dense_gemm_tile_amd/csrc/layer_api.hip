@@ -433,9 +433,11 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
     set_path("noop: empty output");
     return GEMM_OK;
   }
-  if (G > 1 && stride_d < (N - 1) * ldd + K)
+  // (128 bits: a matrix of N - 1 long pitches may be past 64.)
+  const __int128 one = (__int128)(N - 1) * ldd + K;
+  if (G > 1 && stride_d < one)
     return bad("%s=%lld is smaller than one matrix of %lld elements", "stride_d", stride_d,
-               (N - 1) * ldd + K);
+               one > INT64_MAX ? INT64_MAX : (int64_t)one);
   CHECK(check_ptr(md));
   CHECK(check_ptr(moff));
   CHECK(check_apart(md, moff));

@@ -25,3 +25,10 @@ def test_pieces_of_rows(lib):  # noqa: F811
     big = dict(M=M, N=N, lddy=N, ldz=N, lddz=N, Z=1 << 55, dZ=1 << 56, db=None)
     assert act_grad(lib, **big) == 2
     assert "too many" in lib.gemm_last_error()
+
+
+@pytest.mark.parametrize("ldd,stride", [(1 << 33, 0), (1 << 33, 1 << 62), (1 << 40, 1 << 50), (1 << 62, (1 << 63) - 1)])
+def test_overlapping_weight_gradients_of_far_rows(lib, ldd, stride):  # noqa: F811
+    """One matrix is (N - 1) * ldd + K elements, which 64 bits need not hold."""
+    assert grad_weight(lib, G=2, N=MOST, K=8, lda=MOST, M=0, A=None, B=None, D=1 << 40, ldd=ldd, stride=stride) == 1
+    assert "stride_d" in lib.gemm_last_error()
