@@ -72,11 +72,18 @@ def _compile(src: str, extra, incremental: bool = False) -> str:
 
 
 def _build_binding() -> None:
-    """The extension module: host code only, linked to the library beside it."""
+    """The extension module: host code only, linked to the library beside it. Without Python's
+    headers it is left out (the package then calls the library through ctypes)."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        print(f"no Python.h in {include}: the extension module is left out", file=sys.stderr)
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)  # of another build
+        return
     tmp = BINDING_PATH + ".tmp"
     cmd = [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
            "-no-hip-rt",
-           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(ROOT, "include"), "-I", include,
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", PKG_DIR, f"-l:{LIB_NAME}",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
