@@ -255,10 +255,13 @@ constexpr float kGeluB = 0.044715f;
 // The normal distribution's function Phi(z) and exp(-z^2 / 2). With x = |z| /
 // sqrt(2) and t = 1 / (1 + x / 2), erfc(x) exp(x^2) / t is smooth on t in (0, 1]: a
 // polynomial of degree 8 fitted to it for x up to 9.4 by least squares weighted
-// toward the largest relative error (4e-8; 1.4e-7 in float32 arithmetic). The
-// exponent z^2 / 2 log2(e) is held in two floats, so that the exponential keeps
-// its relative accuracy far out: Phi of a negative z is not a difference. (The
-// library's erfc: 4096x4096x1024 48 us, 42 so, 32 without an activation.)
+// toward the largest relative error, 7.4e-8 with these coefficients in exact
+// arithmetic. The exponent z^2 / 2 log2(e) is held in two floats, so that the
+// exponential keeps its relative accuracy far out: Phi of a negative z is not a
+// difference. In float32 Phi is within 4e-7, relative, from -13 on (least
+// accurate near -1.6) where the reciprocal and the exponential are rounded
+// correctly; the hardware's add their last bit each. (The library's erfc:
+// 4096x4096x1024 48 us, 42 so, 32 without an activation.)
 struct LayerNormal {
   float phi, e;
 };
