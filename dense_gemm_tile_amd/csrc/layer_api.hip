@@ -223,16 +223,33 @@ int choose_kernel(const LayerPlan& pl) {
   const LayerArgs& a = pl.a;
   auto tiles = [&](int k) { return count_tiles(a, kLayerKernels[k]); };
   if (!kernel_runs(pl, LK_PP256)) {
-    if (kernel_runs(pl, LK_ANY16)) {
-      if (a.mode == LAYER_ROWS) {
-        if (a.M <= 4 * (int64_t)a.G) return LK_ANY16;  // (16 rows a group: 197 us, 135 on 64 x 64)
-      } else if (a.M <= 64 || tiles(LK_ANY64) <= 256) {
-        // The most rows a tile that still give every CU one (64x4096x4095:
-        // 128 tiles of 64 rows 43 us, 256 of 32 rows 29).
-        for (int k : {LK_ANY64, LK_ANY32})
-          if (a.M > kLayerKernels[k].bm / 2 && tiles(k) >= 224) return k;
-        return a.M <= 32 ? LK_ANY16 : LK_ANY32;
-      }
+    // Few rows a group: one row of tiles each, so 64 x 64 tiles. The count above is of
+    // the most tiles that the groups' sizes could make, not of those to expect. An odd
+    // pitch of A, B stored [N][K], 2 rows a group, us:
+    //                            tiles   u16x32   g64x64k4   g64x64   g128x128
+    //   256 groups of 1024x512    4096     136       135        60        67
+    //   64 groups of 2048x2048    2048     147       140       127       130
+    //   8 groups of 2048x2048      256      21        17        28        36
+    //   8 groups of 1024x1024      128       9        10        13        20
+    // (16 rows of 64 groups: 171, 145, 128, 131; 64 rows: g64x64 145, g128x128 141; B
+    // stored [K][N] with an odd pitch, 16 rows: g64x64 114, g128x128 121, r128x128 131.)
+    // With an odd pitch of B, up to 4 rows a group, u16x32 is ahead to 512 tiles:
+    //   24 groups of 1024x1024     384      15        21        18        24
+    //   8 groups of 4096x2048      512      30        35        32        42
+    //   16 groups of 4096x1024    1024      35        43        24        27
+    const int64_t used = a.G < a.M ? a.G : a.M, rows = a.G ? (a.M + (int64_t)a.G - 1) / a.G : 0;
+    if (a.mode == LAYER_ROWS && rows <= 32) {
+      const int64_t n = used * (((int64_t)a.N + 63) / 64);
+      if (kernel_runs(pl, LK_ANY16) && rows <= 16 && n <= (rows <= 4 && !a.b_direct ? 512 : 128))
+        return LK_ANY16;
+      return n <= 256 && a.K >= 512 ? LK_GENERAL64K4 : LK_GENERAL64;
+    }
+    if (kernel_runs(pl, LK_ANY16) && a.mode == LAYER_DENSE && (a.M <= 64 || tiles(LK_ANY64) <= 256)) {
+      // The most rows a tile that still give every CU one (64x4096x4095:
+      // 128 tiles of 64 rows 43 us, 256 of 32 rows 29).
+      for (int k : {LK_ANY64, LK_ANY32})
+        if (a.M > kLayerKernels[k].bm / 2 && tiles(k) >= 224) return k;
+      return a.M <= 32 ? LK_ANY16 : LK_ANY32;
     }
     // The sum split over wave groups where 64 x 64 tiles leave CUs idle, or a long
     // sum dominates (300x5001x3001: 87 us on 64 x 64 tiles, 65 split).

@@ -1,5 +1,7 @@
 """Sizes at the edge of what a launch or 64-bit arithmetic holds: refused before anything is enqueued.
 No GPU: every call here is refused or only checked."""
+import ctypes
+
 import pytest
 
 from test_layer_cpu import A0, B0, P0, R0, W0, Y0, Z0, act_grad, call, grad_weight, grouped, lib, linear  # noqa: F401
@@ -9,10 +11,15 @@ MOST = 2 ** 31 - 1024
 
 def test_tiles_of_a_launch(lib):  # noqa: F811
     # 512 threads a workgroup: 2^23 - 1 tiles of 16 rows and 32 columns, one row of tiles a group
-    assert grouped(lib, G=32767, M=32767, N=256 * 32, K=65, lda=65, ldb=65, stride=0, Y=1 << 60) == 0
-    assert " u16x32 " in lib.gemm_last_path()
-    assert grouped(lib, G=32768, M=32768, N=256 * 32, K=65, lda=65, ldb=65, stride=0, Y=1 << 60) == 2
-    assert "too many" in lib.gemm_last_error()
+    env = ctypes.CDLL(None)
+    env.setenv(b"GEMM_LAYER_TILE", b"u16x32", 1)
+    try:
+        assert grouped(lib, G=32767, M=32767, N=256 * 32, K=65, lda=65, ldb=65, stride=0, Y=1 << 60) == 0
+        assert " u16x32 " in lib.gemm_last_path()
+        assert grouped(lib, G=32768, M=32768, N=256 * 32, K=65, lda=65, ldb=65, stride=0, Y=1 << 60) == 2
+        assert "too many" in lib.gemm_last_error()
+    finally:
+        env.unsetenv(b"GEMM_LAYER_TILE")
     # the longest dense calls still fit
     assert linear(lib, M=MOST, N=1, K=1, A=A0, B=1 << 56, Y=1 << 60) == 0
     assert linear(lib, M=MOST, N=8, K=8, A=A0, B=1 << 56, Y=1 << 60) == 0
