@@ -3,7 +3,9 @@ and include/gemm_layer.h).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libdense_gemm_tile_amd.so. Importing this package loads that
-library and fails loudly if it has not been built (there is no CPU fallback).
+library and fails loudly if it has not been built (there is no CPU fallback). The
+layer operators' calls convert their arguments in an extension module beside it
+(csrc/binding.cpp), or in ctypes where that was not built for this interpreter.
 
 Pointer arguments accept an int (a device address), None (NULL) or any object
 with ``data_ptr()`` (a torch tensor). ``stream`` accepts an int (a hipStream_t

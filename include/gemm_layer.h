@@ -20,7 +20,11 @@
  * Numbers read on the GPU (expert ids, offsets, slots) cannot be checked
  * before the call returns. The kernels check them where they use them: an id
  * outside [0, E) counts as dropped, a slot outside [0, T*top) is skipped, and
- * offsets are clamped to [0, M], so no access leaves the buffers.
+ * offsets are clamped to [0, M], so no access leaves the buffers, also where
+ * offsets decrease (what such a call computes is not defined).
+ *
+ * A product of more output tiles than one launch holds (2^32 threads: from 2^22
+ * tiles on, by the kernel) is refused with GEMM_ERR_UNSUPPORTED.
  */
 #ifndef GEMM_LAYER_H
 #define GEMM_LAYER_H
@@ -152,7 +156,8 @@ GEMM_API int64_t gemm_route_workspace(int64_t T, int64_t top, int64_t E);
 /*
  * gemm_dispatch: Xs[slot[t][j]] = X[t] for every kept choice. X: T x H,
  * Xs: (T * top) x H, both of `dtype` (f16, bf16 or GEMM_DTYPE_F32); rows of Xs
- * that no slot names are not written.
+ * that no slot names are not written. Rows of more than 65535 * 256 accesses (of 16
+ * bytes, or as few as H, the addresses and the pitches allow) are refused.
  */
 GEMM_API int gemm_dispatch(int64_t T, int64_t top, int64_t H, int dtype, const void* X, int64_t ldx,
                   const int32_t* slot, void* Xs, int64_t ldxs, void* stream);
