@@ -126,7 +126,9 @@ __host__ __device__ inline void schedule_tile(int bid, int tiles_m, int tiles_n,
 
 // Enqueue kernel `k` on `s` with the given arguments. The status returned is
 // that of this launch alone (hipLaunchKernel), so an error left behind by an
-// earlier, unrelated HIP call on the thread is neither reported nor cleared.
+// earlier, unrelated HIP call on the thread is neither reported nor cleared. A
+// launch of 2^32 threads or more along a dimension is an error here: HIP accepts
+// it and runs a part (2^26 + 5 waves: eight of them).
 template <class T>
 struct same_type {
   using type = T;
@@ -134,6 +136,10 @@ struct same_type {
 template <class... P>
 inline hipError_t launch_kernel(void (*k)(P...), dim3 grid, dim3 block, hipStream_t s,
                                 typename same_type<P>::type... args) {
+  const uint64_t most = 0xffffffffu;
+  if ((uint64_t)grid.x * block.x > most || (uint64_t)grid.y * block.y > most ||
+      (uint64_t)grid.z * block.z > most)
+    return hipErrorInvalidConfiguration;
   void* argv[] = {static_cast<void*>(&args)...};
   return hipLaunchKernel(reinterpret_cast<const void*>(k), grid, block, argv, 0, s);
 }

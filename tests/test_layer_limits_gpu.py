@@ -83,3 +83,21 @@ def test_act_grad_of_long_rows(M, N):
     want = torch.where(z > 0, dy, torch.zeros_like(dy))
     assert torch.equal(dz, want)
     assert torch.equal(db[0], want.float().sum(0))
+
+
+def test_a_launch_that_is_too_large_is_an_error(monkeypatch):
+    """2^26 and one tiles of gemm() at 64 threads each: nothing is computed, and the call says so."""
+    need_gpu()
+    import dense_gemm_tile_amd as dgt
+    M = 2 ** 30 + 16
+    say(f"gemm {M}x1x1 on 16x16 tiles")
+    monkeypatch.setenv("GEMM_FORCE_TILE", "t16x16x64")
+    a, b = torch.ones(M, dtype=torch.bfloat16, device=DEV), torch.ones(1, dtype=torch.bfloat16, device=DEV)
+    d = nan(M, dtype=torch.float32)
+    s = torch.cuda.current_stream()
+    with pytest.raises(dgt.GemmError) as e:
+        dgt.gemm(M, 1, 1, "bf16", 0, 1, 1.0, 0.0, a, 1, b, 1, None, 1, d, 1, stream=s)
+    assert e.value.code == dgt.GEMM_ERR_HIP and "t16x16x64" in dgt.gemm_last_path()
+    assert bool(torch.isnan(d).all())
+    dgt.gemm(2 ** 30 - 16, 1, 1, "bf16", 0, 1, 1.0, 0.0, a, 1, b, 1, None, 1, d, 1, stream=s)
+    assert bool((d[:2 ** 30 - 16] == 1).all()) and bool(torch.isnan(d[2 ** 30 - 16:]).all())
