@@ -43,6 +43,7 @@ GEMM_DTYPE_F8_E4M3 = 4   # 8-bit float codes, OCP E4M3
 GEMM_DTYPE_F8_E5M2 = 5   # 8-bit float codes, OCP E5M2
 GEMM_DTYPE_F32 = 6       # float32 results and rows of the layer operators
 GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_ERF, GEMM_ACT_SILU = range(5)
+GEMM_SCORE_SOFTMAX, GEMM_SCORE_SIGMOID = range(2)
 
 # Every symbol the header declares, with its ctypes signature.
 _i64, _int, _f32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p
@@ -82,6 +83,23 @@ _SIGNATURES = {
                             _vp]),
     "gemm_combine_grad": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                                  _vp, _vp]),
+    "gemm_norm": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _vp, _f32, _vp, _i64, _vp, _vp, _vp]),
+    "gemm_norm_grad": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
+                              _i64, _vp, _vp, _vp, _i64, _vp]),
+    "gemm_norm_grad_workspace": (_i64, [_i64, _i64]),
+    "gemm_gate": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _i64, _i64, _int, _f32,
+                         _vp, _vp, _vp]),
+    "gemm_gate_grad": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _int, _int, _f32, _vp, _vp, _vp,
+                              _i64, _vp]),
+    "gemm_linear_w4": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
+                              _vp, _int, _vp, _i64, _vp, _i64, _int, _vp]),
+    "gemm_grouped_w4": (_int, [_i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _i64, _i64, _vp,
+                               _vp, _i64, _i64, _i64, _vp, _int, _vp, _i64, _vp, _i64, _int, _vp]),
+    "gemm_loss": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "gemm_loss_workspace": (_i64, [_i64, _i64, _i64]),
+    "gemm_loss_grad": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+                              _vp, _i64, _int, _int, _vp, _i64, _vp]),
+    "gemm_loss_grad_workspace": (_i64, [_i64, _i64, _i64]),
 }
 
 
@@ -128,6 +146,7 @@ _DTYPE_CODES = {"f16": GEMM_DTYPE_F16, "bf16": GEMM_DTYPE_BF16, "f32_f16": GEMM_
                 "f8e5m2": GEMM_DTYPE_F8_E5M2, "f32": GEMM_DTYPE_F32}
 _ACT_CODES = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GELU,
               "gelu_erf": GEMM_ACT_GELU_ERF, "silu": GEMM_ACT_SILU}
+_SCORE_CODES = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
 
 
 def _dtype(d):
@@ -142,14 +161,25 @@ def _act(a):
     return int(a)
 
 
+def _score(s):
+    if isinstance(s, str):
+        return _SCORE_CODES[s]
+    return int(s)
+
+
 class _CtypesCalls:
     """The calls of the extension module (_binding) through ctypes: the same arguments and status
     codes, at about 3 us of host time a call instead of 0.8."""
 
-    # Positions of dtypes, and of the activation, among an entry point's arguments.
+    # Positions of dtypes, and of the activation or score, among an entry point's arguments.
     _DTYPES = {"gemm_linear": (3, 16), "gemm_grouped": (4, 18), "gemm_grouped_grad_weight": (4, 13),
-               "gemm_act_grad": (3,), "gemm_dispatch": (3,), "gemm_combine": (3,), "gemm_combine_grad": (3,)}
-    _ACT = {"gemm_linear": 11, "gemm_grouped": 13, "gemm_act_grad": 4}
+               "gemm_act_grad": (3,), "gemm_dispatch": (3,), "gemm_combine": (3,), "gemm_combine_grad": (3,),
+               "gemm_norm": (2,), "gemm_norm_grad": (2,), "gemm_gate": (3,), "gemm_gate_grad": (3,),
+               "gemm_linear_w4": (3, 18), "gemm_grouped_w4": (4, 22), "gemm_loss": (3,),
+               "gemm_loss_grad": (3, 15)}
+    _ACT = {"gemm_linear": 11, "gemm_grouped": 13, "gemm_act_grad": 4, "gemm_linear_w4": 13,
+            "gemm_grouped_w4": 17}
+    _SCORE = {"gemm_gate": 6, "gemm_gate_grad": 6}
 
     def __getattr__(self, name):  # once a name
         fn, types = getattr(_lib, name), _SIGNATURES[name][1]
@@ -160,6 +190,8 @@ class _CtypesCalls:
             convert[i] = _dtype
         if name in self._ACT:
             convert[self._ACT[name]] = _act
+        if name in self._SCORE:
+            convert[self._SCORE[name]] = _score
         call = lambda *args: fn(*[c(a) for c, a in zip(convert, args, strict=True)])  # noqa: E731
         setattr(self, name, call)
         return call
@@ -306,6 +338,80 @@ def gemm_combine_grad(T, top, H, dtype, dY, lddy, Ys, ldys, slot, weights, dYs, 
                                    dweights, stream))
 
 
+def gemm_norm(M, N, dtype, X, ldx, gamma, beta, eps, Y, ldy, mean=None, rstd=None, stream=None):
+    """Enqueue Y = (X - mean) * rstd * gamma + beta for rows of N values (gamma and beta may be None;
+    mean and rstd, M float32 values each, are written when given)."""
+    _check(_fast.gemm_norm(M, N, dtype, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, stream))
+
+
+def gemm_norm_grad(M, N, dtype, dY, lddy, X, ldx, gamma, mean, rstd, R, ldr, dX, lddx, dgamma, dbeta,
+                   workspace, workspace_bytes, stream=None):
+    """Enqueue the gradients of gemm_norm(): dX (plus R, which may be None), and dgamma and dbeta
+    in float32. workspace: gemm_norm_grad_workspace(M, N) bytes on the device."""
+    _check(_fast.gemm_norm_grad(M, N, dtype, dY, lddy, X, ldx, gamma, mean, rstd, R, ldr, dX, lddx,
+                                dgamma, dbeta, workspace, workspace_bytes, stream))
+
+
+def gemm_norm_grad_workspace(M, N) -> int:
+    """Bytes of workspace that gemm_norm_grad() needs."""
+    return _fast.gemm_norm_grad_workspace(M, N)
+
+
+def gemm_gate(T, E, top, dtype, L, ldl, score, bias, groups, top_groups, group_top, renorm, scale, ids,
+              weights, stream=None):
+    """Enqueue the choice of `top` of E experts for each token from its logits: ids (T x top int32)
+    and weights (T x top float32). score: "softmax" or "sigmoid"; bias: E float32 values or None;
+    groups, top_groups, group_top: 1, 1, 1 for no groups."""
+    _check(_fast.gemm_gate(T, E, top, dtype, L, ldl, score, bias, groups, top_groups, group_top, renorm,
+                           scale, ids, weights, stream))
+
+
+def gemm_gate_grad(T, E, top, dtype, L, ldl, score, renorm, scale, ids, dweights, dL, lddl, stream=None):
+    """Enqueue the gradient of the logits from that of gemm_gate()'s weights."""
+    _check(_fast.gemm_gate_grad(T, E, top, dtype, L, ldl, score, renorm, scale, ids, dweights, dL, lddl,
+                                stream))
+
+
+def gemm_linear_w4(M, N, K, dtype, A, lda, B, ldb, scales, zeros, lds, group, bias, act, R, ldr, Y, ldy,
+                   out_dtype, stream=None):
+    """Enqueue Y = act(A @ W^T + bias) + R with W[n][k] = scales[n][k // group] * (code[n][k] -
+    zeros[n][k // group]); B holds the codes, two to a byte, the even k in the lower half; zeros None: 8."""
+    _check(_fast.gemm_linear_w4(M, N, K, dtype, A, lda, B, ldb, scales, zeros, lds, group, bias, act, R,
+                                ldr, Y, ldy, out_dtype, stream))
+
+
+def gemm_grouped_w4(G, M, N, K, dtype, offsets, A, lda, B, ldb, stride_b, scales, zeros, lds, stride_s,
+                    group, bias, act, R, ldr, Y, ldy, out_dtype, stream=None):
+    """Enqueue gemm_linear_w4() with one W and bias per group of rows offsets[g] .. offsets[g+1]-1."""
+    _check(_fast.gemm_grouped_w4(G, M, N, K, dtype, offsets, A, lda, B, ldb, stride_b, scales, zeros, lds,
+                                 stride_s, group, bias, act, R, ldr, Y, ldy, out_dtype, stream))
+
+
+def gemm_loss(T, V, H, dtype, X, ldx, W, ldw, labels, loss, lse, workspace, workspace_bytes, stream=None):
+    """Enqueue the cross entropy of the logits X @ W^T (T x V) against int32 labels: loss and lse (may
+    be None), T float32 values each. workspace: gemm_loss_workspace(T, V, H) bytes on the device."""
+    _check(_fast.gemm_loss(T, V, H, dtype, X, ldx, W, ldw, labels, loss, lse, workspace, workspace_bytes,
+                           stream))
+
+
+def gemm_loss_workspace(T, V, H) -> int:
+    """Bytes of workspace that gemm_loss() needs."""
+    return _fast.gemm_loss_workspace(T, V, H)
+
+
+def gemm_loss_grad(T, V, H, dtype, X, ldx, W, ldw, labels, lse, dloss, dX, lddx, dW, lddw, dw_dtype,
+                   accumulate, workspace, workspace_bytes, stream=None):
+    """Enqueue the gradients of gemm_loss(): dX and dW (either may be None) from dloss and lse.
+    workspace: gemm_loss_grad_workspace(T, V, H) bytes on the device."""
+    _check(_fast.gemm_loss_grad(T, V, H, dtype, X, ldx, W, ldw, labels, lse, dloss, dX, lddx, dW, lddw,
+                                dw_dtype, accumulate, workspace, workspace_bytes, stream))
+
+
+def gemm_loss_grad_workspace(T, V, H) -> int:
+    """Bytes of workspace that gemm_loss_grad() needs."""
+    return _fast.gemm_loss_grad_workspace(T, V, H)
+
+
 def gemm_last_error() -> str:
     return _lib.gemm_last_error().decode()
 
@@ -334,4 +440,7 @@ __all__ = ["gemm_i8", "gemm_i8_validate", "gemm", "gemm_status", "gemm_validate"
            "gemm_grouped_grad_weight", "gemm_grouped_grad_weight_validate", "gemm_act_grad",
            "gemm_act_grad_workspace", "gemm_route", "gemm_route_workspace", "gemm_dispatch",
            "gemm_combine", "gemm_combine_grad", "GEMM_DTYPE_F32", "GEMM_ACT_NONE",
-           "GEMM_ACT_RELU", "GEMM_ACT_GELU", "GEMM_ACT_GELU_ERF", "GEMM_ACT_SILU"]
+           "GEMM_ACT_RELU", "GEMM_ACT_GELU", "GEMM_ACT_GELU_ERF", "GEMM_ACT_SILU",
+           "gemm_norm", "gemm_norm_grad", "gemm_norm_grad_workspace", "gemm_gate", "gemm_gate_grad",
+           "gemm_linear_w4", "gemm_grouped_w4", "gemm_loss", "gemm_loss_workspace", "gemm_loss_grad",
+           "gemm_loss_grad_workspace", "GEMM_SCORE_SOFTMAX", "GEMM_SCORE_SIGMOID"]

@@ -7,7 +7,7 @@
 //   tensors   anything with data_ptr(), an integer address, or None for NULL
 //   stream    anything with cuda_stream, an integer handle, or None for NULL
 //   dtype     a code, or one of the names below (KeyError for another name);
-//   act       the same
+//   act       the same, as is score
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -33,12 +33,17 @@ constexpr Name kActs[] = {{"none", GEMM_ACT_NONE},
                           {"gelu", GEMM_ACT_GELU},
                           {"gelu_erf", GEMM_ACT_GELU_ERF},
                           {"silu", GEMM_ACT_SILU}};
+constexpr Name kScores[] = {{"softmax", GEMM_SCORE_SOFTMAX}, {"sigmoid", GEMM_SCORE_SIGMOID}};
 // What a parameter holds, where its C type does not say.
 struct Dtype {
   int code;
   operator int() const { return code; }
 };
 struct Act {
+  int code;
+  operator int() const { return code; }
+};
+struct Score {
   int code;
   operator int() const { return code; }
 };
@@ -77,6 +82,12 @@ bool convert_name(PyObject* o, const Name (&names)[n], int& v) {
 }
 bool convert(PyObject* o, Dtype& v) { return convert_name(o, kDtypes, v.code); }
 bool convert(PyObject* o, Act& v) { return convert_name(o, kActs, v.code); }
+bool convert(PyObject* o, Score& v) { return convert_name(o, kScores, v.code); }
+bool convert(PyObject* o, float& v) {
+  const double d = PyFloat_AsDouble(o);
+  v = (float)d;
+  return d != -1.0 || !PyErr_Occurred();
+}
 bool convert_address(PyObject* o, void*& v) {
   v = PyLong_AsVoidPtr(o);
   return v || !PyErr_Occurred();
@@ -155,6 +166,23 @@ PyMethodDef g_methods[] = {
                Stream>>("gemm_combine"),
     entry<Call<gemm_combine_grad, I, I, I, Dtype, In, I, In, I, const int32_t*, const float*, Out,
                I, float*, Stream>>("gemm_combine_grad"),
+    entry<Call<gemm_norm, I, I, Dtype, In, I, In, In, float, Out, I, float*, float*, Stream>>("gemm_norm"),
+    entry<Call<gemm_norm_grad, I, I, Dtype, In, I, In, I, In, const float*, const float*, In, I, Out, I, float*,
+               float*, Out, I, Stream>>("gemm_norm_grad"),
+    entry<Call<gemm_norm_grad_workspace, I, I>>("gemm_norm_grad_workspace"),
+    entry<Call<gemm_gate, I, I, I, Dtype, In, I, Score, const float*, I, I, I, int, float, int32_t*, float*,
+               Stream>>("gemm_gate"),
+    entry<Call<gemm_gate_grad, I, I, I, Dtype, In, I, Score, int, float, const int32_t*, const float*, Out, I,
+               Stream>>("gemm_gate_grad"),
+    entry<Call<gemm_linear_w4, I, I, I, Dtype, In, I, In, I, In, In, I, I, In, Act, In, I, Out, I, Dtype,
+               Stream>>("gemm_linear_w4"),
+    entry<Call<gemm_grouped_w4, I, I, I, I, Dtype, const int32_t*, In, I, In, I, I, In, In, I, I, I, In, Act, In, I,
+               Out, I, Dtype, Stream>>("gemm_grouped_w4"),
+    entry<Call<gemm_loss, I, I, I, Dtype, In, I, In, I, const int32_t*, float*, float*, Out, I, Stream>>("gemm_loss"),
+    entry<Call<gemm_loss_workspace, I, I, I>>("gemm_loss_workspace"),
+    entry<Call<gemm_loss_grad, I, I, I, Dtype, In, I, In, I, const int32_t*, const float*, const float*, Out, I, Out,
+               I, Dtype, int, Out, I, Stream>>("gemm_loss_grad"),
+    entry<Call<gemm_loss_grad_workspace, I, I, I>>("gemm_loss_grad_workspace"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding",

@@ -9,85 +9,11 @@
 #include "gemm_layer.h"
 #include "api_state.h"
 #include "layer.h"
+#include "layer_checks.h"
 #include "layer_rows.h"
 
 namespace dgt {
 namespace {
-
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;
-constexpr int64_t kMaxGroups = 65535;  // groups index a launch's second dimension
-
-int bad(const char* fmt, const char* name, int64_t a, int64_t b = 0) {
-  char buf[200];
-  std::snprintf(buf, sizeof buf, fmt, name, (long long)a, (long long)b);
-  return fail(GEMM_ERR_INVALID_ARG, buf);
-}
-
-// One matrix (or a stack of them) that a call reads or writes.
-struct Mat {
-  const char* name;
-  const void* ptr;
-  int64_t rows, cols, ld;
-  int elem;                 // bytes
-  int64_t count = 1, stride = 0;  // stacked matrices
-  unsigned __int128 extent() const {
-    if (!ptr || count <= 0) return 0;
-    const unsigned __int128 one = extent_bytes(rows, cols, ld, elem);
-    return one ? one + (unsigned __int128)(count - 1) * (unsigned __int128)stride * elem : 0;
-  }
-};
-
-int check_dim(const char* name, int64_t v) {
-  if (v < 0) return bad("negative dimension: %s=%lld", name, v);
-  if (v > kMaxDim) return fail(GEMM_ERR_UNSUPPORTED, std::string(name) + " exceeds 2^31-1024");
-  return GEMM_OK;
-}
-int check_ld(const Mat& m) {
-  const int64_t least = m.cols > 1 ? m.cols : 1;
-  if (m.ld < least) return bad("leading dimension of %s is %lld, smaller than %lld", m.name, m.ld, least);
-  return GEMM_OK;
-}
-int check_ptr(const Mat& m) {
-  if (!m.ptr) return fail(GEMM_ERR_INVALID_ARG, std::string(m.name) + " is NULL");
-  if ((uintptr_t)m.ptr % m.elem)
-    return bad("%s is not %lld-byte aligned", m.name, m.elem);
-  return GEMM_OK;
-}
-int check_apart(const Mat& w, const Mat& r) {
-  if (w.ptr && r.ptr && overlaps(w.ptr, w.extent(), r.ptr, r.extent()))
-    return fail(GEMM_ERR_ALIAS, std::string(w.name) + " overlaps " + r.name);
-  return GEMM_OK;
-}
-// As check_apart, but the two may be the same matrix.
-int check_apart_or_same(const Mat& w, const Mat& r) {
-  if (w.ptr == r.ptr && (w.ld == r.ld || w.rows <= 1) && w.elem == r.elem && w.stride == r.stride)
-    return GEMM_OK;
-  return check_apart(w, r);
-}
-
-#define CHECK(expr)                      \
-  do {                                   \
-    const int st_ = (expr);              \
-    if (st_ != GEMM_OK) return st_;      \
-  } while (0)
-
-int check_dtype16(int dtype) {
-  if (dtype == GEMM_DTYPE_F16 || dtype == GEMM_DTYPE_BF16) return GEMM_OK;
-  char buf[96];
-  std::snprintf(buf, sizeof buf, "dtype code %d is neither f16 (0) nor bf16 (1)", dtype);
-  return fail(GEMM_ERR_UNSUPPORTED, buf);
-}
-int check_out_dtype(int dtype, int out) {
-  if (out == dtype || out == GEMM_DTYPE_F32) return GEMM_OK;
-  char buf[128];
-  std::snprintf(buf, sizeof buf, "result dtype code %d is neither the operands' (%d) nor f32 (%d)",
-                out, dtype, GEMM_DTYPE_F32);
-  return fail(GEMM_ERR_UNSUPPORTED, buf);
-}
-int check_act(int act) {
-  if (act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU) return GEMM_OK;
-  return bad("%s code %lld is not one of GEMM_ACT_* (0 to 4)", "activation", act);
-}
 
 // Widest staging load, in 16-bit elements, that an operand's base and row
 // pitch allow.
@@ -286,10 +212,11 @@ int choose_kernel(const LayerPlan& pl) {
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
-int plan_tiles(LayerPlan& pl, const char* op) {
+// forced: GEMM_LAYER_TILE counts.
+int plan_tiles(LayerPlan& pl, const char* op, bool forced = true) {
   LayerArgs& a = pl.a;
   pl.kernel = choose_kernel(pl);
-  if (const char* want = forced_layer_tile()) {
+  if (const char* want = forced ? forced_layer_tile() : nullptr) {
     int found = -1;
     for (int k = 0; k < NUM_LAYER_KERNELS; ++k)
       if (std::strcmp(want, kLayerKernels[k].name) == 0) found = k;
@@ -343,7 +270,7 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
                  const int32_t* offsets, const void* A, int64_t lda, const void* B, int64_t ldb,
                  int64_t stride_b, const void* bias, int act, const void* R, int64_t ldr,
                  const void* Y, int64_t ldy, int out_dtype, const void* Z, int64_t ldz,
-                 LayerPlan& pl, bool& noop) {
+                 LayerPlan& pl, bool& noop, bool forced = true) {
   const bool dense = G < 0;
   noop = false;
   CHECK(check_dim("M", M));
@@ -425,7 +352,7 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
   a.a_direct = layer_direct(ma, ta ? M : K);
   a.b_direct = layer_direct(mb, tb ? K : N);
   pl.direct = a.a_direct && a.b_direct;
-  return plan_tiles(pl, dense ? "linear" : "grouped");
+  return plan_tiles(pl, dense ? "linear" : "grouped", forced);
 }
 
 int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t* offsets,
@@ -492,41 +419,7 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
   return plan_tiles(pl, "grad_weight");
 }
 
-int check_groups(int64_t G) {
-  if (G < 0) return bad("negative number of groups: %s=%lld", "G", G);
-  if (G > kMaxGroups) return fail(GEMM_ERR_UNSUPPORTED, "G exceeds 65535");
-  return GEMM_OK;
-}
-
-int launched(hipError_t e) {
-  if (e == hipSuccess) return GEMM_OK;
-  return fail(GEMM_ERR_HIP, std::string("kernel launch failed: ") + hipGetErrorString(e));
-}
-
-// Runs one entry point's work between the thread's state and the log, and
-// keeps C++ exceptions (a failed allocation of a message) from crossing the C
-// boundary.
-template <class F>
-int entry(const char* op, int64_t M, int64_t N, int64_t K, F work) noexcept {
-  try {
-    begin_call();
-    const int st = work();
-    log_layer_call(op, M, N, K, st);
-    return st;
-  } catch (...) {
-    return GEMM_ERR_HIP;
-  }
-}
-
 // ------------------------------------------------------------- rows and ids --
-int check_workspace(const void* ws, int64_t have, int64_t need) {
-  if (need == 0) return GEMM_OK;
-  if (have < need) return bad("%s of %lld bytes is smaller than the %lld needed", "workspace", have, need);
-  if (!ws) return fail(GEMM_ERR_INVALID_ARG, "workspace is NULL");
-  if ((uintptr_t)ws % 16) return fail(GEMM_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
-  return GEMM_OK;
-}
-
 int64_t act_grad_bytes(int64_t G, int64_t M, int64_t N) {
   if (G < 0 || M < 0 || N < 0 || G > kMaxGroups || M > kMaxDim || N > kMaxDim) return 0;
   const int64_t rows = act_grad_rows(M, N);
@@ -544,21 +437,6 @@ int64_t route_bytes(int64_t T, int64_t top, int64_t E) {
   return blocks > 1 ? (int64_t)blocks * (E + 1) * 4 : 0;
 }
 
-int check_choices(int64_t T, int64_t top) {
-  CHECK(check_dim("T", T));
-  CHECK(check_dim("top", top));
-  if (T * top > kMaxDim) return fail(GEMM_ERR_UNSUPPORTED, "T * top exceeds 2^31-1024");
-  return GEMM_OK;
-}
-int check_rowtype(int dtype, int& rowtype, int& elem) {
-  rowtype = dtype == GEMM_DTYPE_F32 ? ROW_F32 : dtype == GEMM_DTYPE_F16 ? ROW_F16 : ROW_BF16;
-  elem = dtype == GEMM_DTYPE_F32 ? 4 : 2;
-  if (dtype == GEMM_DTYPE_F32) return GEMM_OK;
-  if (dtype == GEMM_DTYPE_F16 || dtype == GEMM_DTYPE_BF16) return GEMM_OK;
-  char buf[96];
-  std::snprintf(buf, sizeof buf, "dtype code %d is none of f16 (0), bf16 (1), f32 (6)", dtype);
-  return fail(GEMM_ERR_UNSUPPORTED, buf);
-}
 // Elements per access that H and every matrix's base and pitch allow, at most
 // 16 bytes.
 template <size_t n>
@@ -578,6 +456,16 @@ int check_span(int64_t blocks) {
 }
 
 }  // namespace
+
+int run_dense(const DenseCall& c, bool launch, hipStream_t s) {
+  LayerPlan pl;
+  bool noop;
+  CHECK(plan_product(-1, c.M, c.N, c.K, c.dtype, c.ta, c.tb, nullptr, c.A, c.lda, c.B, c.ldb, 0,
+                     nullptr, GEMM_ACT_NONE, c.R, c.ldr, c.Y, c.ldy, c.out_dtype, nullptr, 0, pl, noop,
+                     false));
+  return noop || !launch ? GEMM_OK : launched(launch_product(pl, s));
+}
+
 }  // namespace dgt
 
 using namespace dgt;

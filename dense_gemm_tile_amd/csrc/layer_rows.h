@@ -10,14 +10,17 @@ namespace dgt {
 // n workgroups as a grid. A launch holds less than 2^32 threads along a
 // dimension (and one of more computes a part without an error), so further
 // workgroups go along z, the last of them in part past n. grid_x: workgroups of
-// one z, which the kernel gets among its arguments (layer_block() in
-// layer_rows.hip): the built-in is a hidden argument more for every launch.
+// one z, which the kernel gets among its arguments (layer_block()): the built-in is a hidden argument more for every launch.
 inline dim3 layer_grid(int64_t n, unsigned threads, unsigned& grid_x, unsigned y = 1) {
   const int64_t most = ((int64_t{1} << 32) - 1) / threads;
   const int64_t z = (n + most - 1) / most;
   grid_x = (unsigned)((n + z - 1) / z);
   return dim3(grid_x, y, (unsigned)z);
 }
+
+// This workgroup's index in a layer_grid().
+template <class Args>
+__device__ __forceinline__ unsigned layer_block(const Args& p) { return blockIdx.z * p.grid_x + blockIdx.x; }
 
 // Element types of rows.
 enum RowType : int { ROW_F16 = 0, ROW_BF16 = 1, ROW_F32 = 2 };

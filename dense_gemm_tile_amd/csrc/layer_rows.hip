@@ -9,10 +9,6 @@ namespace dgt {
 
 namespace {
 
-// This workgroup's index in a layer_grid().
-template <class Args>
-__device__ __forceinline__ unsigned layer_block(const Args& p) { return blockIdx.z * p.grid_x + blockIdx.x; }
-
 // ------------------------------------------------- activation and bias grads --
 // dZ = dY * act'(Z), and sums of dZ over rows before it is rounded. dZ itself is
 // rounded to the layer's type, since the matrix cores take 16-bit operands: dX and

@@ -3,7 +3,9 @@
  * (libdense_gemm_tile_amd.so): the matrix product with bias, activation and
  * residual in its epilogue, its gradients, and the same layer with one weight
  * matrix per expert: tokens sorted by expert, their rows sent out and joined
- * again, and the experts' products.
+ * again, and the experts' products. Around them: the layer norm before a layer,
+ * the gate that chooses the experts, products whose weights are held in 4 bits,
+ * and the cross entropy of the output layer.
  *
  * Conventions are those of dense_gemm_tile.h: row-major matrices, leading
  * dimensions in elements, device pointers owned by the caller, work enqueued
@@ -47,6 +49,10 @@ extern "C" {
 #define GEMM_ACT_GELU 2
 #define GEMM_ACT_GELU_ERF 3
 #define GEMM_ACT_SILU 4
+
+/* Scores of gemm_gate. */
+#define GEMM_SCORE_SOFTMAX 0
+#define GEMM_SCORE_SIGMOID 1
 
 /*
  * gemm_linear: Z = op(A) @ op(B) + bias,  Y = act(Z) + R.
@@ -181,6 +187,171 @@ GEMM_API int gemm_combine(int64_t T, int64_t top, int64_t H, int dtype, const vo
 GEMM_API int gemm_combine_grad(int64_t T, int64_t top, int64_t H, int dtype, const void* dY, int64_t lddy,
                       const void* Ys, int64_t ldys, const int32_t* slot, const float* weights,
                       void* dYs, int64_t lddys, float* dweights, void* stream);
+
+/*
+ * gemm_norm: Y = (X - mean) * rstd * gamma + beta for each row, where mean is
+ * the row's mean and rstd = 1 / sqrt(mean of (X - mean)^2 + eps).
+ *
+ * X, Y      M x N of `dtype` (f16, bf16 or GEMM_DTYPE_F32), N >= 1. Y may be X
+ *           itself (same pointer and leading dimension).
+ * gamma     N values of `dtype`, or NULL for ones. beta: the same, or NULL for
+ *           zeros.
+ * eps       finite and >= 0.
+ * mean,     M float32 values each, written when not NULL (kept for the backward
+ * rstd      pass).
+ */
+GEMM_API int gemm_norm(int64_t M, int64_t N, int dtype, const void* X, int64_t ldx,
+                  const void* gamma, const void* beta, float eps, void* Y, int64_t ldy,
+                  float* mean, float* rstd, void* stream);
+
+/*
+ * gemm_norm_grad: the gradients of gemm_norm from dY. With U = (X - mean) * rstd
+ * and H = dY * gamma,
+ *   dX = rstd * (H - mean of H - U * mean of (H * U)) + R
+ *   dgamma = sum over the rows of dY * U,   dbeta = sum over the rows of dY
+ * in float32, the rows in an order that does not depend on the run.
+ *
+ * R         M x N of `dtype` that is added to dX (the gradient that goes past
+ *           the norm on a residual stream), or NULL.
+ * dX        NULL when only dgamma and dbeta are wanted; may be dY, X or R itself
+ *           (same pointer and leading dimension).
+ * dgamma,   N values each, or NULL when not wanted.
+ * dbeta
+ * workspace gemm_norm_grad_workspace(M, N) bytes on the device, 16-byte aligned,
+ *           used until the call's work has run (not read or written when dgamma
+ *           and dbeta are both NULL).
+ */
+GEMM_API int gemm_norm_grad(int64_t M, int64_t N, int dtype, const void* dY, int64_t lddy,
+                  const void* X, int64_t ldx, const void* gamma, const float* mean,
+                  const float* rstd, const void* R, int64_t ldr, void* dX, int64_t lddx,
+                  float* dgamma, float* dbeta, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* Bytes of workspace that gemm_norm_grad needs; 0 for sizes it refuses. */
+GEMM_API int64_t gemm_norm_grad_workspace(int64_t M, int64_t N);
+
+/*
+ * gemm_gate: the `top` experts of each of T tokens, and their weights, from the
+ * logits L (T x E of `dtype`: f16, bf16 or GEMM_DTYPE_F32).
+ *
+ * score     GEMM_SCORE_SOFTMAX: s[t] = softmax(L[t]); GEMM_SCORE_SIGMOID: s =
+ *           1 / (1 + exp(-L)).
+ * bias      E float32 values, or NULL for none. Experts are compared by their
+ *           key, s + bias; the weights do not contain the bias.
+ * groups    >= 1, divides E. Experts form `groups` groups of neighbours. A
+ *           group's rank is the sum of its group_top (1 or 2) largest keys, and
+ *           only the experts of the top_groups best groups are chosen from.
+ *           groups == 1: all of them (top_groups and group_top are 1).
+ * top       experts a token, at most top_groups * (E / groups), and at most 64.
+ * renorm    != 0: the weights of a token's choices are divided by their sum
+ *           (where that is 0 they stay 0).
+ * scale     a factor of every weight.
+ *   ids[T * top]      the chosen experts, by falling key; equal ones by rising
+ *                     number (of groups too)
+ *   weights[T * top]  scale * s[ids], renormalised if wanted
+ *
+ * Keys are compared as they come out in 64 bits, so that a choice does not hang
+ * on a rounding. An expert whose logit or bias is -infinity is masked: it is not
+ * chosen, and adds nothing to its group's rank (a group of masked experts ranks
+ * last). Choices that a token has no expert left for are dropped: id -1 and
+ * weight 0, which gemm_route, gemm_combine and gemm_gate_grad leave out. NaN
+ * ranks below every number and above masked experts, and reaches the weights.
+ *
+ * E is at most 1024.
+ */
+GEMM_API int gemm_gate(int64_t T, int64_t E, int64_t top, int dtype, const void* L, int64_t ldl,
+                  int score, const float* bias, int64_t groups, int64_t top_groups,
+                  int64_t group_top, int renorm, float scale, int32_t* ids, float* weights,
+                  void* stream);
+
+/*
+ * gemm_gate_grad: dL (T x E of `dtype`), the gradient of L from the gradients
+ * dweights of gemm_gate's weights, for the choices in ids. An id outside [0, E)
+ * is a dropped choice, whose gradient is not read; a token without choices gets
+ * zeros. The gradient does not depend on the bias and the groups except through
+ * ids. dL may be L itself (same pointer and leading dimension).
+ */
+GEMM_API int gemm_gate_grad(int64_t T, int64_t E, int64_t top, int dtype, const void* L,
+                  int64_t ldl, int score, int renorm, float scale, const int32_t* ids,
+                  const float* dweights, void* dL, int64_t lddl, void* stream);
+
+/*
+ * gemm_linear_w4: Y = act(A @ W^T + bias) + R with 4-bit weights,
+ *   W[n][k] = scales[n][k / group] * (code[n][k] - zeros[n][k / group]).
+ *
+ * A         M x K of `dtype` (f16 or bf16).
+ * B         the codes, 0 to 15, two to a byte: code[n][k] is the lower (k even)
+ *           or upper half (k odd) of byte k / 2 of row n. ldb: codes from one
+ *           row to the next, even, at least K.
+ * scales    N x ceil(K / group) values of `dtype`, leading dimension lds.
+ * zeros     the same for the zero points (any values, 7.5 as well as 8), or NULL
+ *           for 8 everywhere.
+ * group     codes that share a scale: a multiple of 32.
+ * bias, act, R, Y, out_dtype: as in gemm_linear. K == 0 leaves act(bias) + R.
+ *
+ * The codes' products are summed group by group in float32, and each group's sum
+ * is scaled in float32: no weight is rounded.
+ */
+GEMM_API int gemm_linear_w4(int64_t M, int64_t N, int64_t K, int dtype, const void* A, int64_t lda,
+                  const void* B, int64_t ldb, const void* scales, const void* zeros, int64_t lds,
+                  int64_t group, const void* bias, int act, const void* R, int64_t ldr, void* Y,
+                  int64_t ldy, int out_dtype, void* stream);
+
+/*
+ * gemm_grouped_w4: gemm_linear_w4 with one W (and bias) per group of consecutive
+ * rows, as gemm_grouped is to gemm_linear: G groups, offsets, M rows.
+ *
+ * stride_b  codes from one group's B to the next (even; 0: one for all).
+ * stride_s  elements from one group's scales, and zeros, to the next.
+ */
+GEMM_API int gemm_grouped_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dtype,
+                  const int32_t* offsets, const void* A, int64_t lda, const void* B, int64_t ldb,
+                  int64_t stride_b, const void* scales, const void* zeros, int64_t lds,
+                  int64_t stride_s, int64_t group, const void* bias, int act, const void* R,
+                  int64_t ldr, void* Y, int64_t ldy, int out_dtype, void* stream);
+
+/*
+ * gemm_loss: cross entropy of an output layer, for T tokens and a vocabulary of
+ * V: with the logits L = X @ W^T,
+ *   lse[t] = log(sum over v of exp(L[t][v])),   loss[t] = lse[t] - L[t][labels[t]].
+ * The logits are made in pieces and not kept.
+ *
+ * X         T x H, W: V x H, of `dtype` (f16 or bf16). H == 0: all logits are 0.
+ * labels    T int32. A token whose label is outside [0, V) has the loss 0.
+ * loss, lse T float32 values each; lse is written when not NULL (gemm_loss_grad
+ *           reads it).
+ * V         >= 1.
+ * workspace gemm_loss_workspace(T, V, H) bytes on the device, 16-byte aligned,
+ *           used until the call's work has run.
+ */
+GEMM_API int gemm_loss(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t ldx,
+                  const void* W, int64_t ldw, const int32_t* labels, float* loss, float* lse,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that gemm_loss needs; 0 for sizes it refuses. */
+GEMM_API int64_t gemm_loss_workspace(int64_t T, int64_t V, int64_t H);
+
+/*
+ * gemm_loss_grad: the gradients of gemm_loss from dloss (T float32). With
+ *   G[t][v] = dloss[t] * (exp(L[t][v] - lse[t]) - (v == labels[t]))
+ * (0 for a token whose label is outside [0, V), whose dloss is not read),
+ *   dX = G @ W,   dW = G^T @ X.
+ * The logits are made again in pieces of the vocabulary, and G is rounded to
+ * `dtype`, as the matrix cores read it, before its two products: an f16 call
+ * wants a dloss that carries the training's loss scale.
+ *
+ * dX        T x H of `dtype`, or NULL when not wanted.
+ * dW        V x H of dw_dtype (`dtype` or GEMM_DTYPE_F32), or NULL when not
+ *           wanted. accumulate != 0 adds to what dW holds.
+ * workspace gemm_loss_grad_workspace(T, V, H) bytes, as above.
+ */
+GEMM_API int gemm_loss_grad(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t ldx,
+                  const void* W, int64_t ldw, const int32_t* labels, const float* lse,
+                  const float* dloss, void* dX, int64_t lddx, void* dW, int64_t lddw, int dw_dtype,
+                  int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that gemm_loss_grad needs; 0 for sizes it refuses. */
+GEMM_API int64_t gemm_loss_grad_workspace(int64_t T, int64_t V, int64_t H);
 
 #ifdef __cplusplus
 }
