@@ -133,15 +133,21 @@ template <class T>
 struct same_type {
   using type = T;
 };
+// lds: bytes of LDS beside what the kernel itself declares.
 template <class... P>
-inline hipError_t launch_kernel(void (*k)(P...), dim3 grid, dim3 block, hipStream_t s,
-                                typename same_type<P>::type... args) {
+inline hipError_t launch_kernel_lds(void (*k)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                                    typename same_type<P>::type... args) {
   const uint64_t most = 0xffffffffu;
   if ((uint64_t)grid.x * block.x > most || (uint64_t)grid.y * block.y > most ||
       (uint64_t)grid.z * block.z > most)
     return hipErrorInvalidConfiguration;
   void* argv[] = {static_cast<void*>(&args)...};
-  return hipLaunchKernel(reinterpret_cast<const void*>(k), grid, block, argv, 0, s);
+  return hipLaunchKernel(reinterpret_cast<const void*>(k), grid, block, argv, lds, s);
+}
+template <class... P>
+inline hipError_t launch_kernel(void (*k)(P...), dim3 grid, dim3 block, hipStream_t s,
+                                typename same_type<P>::type... args) {
+  return launch_kernel_lds(k, grid, block, 0, s, args...);
 }
 
 // Launchers (defined next to their kernels). They return the HIP status of

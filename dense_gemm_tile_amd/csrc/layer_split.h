@@ -34,6 +34,30 @@ __device__ __forceinline__ int split_start(int column_tile, int KT) {
   return (int)(((uint64_t)((unsigned)column_tile * 0x9E3779B1u) * (unsigned)KT) >> 32);
 }
 
+// A slice of an operand stored along K: 16 T rows of 64 K values, 128 bytes each
+// in LDS. Chunk c (8 values) of row r sits at chunk c ^ swz(r), the conflict-free
+// swizzle of gemm_mfma_pingpong.h's 16-wide atom. Of the rows 8 L are loaded.
+template <int T, int L = 2 * T>
+struct SplitAlong {
+  static constexpr int LOADS = L;
+  using Op = PpOperand<false, T, 16>;
+  // rs starts at the tile's first row; `rows` and `K` are left of the operand.
+  __device__ static __forceinline__ void request(const __amdgpu_buffer_rsrc_t& rs, int ld2,
+                                                 int rows, int K, int slice, char* lds, int lane) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int r = 8 * i + (lane >> 3), k = slice * 64 + 8 * ((lane & 7) ^ Op::swz(r));
+      const int off = r < rows && k < K ? r * ld2 + k * 2 : kOutOfRange;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (pp_lds_ptr_t)(lds + i * 1024), 16, off, 0, 0, 0);
+    }
+  }
+  // The fragment of rows 16 t .. +15, K values 32 h .. +31 of the slice.
+  __device__ static __forceinline__ u32x4 read(const char* lds, int t, int h, int lane) {
+    return *reinterpret_cast<const u32x4*>(
+        lds + Op::lds_off(16 * t + SplitAtom::frag_row(lane), 4 * h + SplitAtom::frag_koct(lane)));
+  }
+};
+
 // A workgroup of KW waves, each with sums of its own part of K for the same
 // 16 MT x 16 NT outputs: they meet in LDS, are added in wave order, and go
 // through the epilogue.

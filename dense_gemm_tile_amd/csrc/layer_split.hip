@@ -26,30 +26,6 @@ __device__ __forceinline__ void split_wait(int n) {
   layer_fixed_order();
 }
 
-// A slice of an operand stored along K: 16 T rows of 64 K values, 128 bytes each
-// in LDS. Chunk c (8 values) of row r sits at chunk c ^ swz(r), the conflict-free
-// swizzle of gemm_mfma_pingpong.h's 16-wide atom.
-template <int T>
-struct SplitAlong {
-  static constexpr int LOADS = 2 * T;
-  using Op = PpOperand<false, T, 16>;
-  // rs starts at the tile's first row; `rows` and `K` are left of the operand.
-  __device__ static __forceinline__ void request(const __amdgpu_buffer_rsrc_t& rs, int ld2,
-                                                 int rows, int K, int slice, char* lds, int lane) {
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int r = 8 * i + (lane >> 3), k = slice * 64 + 8 * ((lane & 7) ^ Op::swz(r));
-      const int off = r < rows && k < K ? r * ld2 + k * 2 : kOutOfRange;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (pp_lds_ptr_t)(lds + i * 1024), 16, off, 0, 0, 0);
-    }
-  }
-  // The fragment of rows 16 t .. +15, K values 32 h .. +31 of the slice.
-  __device__ static __forceinline__ u32x4 read(const char* lds, int t, int h, int lane) {
-    return *reinterpret_cast<const u32x4*>(
-        lds + Op::lds_off(16 * t + SplitAtom::frag_row(lane), 4 * h + SplitAtom::frag_koct(lane)));
-  }
-};
-
 // A slice of B stored [K][N]: 64 K rows of 16 NT columns (32 NT bytes) in LDS.
 // Chunk c (8 columns) of row r sits at chunk c ^ swz(r), so that the rows 0-3
 // and 8-11 that 32 lanes of a transposed read name lie in different banks.

@@ -1,0 +1,8 @@
+// Products of f16 values with 4-bit weights (layer_w4.h).
+#include "layer_w4.h"
+
+namespace dgt {
+
+hipError_t launch_w4_f16(const W4Args& p, hipStream_t s) { return launch_modes<TagF16>(p, s); }
+
+}  // namespace dgt
