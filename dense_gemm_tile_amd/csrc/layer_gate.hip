@@ -5,9 +5,12 @@
 //   groups by the sum of their group_top largest keys, experts of the best groups by
 //   key;  w = scale s[id]  (renorm: / sum of the chosen s)
 //
-// A wave takes a token; lane l holds experts l, l + 64, ... Keys are compared as
-// integers that order as the numbers do, with a place for NaN (1) and for masked
-// experts (0) below them.
+// A wave takes a token. Choices are whole numbers and must not hang on a rounding, so
+// keys count as they are in 64 bits; in 64 bits throughout, the exponentials and the
+// search take most of the time (16384 tokens, 8 of 256 experts in groups, with the
+// gradient: 68 us, 20 so). So keys are made and searched in float32, with a bound
+// of their error, and a token two of whose keys come too close for it is done again in
+// 64 bits.
 #include "layer.h"
 #include "layer_checks.h"
 
@@ -25,6 +28,8 @@ struct GateArgs {
   int64_t ldl;
   int T, E, top, score;
   int groups, top_groups, group_top, renorm;
+  int lanes;            // 1 << lanes lanes hold a group
+  int bits;             // that number an expert
   float scale;
   unsigned grid_x;
 };
@@ -40,16 +45,23 @@ struct GateGradArgs {
 };
 
 struct GateF32 {};
+template <class Row>
+struct GateElemOf { using type = unsigned short; };
+template <>
+struct GateElemOf<GateF32> { using type = float; };
+template <class Row>
+using GateElem = typename GateElemOf<Row>::type;
+__device__ __forceinline__ float gate_float(GateF32, float v) { return v; }
+template <class Tag>
+__device__ __forceinline__ float gate_float(Tag t, unsigned short v) { return layer_f32(t, v); }
 __device__ __forceinline__ float gate_load(GateF32, const void* p, int64_t at) { return static_cast<const float*>(p)[at]; }
 template <class Tag>
 __device__ __forceinline__ float gate_load(Tag t, const void* p, int64_t at) {
   return layer_f32(t, static_cast<const unsigned short*>(p)[at]);
 }
-__device__ __forceinline__ void gate_store(GateF32, void* p, int64_t at, float v) { static_cast<float*>(p)[at] = v; }
+__device__ __forceinline__ float gate_elem(GateF32, float v) { return v; }
 template <class Tag>
-__device__ __forceinline__ void gate_store(Tag t, void* p, int64_t at, float v) {
-  static_cast<unsigned short*>(p)[at] = layer_16(t, v);
-}
+__device__ __forceinline__ unsigned short gate_elem(Tag t, float v) { return layer_16(t, v); }
 
 template <class T>
 __device__ __forceinline__ T gate_wave_sum(T v) {
@@ -74,27 +86,55 @@ __device__ __forceinline__ uint64_t gate_order(double v) {
   return u >> 63 ? ~u : u | ((uint64_t)1 << 63);
 }
 
+// Reductions over groups of 16 or of all 64 lanes, by lane swaps; every lane gets the result.
+template <int CTRL>
+__device__ __forceinline__ unsigned gate_swap(unsigned v) {
+  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int LANES, class F>
+__device__ __forceinline__ unsigned gate_reduce(unsigned v, F join) {
+  static_assert(LANES == 16 || LANES == 64, "");
+  v = join(v, gate_swap<0xB1>(v));   // lanes 1 0 3 2 of each 4
+  v = join(v, gate_swap<0x4E>(v));   // 2 3 0 1
+  v = join(v, gate_swap<0x141>(v));  // 8 lanes mirrored
+  v = join(v, gate_swap<0x140>(v));  // 16 lanes mirrored
+  if constexpr (LANES == 64) {
+    const auto h = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = join(h[0], h[1]);
+    const auto w = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = join(w[0], w[1]);
+  }
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ unsigned gate_max32(unsigned v) {
+  return gate_reduce<LANES>(v, [](unsigned a, unsigned b) { return a > b ? a : b; });
+}
+template <int LANES>
+__device__ __forceinline__ float gate_sum32(float v) {
+  return __builtin_bit_cast(float, gate_reduce<LANES>(__builtin_bit_cast(unsigned, v), [](unsigned a, unsigned b) {
+    return __builtin_bit_cast(unsigned, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+  }));
+}
 // The largest of the wave's keys, and of equal ones the first; every lane gets both.
 struct GateBest {
   uint64_t key;
   int at;
 };
 __device__ __forceinline__ GateBest gate_best(GateBest b) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t k = __shfl_xor((unsigned long long)b.key, d, 64);
-    const int at = __shfl_xor(b.at, d, 64);
-    if (k > b.key || (k == b.key && at < b.at)) b = {k, at};
-  }
-  return b;
+  const unsigned high = gate_max32<64>((unsigned)(b.key >> 32));
+  const unsigned low = gate_max32<64>((unsigned)(b.key >> 32) == high ? (unsigned)b.key : 0u);
+  const uint64_t key = (uint64_t)high << 32 | low;
+  const unsigned at = ~gate_max32<64>(b.key == key ? ~(unsigned)b.at : 0u);
+  return {key, (int)at};
 }
 
+// The choices of token t in 64 bits: lane j gets the id and the score of choice j (-1 and 0
+// past the last). Lane l holds experts l, l + 64, ... all: 2 * 64 * PER numbers of LDS,
+// this wave's own (GROUPS).
 template <class Row, int PER, bool GROUPS>
-__global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
-  __shared__ uint64_t lds[GROUPS ? 4 * 2 * 64 * PER : 1];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t t = (int64_t)layer_block(p) * 4 + w;
-  if (t >= p.T) return;
+__device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, uint64_t* all, int& id, double& weight) {
+  const int lane = threadIdx.x & 63;
   double s[PER];
   uint64_t key[PER];
   // Scores.
@@ -130,7 +170,6 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   }
   if constexpr (GROUPS) {
     // Each lane ranks groups lane, lane + 64, ... from the keys in LDS.
-    uint64_t* const all = lds + w * 2 * 64 * PER;
     uint64_t* const rank = all + 64 * PER;
     const int size = p.E / p.groups;
 #pragma unroll
@@ -138,6 +177,7 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     layer_wave_order();
     for (int g = lane; g < p.groups; g += 64) {
       uint64_t a = 0, b = 0;
+#pragma unroll 4
       for (int e = g * size; e < (g + 1) * size; ++e) {
         const uint64_t k = all[e];
         if (k > a) {
@@ -172,9 +212,9 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
       if (e < p.E && rank[e / size] != ~(uint64_t)0) key[i] = kGateMasked;
     }
   }
-  // Choices in falling order: lane j keeps choice j.
-  int id = -1;
-  double weight = 0;
+  // Choices in falling order.
+  id = -1;
+  weight = 0;
   for (int j = 0; j < p.top; ++j) {
     GateBest b = {kGateMasked, 0x7fffffff};
     double v = 0;
@@ -195,13 +235,260 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     for (int i = 0; i < PER; ++i)
       if (b.at == i * 64 + lane) key[i] = kGateMasked;
   }
-  if (p.renorm) {
-    const double sum = gate_wave_sum(weight);
-    weight = sum == 0 ? 0 : weight / sum;
+}
+
+// Numbers as integers of the same order (NaN has no place).
+__device__ __forceinline__ unsigned gate_order32(float v) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float gate_value32(unsigned k) {
+  return __builtin_bit_cast(float, k >> 31 ? k & 0x7fffffffu : ~k);
+}
+// PER elements of `size` neighbouring ones, shared by LANES lanes four at a time: item i of
+// lane `in` is element 4 (i / 4 LANES + in) + i % 4.
+__device__ __forceinline__ int gate_item(int i, int lanes, int in) { return 4 * ((i >> 2) * lanes + in) + (i & 3); }
+template <class Row>
+struct __attribute__((packed, aligned(sizeof(GateElem<Row>)))) GateFour {
+  GateElem<Row> e[4];
+};
+template <class Row, int PER>
+__device__ __forceinline__ void gate_load_row(const void* p, int64_t at, int lanes, int in, int size, float none,
+                                              float (&f)[PER]) {
+  static_assert(PER % 4 == 0, "whole fours");
+#pragma unroll
+  for (int i = 0; i < PER; i += 4) {
+    const int first = gate_item(i, lanes, in);
+    if (first + 4 <= size) {
+      const auto v = *reinterpret_cast<const GateFour<Row>*>(static_cast<const GateElem<Row>*>(p) + at + first);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[i + e] = gate_float(Row{}, v.e[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[i + e] = first + e < size ? gate_load(Row{}, p, at + first + e) : none;
+    }
   }
+}
+template <class Row, int PER>
+__device__ __forceinline__ void gate_store_row(void* p, int64_t at, int lanes, int in, int size, const float (&f)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; i += 4) {
+    const int first = gate_item(i, lanes, in);
+    if (first + 4 <= size) {
+      GateFour<Row> v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.e[e] = gate_elem(Row{}, f[i + e]);
+      *reinterpret_cast<GateFour<Row>*>(static_cast<GateElem<Row>*>(p) + at + first) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (first + e < size) static_cast<GateElem<Row>*>(p)[at + first + e] = gate_elem(Row{}, f[i + e]);
+    }
+  }
+}
+
+// The float32 search. LANES lanes take a token (four tokens a wave, or one). A key is an
+// integer of the float32 key's order; the largest one below the last choice is the largest of
+// (key - last) as unsigned numbers, so nothing is removed. Its lowest bits say whose it
+// is, in place of a search:
+//   ranked by logits (without a bias their order is the scores'): the expert's number from
+//     behind, so that keys of a token differ and of equal logits the first expert's is
+//     larger. Exact for 16-bit logits, which have zeros there, and for float32 ones that
+//     differ above these bits.
+//   ranked by scores: the lane's item from behind; the lane is the one that has the key.
+//     Two keys next to each other in the order have to be further apart than their errors: a
+//     score's, relative, of 2^-21 (sigmoid: an exponential, an addition and a division, one or
+//     half a step each) or 2^-17 (softmax: the largest logit taken off first, half a step of
+//     a number below 128 where the score is not 0 to float32, 2^-18; the sum, whose
+//     additions one after the other are PER + 6 at most), half a step more for the bias, and
+//     for the lowest bits 2^-19 or, of a group's rank, 2^-17.
+// (Experts' numbers in the lowest bits of scores too: one token in ten of the case above
+// was too close, 54 us for the choices alone.)
+template <class Row, int LANES, int PER, bool GROUPS>
+__global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
+  constexpr int WIDE = 64 / LANES;                     // tokens a wave
+  constexpr int PER64 = PER / WIDE > 0 ? PER / WIDE : 1;
+  __shared__ uint64_t lds[GROUPS ? 4 * 2 * 64 * PER64 : 1];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane & (LANES - 1);
+  const int64_t t0 = ((int64_t)layer_block(p) * 4 + w) * WIDE;
+  if (t0 >= p.T) return;
+  const int64_t mine = t0 + lane / LANES, t = mine < p.T ? mine : p.T - 1;  // (the last token again past it)
+  const bool soft = p.score == GEMM_SCORE_SOFTMAX;
+  const bool scored = p.bias || (GROUPS && p.group_top > 1);
+  // The group that this lane holds a part of.
+  const int lanes = GROUPS ? 1 << p.lanes : LANES, group = GROUPS ? li >> p.lanes : 0;
+  const int in = GROUPS ? li & (lanes - 1) : li;
+  const int size = GROUPS ? (group < p.groups ? p.E / p.groups : 0) : p.E, first = GROUPS ? group * (p.E / p.groups) : 0;
+  const unsigned low = scored ? PER - 1 : (1u << p.bits) - 1;
+  const float inf = __builtin_inff();
+
+  float l[PER];
+  gate_load_row<Row, PER>(p.L, t * p.ldl + first, lanes, in, size, -inf, l);
+  unsigned key[PER];
+  bool close = false, odd = false;
+  float top = -inf, sum = 0.0f, bmax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) odd |= soft ? !(l[i] < inf) : l[i] != l[i];
+  if (soft && (scored || !p.renorm)) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = l[i] > top ? l[i] : top;
+    top = gate_value32(gate_max32<LANES>(gate_order32(top)));
+    const float base = top == -inf ? 0.0f : top;
+    float s[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      s[i] = expf(l[i] - base);
+      sum += s[i];
+    }
+    sum = gate_sum32<LANES>(sum);
+    if (scored) {
+      const float inv = 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) s[i] = l[i] == -inf ? -inf : s[i] * inv;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) l[i] = s[i];
+    }
+  } else if (scored) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = l[i] == -inf ? -inf : 1.0f / (1.0f + expf(-l[i]));
+  }
+  if (p.bias) {
+    float b[PER];
+    gate_load_row<GateF32, PER>(p.bias, first, lanes, in, size, -inf, b);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool masked = l[i] == -inf || b[i] == -inf;
+      odd |= !masked && !(__builtin_fabsf(b[i]) < inf);
+      l[i] = masked ? -inf : l[i] + b[i];
+      bmax = !masked && __builtin_fabsf(b[i]) > bmax ? __builtin_fabsf(b[i]) : bmax;
+    }
+    bmax = gate_value32(gate_max32<LANES>(gate_order32(bmax)));
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)  // (+ 0: -0 is no other number)
+    key[i] = l[i] == -inf ? 0u : (gate_order32(l[i] + 0.0f) & ~low) | (low - (scored ? i : first + gate_item(i, lanes, in)));
+  // Whether one key (or sum of keys) may not be above the next.
+  auto unsure = [&](unsigned a, unsigned b, unsigned rest, float share, float bias) {
+    if (!scored) return sizeof(GateElem<Row>) == 4 && ((a ^ b) & ~rest) == 0;
+    const float u = gate_value32(a & ~rest), v = gate_value32(b & ~rest);
+    return u - v <= share * (__builtin_fabsf(u) + __builtin_fabsf(v) + 2.0f * bias) + 1e-30f;
+  };
+  const float share = soft ? 0x1p-16f : 0x1.8p-19f;  // (of both keys: 2^-17 or 2^-21, 2^-24 and 2^-19)
+  if constexpr (GROUPS) {
+    // The group's two largest keys, in each of its lanes.
+    unsigned a = 0, b = 0;
+    auto enter = [&](unsigned k) {
+      const unsigned least = k < a ? k : a;
+      a = k > a ? k : a;
+      b = least > b ? least : b;
+    };
+#pragma unroll
+    for (int i = 0; i < PER; ++i) enter(key[i]);
+    auto join = [&](unsigned oa, unsigned ob) {
+      enter(oa);
+      enter(ob);
+    };
+    if (p.lanes > 0) join(gate_swap<0xB1>(a), gate_swap<0xB1>(b));
+    if (p.lanes > 1) join(gate_swap<0x4E>(a), gate_swap<0x4E>(b));
+    if (p.lanes > 2) join(gate_swap<0x141>(a), gate_swap<0x141>(b));
+    if (p.lanes > 3) join(gate_swap<0x140>(a), gate_swap<0x140>(b));
+    if (p.lanes > 4) join(__shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
+    if (scored && a) {  // the lowest bits: the group's number from behind
+      float r = gate_value32(a & ~low);
+      if (p.group_top > 1 && b) r += gate_value32(b & ~low);
+      a = (gate_order32(r + 0.0f) & ~63u) | (63u - group);
+    }
+    // The best groups' ranks, down to the last one that is kept, and the next.
+    unsigned rank = group < p.groups ? a : 0, last = ~0u;
+    const unsigned own = rank;
+    for (int j = 0; j < p.top_groups; ++j) {
+      const unsigned m = gate_max32<LANES>(rank);
+      last = m ? m : last;
+      rank = rank < m ? rank : 0;
+    }
+    const unsigned next = gate_max32<LANES>(rank);
+    close = next && unsure(last, next, scored ? 63u : low, share + 0x1p-16f, 2.0f * bmax);
+    if (own < last) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = 0;
+    }
+  }
+  // The choices, and one more that the last one must be clear of. Lane j keeps choice j.
+  constexpr uint64_t all = LANES == 64 ? ~(uint64_t)0 : ((uint64_t)1 << (LANES & 63)) - 1;
+  unsigned taken = 0;
+  int id = -1;
+  for (int j = 0; j <= p.top; ++j) {
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = key[i] - taken > m ? key[i] - taken : m;
+    // (Before the first: taken is 0 and m the largest key. Where none is left below taken, m is
+    // a difference to one above it.)
+    m += taken;
+    m = j > 0 && m >= taken ? 0 : m;
+    const unsigned best = gate_max32<LANES>(m);
+    if (j > 0) close |= best && unsure(taken, best, low, share, bmax);
+    int expert = low - (best & low);
+    if (scored) {
+      const uint64_t having = __ballot(m == best) >> (lane - li) & all;
+      close |= best && (having & (having - 1));  // (several: not decided here)
+      const int from = __builtin_ctzll(having), fin = GROUPS ? from & (lanes - 1) : from;
+      expert = (GROUPS ? (from >> p.lanes) * (p.E / p.groups) : 0) + gate_item(expert, lanes, fin);
+    }
+    if (j < p.top && li == j && best) id = expert;
+    taken = best ? best : 1;  // (nothing lies below 1)
+  }
+  // Weights. Renormalised softmax scores are the softmax of the chosen logits.
+  const bool chosen = id >= 0;
+  const float z = chosen ? gate_load(Row{}, p.L, t * p.ldl + id) : -inf;
+  float out = 0.0f;
+  if (!soft) {
+    out = 1.0f / (1.0f + expf(-z));
+  } else if (p.renorm) {
+    const float best = gate_value32(gate_max32<LANES>(chosen ? gate_order32(z) : 0u));
+    out = expf(z - best);
+  } else {
+    out = expf(z - top) / sum;
+  }
+  out = chosen ? out : 0.0f;
+  if (p.renorm) {
+    const float total = gate_sum32<LANES>(out);
+    close |= total < 1e-30f && gate_max32<LANES>(chosen) != 0u;  // (next to float32's smallest numbers)
+    out = chosen ? out / total : 0.0f;
+  }
+  // Tokens that float32 does not decide go through 64 bits.
+  const uint64_t again = __ballot(close || odd);
+  if (li < p.top && mine < p.T && (again >> (lane - li) & all) == 0) {
+    p.ids[t * p.top + li] = id;
+    p.weights[t * p.top + li] = out * p.scale;
+  }
+#pragma unroll
+  for (int u = 0; u < WIDE; ++u) {
+    if ((again >> (u * LANES) & all) == 0 || t0 + u >= p.T) continue;
+    int found;
+    double exact;
+    gate_in_64_bits<Row, PER64, GROUPS>(p, t0 + u, lds + w * 2 * 64 * PER64 * GROUPS, found, exact);
+    const double total = p.renorm ? gate_wave_sum(exact) : 1.0;
+    if (lane < p.top) {
+      p.ids[(t0 + u) * p.top + lane] = found;
+      p.weights[(t0 + u) * p.top + lane] = total == 0 ? 0.0f : (float)(exact / total * (double)p.scale);
+    }
+  }
+}
+
+// Every token in 64 bits: groups that no power of two of lanes holds.
+template <class Row>
+__global__ void __launch_bounds__(256) layer_gate_exact_kernel(const GateArgs p) {
+  __shared__ uint64_t lds[4 * 2 * 64 * 16];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t t = (int64_t)layer_block(p) * 4 + w;
+  if (t >= p.T) return;
+  int id;
+  double weight;
+  gate_in_64_bits<Row, 16, true>(p, t, lds + w * 2 * 64 * 16, id, weight);
+  const double total = p.renorm ? gate_wave_sum(weight) : 1.0;
   if (lane < p.top) {
     p.ids[t * p.top + lane] = id;
-    p.weights[t * p.top + lane] = (float)(weight * (double)p.scale);
+    p.weights[t * p.top + lane] = total == 0 ? 0.0f : (float)(weight / total * (double)p.scale);
   }
 }
 
@@ -211,16 +498,18 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
 //   sigmoid: dl_j = s_j (1 - s_j) ds_j
 // Renormalised softmax weights need the chosen logits alone: s_j / S is their own
 // softmax.
-template <class Row, int PER>
+template <class Row, int LANES, int PER>
 __global__ void __launch_bounds__(256) layer_gate_grad_kernel(const GateGradArgs p) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t t = (int64_t)layer_block(p) * 4 + w;
-  if (t >= p.T) return;
-  const int id = lane < p.top ? p.ids[t * p.top + lane] : -1;
-  float l = -__builtin_inff();
+  const int lane = threadIdx.x & 63, li = lane & (LANES - 1);
+  const int64_t t = ((int64_t)layer_block(p) * 4 + (threadIdx.x >> 6)) * (64 / LANES) + lane / LANES;
+  const bool there = t < p.T;
+  const int id = there && li < p.top ? p.ids[t * p.top + li] : -1;
+  const float inf = __builtin_inff();
+  float l = -inf;
   if ((unsigned)id < (unsigned)p.E) l = gate_load(Row{}, p.L, t * p.ldl + id);
-  const bool chosen = l != -__builtin_inff();  // (a masked one has the score 0, and no gradient)
-  const float g = chosen ? p.scale * p.dweights[t * p.top + lane] : 0.0f;
+  const bool chosen = l != -inf;  // (a masked one has the score 0, and no gradient)
+  const float g = chosen ? p.scale * p.dweights[t * p.top + li] : 0.0f;
+  const int size = there ? p.E : 0;
   float s = 0.0f, ds = g, d[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) d[i] = 0.0f;
@@ -228,59 +517,78 @@ __global__ void __launch_bounds__(256) layer_gate_grad_kernel(const GateGradArgs
     const float z = expf(-l), r = 1.0f / (1.0f + z);
     s = chosen ? r : 0.0f;
     if (p.renorm) {
-      const float sum = gate_wave_sum(s), mean = gate_wave_sum(g * s) / sum;
+      const float sum = gate_sum32<LANES>(s), mean = gate_sum32<LANES>(g * s) / sum;
       ds = sum == 0.0f ? 0.0f : (g - mean) / sum;
     }
     ds = chosen ? s * (l > 0.0f ? z * r : 1.0f - s) * ds : 0.0f;  // (1 - s = z / (1 + z))
   } else if (p.renorm) {
-    const float top = gate_wave_max(l);
+    const bool nan = l != l;
+    const float top = gate_value32(gate_max32<LANES>(nan ? 0u : gate_order32(l)));
     s = chosen ? expf(l - top) : 0.0f;
-    const float sum = gate_wave_sum(s);
+    const float sum = gate_sum32<LANES>(s);
     s = chosen ? s / sum : 0.0f;
-    const float mean = gate_wave_sum(g * s);  // (every lane takes part)
+    const float mean = gate_sum32<LANES>(g * s);  // (every lane takes part)
     ds = s * (g - mean);
   } else {
-    float top = -__builtin_inff(), sum = 0.0f, e[PER];
+    float top = -inf, sum = 0.0f, e[PER];
+    gate_load_row<Row, PER>(p.L, t * p.ldl, LANES, li, size, -inf, e);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = e[i] > top ? e[i] : top;
+    top = gate_value32(gate_max32<LANES>(gate_order32(top)));
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      e[i] = i * 64 + lane < p.E ? gate_load(Row{}, p.L, t * p.ldl + i * 64 + lane) : -__builtin_inff();
-      top = e[i] > top ? e[i] : top;
-    }
-    top = gate_wave_max(top);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      e[i] = e[i] == -__builtin_inff() ? 0.0f : expf(e[i] - top);
+      e[i] = e[i] == -inf ? 0.0f : expf(e[i] - top);
       sum += e[i];
     }
-    sum = gate_wave_sum(sum);
+    sum = gate_sum32<LANES>(sum);
     s = chosen ? expf(l - top) / sum : 0.0f;
-    const float mean = gate_wave_sum(g * s);
+    const float mean = gate_sum32<LANES>(g * s);
     ds = g * s;
 #pragma unroll
     for (int i = 0; i < PER; ++i) d[i] = sum == 0.0f ? 0.0f : -(e[i] / sum) * mean;
   }
   for (int j = 0; j < p.top; ++j) {
-    const int at = __shfl(id, j, 64);
-    const float v = __shfl(ds, j, 64);
+    // Choice j's place: item i of lane `in` of this token's lanes, if it is kept.
+    const int from = (lane & ~(LANES - 1)) + j;
+    const int at = __shfl(id, from, 64);
+    const float v = __shfl(ds, from, 64);
+    const int i0 = (at >> 2) / LANES * 4 + (at & 3);
+    const bool here = (unsigned)at < (unsigned)size && ((at >> 2) & (LANES - 1)) == li;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (at == i * 64 + lane && at < p.E) d[i] += v;
+      if (here && i0 == i) d[i] += v;
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (i * 64 + lane < p.E) gate_store(Row{}, p.dL, t * p.lddl + i * 64 + lane, d[i]);
+  gate_store_row<Row, PER>(p.dL, t * p.lddl, LANES, li, size, d);
 }
 
+// f(row, lanes, per) with the form of a call: 16 lanes a token where they hold its experts (and a
+// choice each), 64 otherwise.
 template <class F>
-hipError_t gate_for(int rowtype, int E, F f) {
-  auto per = [&](auto row) {
-    if (E <= 64) return f(row, LayerConst<1>{});
-    if (E <= 128) return f(row, LayerConst<2>{});
-    if (E <= 256) return f(row, LayerConst<4>{});
-    if (E <= 512) return f(row, LayerConst<8>{});
-    return f(row, LayerConst<16>{});
+hipError_t gate_for(int rowtype, int form, F f) {
+  auto with = [&](auto row) {
+    switch (form) {
+      case 0: return f(row, LayerConst<16>{}, LayerConst<4>{});
+      case 1: return f(row, LayerConst<16>{}, LayerConst<8>{});
+      case 2: return f(row, LayerConst<16>{}, LayerConst<16>{});
+      case 3: return f(row, LayerConst<64>{}, LayerConst<4>{});
+      case 4: return f(row, LayerConst<64>{}, LayerConst<8>{});
+      default: return f(row, LayerConst<64>{}, LayerConst<16>{});
+    }
   };
-  return rowtype == ROW_F32 ? per(GateF32{}) : rowtype == ROW_F16 ? per(TagF16{}) : per(TagBF16{});
+  return rowtype == ROW_F32 ? with(GateF32{}) : rowtype == ROW_F16 ? with(TagF16{}) : with(TagBF16{});
+}
+constexpr int kGateForms = 6;
+constexpr int kGateFormLanes[kGateForms] = {16, 16, 16, 64, 64, 64}, kGateFormPer[kGateForms] = {4, 8, 16, 4, 8, 16};
+// The first form that holds E experts in so many groups, each in a power of two of lanes
+// (log2 of it: lanes), and `top` choices; kGateForms if none does.
+int gate_form(int64_t E, int64_t groups, int64_t top, int& lanes) {
+  const int64_t size = E / groups;
+  for (int f = 0; f < kGateForms; ++f) {
+    if (top > kGateFormLanes[f]) continue;
+    for (lanes = 0; groups << lanes <= kGateFormLanes[f]; ++lanes)
+      if ((int64_t)kGateFormPer[f] << lanes >= size) return f;
+  }
+  return kGateForms;
 }
 
 int check_gate(int64_t T, int64_t E, int64_t top, int dtype, int score, float scale, int& rowtype, int& elem) {
@@ -345,13 +653,22 @@ int gemm_gate(int64_t T, int64_t E, int64_t top, int dtype, const void* L, int64
     a.group_top = (int)group_top;
     a.renorm = renorm != 0;
     a.scale = scale;
-    set_path("gate, a wave a token");
-    const dim3 grid = layer_grid((T + 3) / 4, 256, a.grid_x);
-    return launched(gate_for(rowtype, a.E, [&](auto row, auto per) {
-      hipStream_t s = static_cast<hipStream_t>(stream);
-      if (a.groups > 1)
-        return launch_kernel(layer_gate_kernel<decltype(row), decltype(per)::value, true>, grid, dim3(256), s, a);
-      return launch_kernel(layer_gate_kernel<decltype(row), decltype(per)::value, false>, grid, dim3(256), s, a);
+    while (E > 1 << a.bits) ++a.bits;
+    const int form = gate_form(E, groups, top, a.lanes);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (form == kGateForms) {  // groups that do not fit a wave
+      set_path("gate in 64 bits");
+      const dim3 grid = layer_grid((T + 3) / 4, 256, a.grid_x);
+      const auto k = rowtype == ROW_F32 ? layer_gate_exact_kernel<GateF32> : rowtype == ROW_F16 ? layer_gate_exact_kernel<TagF16> : layer_gate_exact_kernel<TagBF16>;
+      return launched(launch_kernel(k, grid, dim3(256), s, a));
+    }
+    set_path(std::string("gate, ") + (kGateFormLanes[form] == 16 ? "16 lanes a token" : "a wave a token"));
+    const int tokens = 4 * 64 / kGateFormLanes[form];
+    const dim3 grid = layer_grid((T + tokens - 1) / tokens, 256, a.grid_x);
+    return launched(gate_for(rowtype, form, [&](auto row, auto lanes, auto per) {
+      constexpr int LANES = decltype(lanes)::value, PER = decltype(per)::value;
+      if (a.groups > 1) return launch_kernel(layer_gate_kernel<decltype(row), LANES, PER, true>, grid, dim3(256), s, a);
+      return launch_kernel(layer_gate_kernel<decltype(row), LANES, PER, false>, grid, dim3(256), s, a);
     }));
   });
 }
@@ -393,10 +710,12 @@ int gemm_gate_grad(int64_t T, int64_t E, int64_t top, int dtype, const void* L, 
     a.score = score;
     a.renorm = renorm != 0;
     a.scale = scale;
-    set_path("gate_grad, a wave a token");
-    const dim3 grid = layer_grid((T + 3) / 4, 256, a.grid_x);
-    return launched(gate_for(rowtype, a.E, [&](auto row, auto per) {
-      return launch_kernel(layer_gate_grad_kernel<decltype(row), decltype(per)::value>, grid, dim3(256),
+    int lanes;
+    const int form = gate_form(E, 1, top, lanes), tokens = 4 * 64 / kGateFormLanes[form];
+    set_path(std::string("gate_grad, ") + (kGateFormLanes[form] == 16 ? "16 lanes a token" : "a wave a token"));
+    const dim3 grid = layer_grid((T + tokens - 1) / tokens, 256, a.grid_x);
+    return launched(gate_for(rowtype, form, [&](auto row, auto lanes, auto per) {
+      return launch_kernel(layer_gate_grad_kernel<decltype(row), decltype(lanes)::value, decltype(per)::value>, grid, dim3(256),
                            static_cast<hipStream_t>(stream), a);
     }));
   });
