@@ -31,7 +31,7 @@ struct NormGradArgs {
   float* part;         // [parts][2][N]: partial sums of dgamma and dbeta
   int64_t lddy, ldx, ldr, lddx;
   int M, N;
-  int rows, parts;     // rows that one partial sum covers, and their number
+  int rows, parts;     // rows that one partial sum covers (long rows), and their number
   unsigned grid_x;
 };
 

@@ -14,19 +14,58 @@ namespace dgt {
 
 namespace {
 
-// Eight elements of a row of any type.
+// Eight elements of a row of any type. ONCE: with the hint not to keep the bytes in the
+// caches, for calls whose rows fill half of the last one (256 MiB) or more (gradients of
+// 16384 x 4096 bf16: 113 us without, 93 so).
 struct NormF32 {};
+template <bool ONCE, class V>
+__device__ __forceinline__ V norm_load(const V* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+template <bool ONCE, class V>
+__device__ __forceinline__ void norm_store(V* p, V v) {
+  if constexpr (ONCE) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 template <class Row>
 struct NormIo {
   static constexpr int SIZE = 2;
-  __device__ static __forceinline__ void load(const char* p, int nv, float (&f)[8]) { layer_load8_16<Row>(p, nv, f); }
-  __device__ static __forceinline__ void store(char* p, int nv, const float (&f)[8]) { layer_store8_16<Row>(p, nv, f); }
+  template <bool ONCE = false>
+  __device__ static __forceinline__ void load(const char* p, int nv, float (&f)[8]) {
+    if (ONCE && nv == 8) layer_unpack8<Row>(norm_load<ONCE>(reinterpret_cast<const u32x4_at2*>(p)), f);
+    else layer_load8_16<Row>(p, nv, f);
+  }
+  template <bool ONCE = false>
+  __device__ static __forceinline__ void store(char* p, int nv, const float (&f)[8]) {
+    if (ONCE && nv == 8) norm_store<ONCE>(reinterpret_cast<u32x4_at2*>(p), u32x4_at2(layer_pack8<Row>(f)));
+    else layer_store8_16<Row>(p, nv, f);
+  }
 };
 template <>
 struct NormIo<NormF32> {
   static constexpr int SIZE = 4;
-  __device__ static __forceinline__ void load(const char* p, int nv, float (&f)[8]) { layer_load8_32(p, nv, f); }
-  __device__ static __forceinline__ void store(char* p, int nv, const float (&f)[8]) { layer_store8_32(p, nv, f); }
+  template <bool ONCE = false>
+  __device__ static __forceinline__ void load(const char* p, int nv, float (&f)[8]) {
+    if (ONCE && nv == 8) {
+      const u32x4_at4* v = reinterpret_cast<const u32x4_at4*>(p);
+      const f32x4 lo = __builtin_bit_cast(f32x4, u32x4(norm_load<ONCE>(v))), hi = __builtin_bit_cast(f32x4, u32x4(norm_load<ONCE>(v + 1)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = lo[e], f[e + 4] = hi[e];
+    } else {
+      layer_load8_32(p, nv, f);
+    }
+  }
+  template <bool ONCE = false>
+  __device__ static __forceinline__ void store(char* p, int nv, const float (&f)[8]) {
+    if (ONCE && nv == 8) {
+      u32x4_at4* v = reinterpret_cast<u32x4_at4*>(p);
+      norm_store<ONCE>(v, u32x4_at4(__builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]})));
+      norm_store<ONCE>(v + 1, u32x4_at4(__builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]})));
+    } else {
+      layer_store8_32(p, nv, f);
+    }
+  }
 };
 
 // Gamma and beta: eight elements, or a constant where there are none.
@@ -64,6 +103,231 @@ __device__ __forceinline__ void norm_block_sum(float& a, float& b, float* part, 
     a += part[2 * u];
     b += part[2 * u + 1];
   }
+}
+
+// A piece as it is stored, between its load and its use.
+template <class Row>
+struct NormRaw {
+  u32x4 v;
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const char* p, int nv) {
+    if (nv == 8) {
+      v = norm_load<ONCE>(reinterpret_cast<const u32x4_at2*>(p));
+    } else {
+      v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < nv) v[e / 2] |= (unsigned)reinterpret_cast<const unsigned short*>(p)[e] << (16 * (e % 2));
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const { layer_unpack8<Row>(v, f); }
+};
+template <>
+struct NormRaw<NormF32> {
+  float v[8];
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const char* p, int nv) { NormIo<NormF32>::load<ONCE>(p, nv, v); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = v[e];
+  }
+};
+
+// -------------------------------------------------- rows held in registers --
+// W waves take a row, V pieces of 8 columns a lane (piece v at column 8 (lane of the row + 64 W
+// v)), and hold it from its one reading to its writing. Four waves a workgroup, or one row
+// of more.
+
+// A sum over each group of W waves that share a row. part: two places per wave, used in turn.
+template <int W>
+__device__ __forceinline__ void norm_join(float& a, float& b, float (*part)[2]) {
+  a = norm_wave_sum(a);
+  b = norm_wave_sum(b);
+  if constexpr (W > 1) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      part[wave][0] = a;
+      part[wave][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      a += part[wave / W * W + u][0];
+      b += part[wave / W * W + u][1];
+    }
+  }
+}
+
+template <class Row, int W, int V, bool ONCE>
+__global__ void __launch_bounds__(W > 4 ? 64 * W : 256) layer_norm_kernel(const NormArgs p) {
+  using Io = NormIo<Row>;
+  constexpr int ROWS = W > 4 ? 1 : 4 / W, SPAN = 64 * W * 8;
+  __shared__ float part[2][W * ROWS][2];
+  const int lane = threadIdx.x % (64 * W);
+  const int64_t at = (int64_t)layer_block(p) * ROWS + threadIdx.x / (64 * W);
+  const int64_t row = at < p.M ? at : p.M - 1;  // (waves past the last row meet its barriers)
+  const char* x = static_cast<const char*>(p.X) + row * p.ldx * Io::SIZE;
+  const float inv = 1.0f / (float)p.N;
+  float f[V][8], sum = 0.0f, sq = 0.0f, none = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = 8 * lane + v * SPAN, nv = norm_left(p.N, c);
+    if (nv > 0) Io::template load<ONCE>(x + (int64_t)c * Io::SIZE, nv, f[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (8 * lane + v * SPAN + e >= p.N) f[v][e] = 0.0f;
+      sum += f[v][e];
+    }
+  norm_join<W>(sum, none, part[0]);
+  const float mean = sum * inv;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = f[v][e] - mean;
+      sq = 8 * lane + v * SPAN + e < p.N ? __builtin_fmaf(d, d, sq) : sq;
+    }
+  none = 0.0f;
+  norm_join<W>(sq, none, part[1]);
+  const float rstd = 1.0f / __builtin_sqrtf(sq * inv + p.eps);
+  if (at >= p.M) return;
+  char* y = static_cast<char*>(p.Y) + row * p.ldy * Io::SIZE;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = 8 * lane + v * SPAN, nv = norm_left(p.N, c);
+    if (nv <= 0) continue;
+    float g[8], b[8];
+    norm_param<Row>(static_cast<const char*>(p.gamma), c, nv, 1.0f, g);
+    norm_param<Row>(static_cast<const char*>(p.beta), c, nv, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[v][e] = __builtin_fmaf((f[v][e] - mean) * rstd, g[e], b[e]);
+    Io::template store<ONCE>(y + (int64_t)c * Io::SIZE, nv, f[v]);
+  }
+  if (lane == 0) {
+    if (p.mean) p.mean[row] = mean;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+}
+
+// Each workgroup takes rows a grid apart, with the next row's pieces asked for before the row
+// at hand is finished; dY U and dY are summed over them in registers, then over the rows
+// that the workgroup has at hand, and written as one part.
+template <class Row, int W, int V, bool ONCE>
+__global__ void __launch_bounds__(W > 4 ? 64 * W : 256) layer_norm_grad_kernel(const NormGradArgs p) {
+  using Io = NormIo<Row>;
+  constexpr int ROWS = W > 4 ? 1 : 4 / W, SPAN = 64 * W * 8;
+  __shared__ float part[2][W * ROWS][2];
+  __shared__ float joined[ROWS > 1 ? 2 * SPAN * V : 1];
+  const int lane = threadIdx.x % (64 * W), sub = threadIdx.x / (64 * W);
+  const int64_t block = layer_block(p), first = block * ROWS + sub;
+  if (block >= p.parts) return;
+  const float inv = 1.0f / (float)p.N;
+  float g[V][8], sg[V][8], sb[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = 8 * lane + v * SPAN, nv = norm_left(p.N, c);
+    if (nv > 0) norm_param<Row>(static_cast<const char*>(p.gamma), c, nv, 1.0f, g[v]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (c + e >= p.N) g[v][e] = 0.0f;
+      sg[v][e] = sb[v][e] = 0.0f;
+    }
+  }
+  NormRaw<Row> x[V], d[V], r[V];
+  float mean = 0.0f, rstd = 0.0f;
+  auto request = [&](int64_t row) {
+    mean = p.mean[row];
+    rstd = p.rstd[row];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int64_t c = 8 * lane + v * SPAN;
+      const int nv = norm_left(p.N, (int)c);
+      if (nv <= 0) continue;
+      x[v].template load<ONCE>(static_cast<const char*>(p.X) + (row * p.ldx + c) * Io::SIZE, nv);
+      d[v].template load<ONCE>(static_cast<const char*>(p.dY) + (row * p.lddy + c) * Io::SIZE, nv);
+      if (p.R) r[v].template load<ONCE>(static_cast<const char*>(p.R) + (row * p.ldr + c) * Io::SIZE, nv);
+    }
+  };
+  // Every wave of a workgroup takes as many turns, so that all meet the barriers.
+  const int64_t step = (int64_t)p.parts * ROWS, turns = (p.M - block * ROWS + step - 1) / step;
+  auto clamp = [&](int64_t row) { return row < p.M ? row : p.M - 1; };
+  request(clamp(first));
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    const int64_t row = first + turn * step;
+    const bool in = row < p.M;
+    float u[V][8], h[V][8], rr[V][8], s1 = 0.0f, s2 = 0.0f;
+    const float m = mean, rs = rstd;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v].get(u[v]);
+      d[v].get(h[v]);
+      if (p.R) r[v].get(rr[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool has = 8 * lane + v * SPAN + e < p.N;
+        u[v][e] = has ? (u[v][e] - m) * rs : 0.0f;
+        h[v][e] = has && in ? h[v][e] : 0.0f;
+        sg[v][e] = __builtin_fmaf(h[v][e], u[v][e], sg[v][e]);
+        sb[v][e] += h[v][e];
+        h[v][e] *= g[v][e];
+        s1 += h[v][e];
+        s2 = __builtin_fmaf(h[v][e], u[v][e], s2);
+      }
+    }
+    if (turn + 1 < turns) request(clamp(row + step));
+    norm_join<W>(s1, s2, part[turn & 1]);
+    s1 *= inv;
+    s2 *= inv;
+    if (p.dX && in) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int64_t c = 8 * lane + v * SPAN;
+        const int nv = norm_left(p.N, (int)c);
+        if (nv <= 0) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[v][e] = rs * (h[v][e] - s1 - u[v][e] * s2);
+          if (p.R) h[v][e] += rr[v][e];
+        }
+        Io::template store<ONCE>(static_cast<char*>(p.dX) + (row * p.lddx + c) * Io::SIZE, nv, h[v]);
+      }
+    }
+  }
+  if (!p.part) return;
+  if constexpr (ROWS > 1) {
+#pragma unroll
+    for (int turn = 0; turn < ROWS; ++turn) {
+      if (sub == turn) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float* const at = joined + (v * 8 + e) * 64 * W + lane;
+            sg[v][e] = turn ? at[0] + sg[v][e] : sg[v][e];
+            sb[v][e] = turn ? at[SPAN * V] + sb[v][e] : sb[v][e];
+            at[0] = sg[v][e];
+            at[SPAN * V] = sb[v][e];
+          }
+      }
+      __syncthreads();
+    }
+    if (sub != ROWS - 1) return;
+  }
+  float* out = p.part + 2 * block * p.N;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = 8 * lane + v * SPAN + e;
+      if (c < p.N) {
+        out[c] = sg[v][e];
+        out[p.N + c] = sb[v][e];
+      }
+    }
 }
 
 // ------------------------------------------------------------------ any row --
@@ -232,36 +496,109 @@ __global__ void __launch_bounds__(64 * kSumWaves) layer_norm_sum_kernel(const No
   }
 }
 
+// Waves a row and pieces a lane that hold N columns, by rising width.
+constexpr int kNormForms = 7;
+constexpr int kNormWaves[kNormForms] = {1, 1, 1, 4, 4, 16, 16}, kNormPieces[kNormForms] = {1, 2, 4, 2, 4, 2, 4};
+int norm_form(int64_t N) {
+  int f = 0;
+  while (f < kNormForms && (int64_t)kNormWaves[f] * kNormPieces[f] * 512 < N) ++f;
+  return f;
+}
+int norm_form_rows(int form) { return kNormWaves[form] > 4 ? 1 : 4 / kNormWaves[form]; }
+template <class F>
+hipError_t norm_for(int form, F f) {
+  switch (form) {
+    case 0: return f(LayerConst<1>{}, LayerConst<1>{});
+    case 1: return f(LayerConst<1>{}, LayerConst<2>{});
+    case 2: return f(LayerConst<1>{}, LayerConst<4>{});
+    case 3: return f(LayerConst<4>{}, LayerConst<2>{});
+    case 4: return f(LayerConst<4>{}, LayerConst<4>{});
+    case 5: return f(LayerConst<16>{}, LayerConst<2>{});
+    default: return f(LayerConst<16>{}, LayerConst<4>{});
+  }
+}
+
+template <class Row, class Args>
+bool norm_once(const Args& a) { return (int64_t)a.M * a.N * NormIo<Row>::SIZE >= (int64_t{128} << 20); }
+
 template <class Row>
 hipError_t norm(NormArgs a, hipStream_t s) {
+  const int form = norm_form(a.N);
+  if (form < kNormForms) {
+    const int rows = norm_form_rows(form), threads = kNormWaves[form] > 4 ? 64 * kNormWaves[form] : 256;
+    const dim3 grid = layer_grid(((int64_t)a.M + rows - 1) / rows, threads, a.grid_x);
+    return norm_for(form, [&](auto w, auto v) {
+      constexpr int W = decltype(w)::value, V = decltype(v)::value;
+      if (norm_once<Row>(a)) return launch_kernel(layer_norm_kernel<Row, W, V, true>, grid, dim3(threads), s, a);
+      return launch_kernel(layer_norm_kernel<Row, W, V, false>, grid, dim3(threads), s, a);
+    });
+  }
   const dim3 grid = layer_grid(a.M, kLongThreads, a.grid_x);
   return launch_kernel(layer_norm_long_kernel<Row>, grid, dim3(kLongThreads), s, a);
 }
 
+// The same for the gradients, which hold more for each column: wider rows are read again.
+constexpr int kNormGradForms = 5;
+constexpr int kNormGradWaves[kNormGradForms] = {1, 1, 2, 4, 8}, kNormGradPieces[kNormGradForms] = {1, 2, 2, 2, 2};
+int norm_grad_form(int64_t N) {
+  int f = 0;
+  while (f < kNormGradForms && (int64_t)kNormGradWaves[f] * kNormGradPieces[f] * 512 < N) ++f;
+  return f;
+}
+int norm_grad_rows(int form) { return form == kNormGradForms || kNormGradWaves[form] > 4 ? 1 : 4 / kNormGradWaves[form]; }
+template <class F>
+hipError_t norm_grad_for(int form, F f) {
+  switch (form) {
+    case 0: return f(LayerConst<1>{}, LayerConst<1>{});
+    case 1: return f(LayerConst<1>{}, LayerConst<2>{});
+    case 2: return f(LayerConst<2>{}, LayerConst<2>{});
+    case 3: return f(LayerConst<4>{}, LayerConst<2>{});
+    default: return f(LayerConst<8>{}, LayerConst<2>{});
+  }
+}
+
 template <class Row>
 hipError_t norm_grad(NormGradArgs a, hipStream_t s) {
-  if (a.dgamma || a.dbeta) {
+  const int form = norm_grad_form(a.N);
+  const bool sums = a.dgamma || a.dbeta;
+  if (!sums) a.part = nullptr;
+  if (form < kNormGradForms) {
     if (a.M > 0) {
-      const dim3 grid = layer_grid((a.parts * (((int64_t)a.N + 511) / 512) + 3) / 4, 256, a.grid_x);
-      const hipError_t e = launch_kernel(layer_norm_grad_columns_kernel<Row>, grid, dim3(256), s, a);
+      const int threads = kNormGradWaves[form] > 4 ? 64 * kNormGradWaves[form] : 256;
+      const dim3 grid = layer_grid(a.parts, threads, a.grid_x);
+      const hipError_t e = norm_grad_for(form, [&](auto w, auto v) {
+        constexpr int W = decltype(w)::value, V = decltype(v)::value;
+        if (norm_once<Row>(a)) return launch_kernel(layer_norm_grad_kernel<Row, W, V, true>, grid, dim3(threads), s, a);
+        return launch_kernel(layer_norm_grad_kernel<Row, W, V, false>, grid, dim3(threads), s, a);
+      });
       if (e != hipSuccess) return e;
     }
+  } else if (sums && a.M > 0) {
+    const dim3 grid = layer_grid((a.parts * (((int64_t)a.N + 511) / 512) + 3) / 4, 256, a.grid_x);
+    const hipError_t e = launch_kernel(layer_norm_grad_columns_kernel<Row>, grid, dim3(256), s, a);
+    if (e != hipSuccess) return e;
+  }
+  if (sums) {
     const dim3 grid = layer_grid(((int64_t)a.N + 63) / 64, 64 * kSumWaves, a.grid_x, 2);
     const hipError_t e = launch_kernel(layer_norm_sum_kernel, grid, dim3(64 * kSumWaves), s, a);
     if (e != hipSuccess) return e;
   }
-  if (!a.dX || a.M == 0) return hipSuccess;
+  if (form < kNormGradForms || !a.dX || a.M == 0) return hipSuccess;
   const dim3 grid = layer_grid(a.M, kLongThreads, a.grid_x);
   return launch_kernel(layer_norm_grad_long_kernel<Row>, grid, dim3(kLongThreads), s, a);
 }
 
-// Rows of one partial sum: at most 1024 parts.
-int64_t norm_rows(int64_t m) { return (m + 1023) / 1024 > 0 ? (m + 1023) / 1024 : 1; }
-int64_t norm_parts(int64_t m) { return (m + norm_rows(m) - 1) / norm_rows(m); }
+// Workgroups, and so partial sums of dgamma and dbeta: two a CU (16384 x 4096 bf16, us: 256
+// workgroups 128, 512 117, 1024 128 with the partial sums joined).
+int64_t norm_parts(int64_t m, int64_t n) {
+  const int64_t rows = norm_grad_rows(norm_grad_form(n)), most = 512;
+  const int64_t all = (m + rows - 1) / rows;
+  return all < most ? all : most;
+}
 
 int64_t norm_grad_bytes(int64_t M, int64_t N) {
   if (M < 0 || N < 0 || M > kMaxDim || N > kMaxDim) return 0;
-  return norm_parts(M) * N * 8;
+  return norm_parts(M, N) * N * 8;
 }
 
 int check_norm(int64_t M, int64_t N, int dtype, int& rowtype, int& elem) {
@@ -382,8 +719,8 @@ int gemm_norm_grad(int64_t M, int64_t N, int dtype, const void* dY, int64_t lddy
     a.lddx = lddx;
     a.M = (int)M;
     a.N = (int)N;
-    a.rows = (int)norm_rows(M);
-    a.parts = (int)norm_parts(M);
+    a.parts = (int)norm_parts(M, N);
+    a.rows = M ? (int)((M + a.parts - 1) / a.parts) : 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
     set_path("norm_grad row by row");
     return launched(rowtype == ROW_F32   ? norm_grad<NormF32>(a, s)
