@@ -358,7 +358,7 @@ int plan_product(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, int tran
 int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t* offsets,
                      const void* A, int64_t lda, const void* B, int64_t ldb, const void* D,
                      int64_t ldd, int64_t stride_d, int out_dtype, int accumulate, LayerPlan& pl,
-                     bool& noop) {
+                     bool& noop, bool forced = true) {
   noop = false;
   CHECK(check_dim("M", M));
   CHECK(check_dim("N", N));
@@ -416,7 +416,7 @@ int plan_grad_weight(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, cons
   a.a_direct = M > 0 && layer_direct(ma, N);
   a.b_direct = M > 0 && layer_direct(mb, K);
   pl.direct = a.a_direct && a.b_direct;
-  return plan_tiles(pl, "grad_weight");
+  return plan_tiles(pl, "grad_weight", forced);
 }
 
 // ------------------------------------------------------------- rows and ids --
@@ -463,6 +463,14 @@ int run_dense(const DenseCall& c, bool launch, hipStream_t s) {
   CHECK(plan_product(-1, c.M, c.N, c.K, c.dtype, c.ta, c.tb, nullptr, c.A, c.lda, c.B, c.ldb, 0,
                      nullptr, GEMM_ACT_NONE, c.R, c.ldr, c.Y, c.ldy, c.out_dtype, nullptr, 0, pl, noop,
                      false));
+  return noop || !launch ? GEMM_OK : launched(launch_product(pl, s));
+}
+
+int run_sums(const SumsCall& c, bool launch, hipStream_t s) {
+  LayerPlan pl;
+  bool noop;
+  CHECK(plan_grad_weight(c.G, c.M, c.N, c.K, c.dtype, c.offsets, c.A, c.lda, c.B, c.ldb, c.D, c.ldd, c.stride_d,
+                         c.out_dtype, c.accumulate, pl, noop, false));
   return noop || !launch ? GEMM_OK : launched(launch_product(pl, s));
 }
 

@@ -157,4 +157,20 @@ struct DenseCall {
 };
 int run_dense(const DenseCall& c, bool launch, hipStream_t s);
 
+// The same of gemm_grouped_grad_weight: D_g = A_g^T @ B_g (+ D_g).
+struct SumsCall {
+  int64_t G, M, N, K;
+  int dtype;
+  const int32_t* offsets;
+  const void* A;
+  int64_t lda;
+  const void* B;
+  int64_t ldb;
+  void* D;
+  int64_t ldd, stride_d;
+  int out_dtype;
+  bool accumulate;
+};
+int run_sums(const SumsCall& c, bool launch, hipStream_t s);
+
 }  // namespace dgt

@@ -1,12 +1,24 @@
-// Cross entropy of an output layer: logits L = X W^T made in pieces of the
-// vocabulary, and never all of them held.
+// Cross entropy of an output layer: logits L = X W^T made in pieces of the vocabulary, and
+// never all of them held.
 //
 //   lse = log sum exp L,  loss = lse - L[label]
 //   G = dloss (exp(L - lse) - [v = label]),  dX = G W,  dW = G^T X
 //
-// A piece's logits are a product of gemm_linear in float32. Each row keeps the largest
-// logit so far and the sum of exponentials relative to it; the gradient makes the
-// logits again, turns a piece of them into G, and multiplies it from both sides.
+// Forward: parts of the vocabulary leave their largest logit and their sum of
+// exponentials for each token, which a second kernel joins. Gradient: a piece's logits
+// are made again and turned into G, stored as G^T (n x T8: a vocabulary entry's row,
+// tokens in whole pieces of 8, zeros past T), whose two products follow:
+//   dW   G^T X, each piece its own rows
+//   dX   G W, a sum over the vocabulary: both operands lie along it, so it can be cut into S
+//        parts that fill the CUs where T x H has few tiles; parts and pieces are added
+//        in float32
+// X is copied to T8 rows where T is not a multiple of 8.
+//
+// The logits come from layer_loss_pp256.hip, which turns them into parts or G in
+// registers. Fewer tokens, and operands not in whole 16-byte pieces, take a product of
+// gemm_linear in float32 and a kernel over its rows instead.
+#include "layer_loss.h"
+
 #include "layer.h"
 #include "layer_checks.h"
 
@@ -14,16 +26,25 @@ namespace dgt {
 
 namespace {
 
-// One piece of the vocabulary, columns [v0, v0 + n).
-struct LossArgs {
-  const float* L;       // logits of the piece, T x n, pitch ldl
+constexpr int kLossChunk = 4096;  // logits of a row that a workgroup takes
+
+// Sub-piece of float32 logits, T x n: columns [v0, v0 + n) of the vocabulary.
+struct LossRowsArgs {
+  const float* L;
   const int* labels;
-  float* state;         // [3][T]: largest logit, sum, the label's logit
-  float* loss;
-  float* lse;           // null: not wanted
+  float2* parts;        // of this sub-piece: [chunks][T]
+  float* target;
   int64_t ldl;
   int T, V, v0, n;
-  int first, last;      // whether this is the first, the last piece
+  unsigned grid_x;
+};
+struct LossJoinArgs {
+  const float2* parts;  // [Q][T]
+  const float* target;
+  const int* labels;
+  float* loss;
+  float* lse;           // null: not wanted
+  int T, V, Q;
   unsigned grid_x;
 };
 struct LossGradArgs {
@@ -31,105 +52,212 @@ struct LossGradArgs {
   const int* labels;
   const float* lse;
   const float* dloss;
-  void* G;              // T x n, pitch ldg
-  int64_t ldl, ldg;
-  int T, V, v0, n;
+  void* G;              // n x T8
+  int64_t ldl;
+  int T, T8, V, v0, n;
   unsigned grid_x;
 };
 
+__device__ __forceinline__ float loss_exp(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
 // Two partial (largest, sum) as one. A side without logits has (-inf, 0).
-__device__ __forceinline__ void loss_join(float& m, float& s, float om, float os) {
-  const float top = om > m ? om : m;
-  const float base = top == -__builtin_inff() ? 0.0f : top;
-  s = s * __expf(m - base) + os * __expf(om - base);
-  m = top;
+__device__ __forceinline__ float2 loss_join(float2 a, float2 b) {
+  const float m = __builtin_fmaxf(a.x, b.x), base = m == -__builtin_inff() ? 0.0f : m;
+  return float2{m, a.y * loss_exp(a.x - base) + b.y * loss_exp(b.x - base)};
 }
 
-// A workgroup a row of the piece.
-__global__ void __launch_bounds__(256) layer_loss_rows_kernel(const LossArgs p) {
-  __shared__ float part[8];
-  const int64_t t = layer_block(p);
+// A workgroup takes kLossChunk logits of a row.
+__global__ void __launch_bounds__(256) layer_loss_rows_kernel(const LossRowsArgs p) {
+  __shared__ float2 part[4];
+  const unsigned chunks = (unsigned)(p.n + kLossChunk - 1) / kLossChunk, id = layer_block(p);
+  const int64_t t = id / chunks;
   if (t >= p.T) return;
+  const int chunk = id - (unsigned)t * chunks, c0 = chunk * kLossChunk;
   const float* l = p.L + t * p.ldl;
-  float m = -__builtin_inff(), s = 0.0f;
-  for (int c = threadIdx.x; c < p.n; c += 256) loss_join(m, s, l[c], 1.0f);
+  constexpr int PER = kLossChunk / 1024;
+  float f[PER][4], m = -__builtin_inff(), s = 0.0f;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) loss_join(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64));
-  if ((threadIdx.x & 63) == 0) {
-    part[threadIdx.x >> 6] = m;
-    part[4 + (threadIdx.x >> 6)] = s;
+  for (int i = 0; i < PER; ++i) {
+    const int c = c0 + 1024 * i + 4 * threadIdx.x;
+    if (c + 4 <= p.n) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(l + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[i][e] = v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[i][e] = c + e < p.n ? l[c + e] : -__builtin_inff();
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __builtin_fmaxf(m, f[i][e]);
   }
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += loss_exp(f[i][e] - base);
+  float2 a{m, s};
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) a = loss_join(a, float2{__shfl_xor(a.x, d, 64), __shfl_xor(a.y, d, 64)});
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
   if (threadIdx.x) return;
-  for (int w = 1; w < 4; ++w) loss_join(m, s, part[w], part[4 + w]);
-  float at = 0.0f;
+  for (int w = 1; w < 4; ++w) a = loss_join(a, part[w]);
+  p.parts[(int64_t)chunk * p.T + t] = a;
   const int label = p.labels[t];
-  const bool has = (unsigned)label < (unsigned)p.V;
-  if (!p.first) {
-    loss_join(m, s, p.state[t], p.state[p.T + t]);
-    at = p.state[2 * (int64_t)p.T + t];
-  }
-  if (has && label >= p.v0 && label - p.v0 < p.n) at = l[label - p.v0];
-  if (p.last) {
-    const float lse = m + logf(s);
-    p.loss[t] = has ? lse - at : 0.0f;
-    if (p.lse) p.lse[t] = lse;
-  } else {
-    p.state[t] = m;
-    p.state[p.T + t] = s;
-    p.state[2 * (int64_t)p.T + t] = at;
-  }
+  if ((unsigned)label >= (unsigned)p.V) return;
+  const int at = label - p.v0;
+  if (at >= c0 && at < p.n && at - c0 < kLossChunk) p.target[t] = l[at];
 }
 
-// G of a piece.
+// The parts of 64 tokens: every kJoinWaves-th for each wave, joined in wave order.
+constexpr int kJoinWaves = 16;
+__global__ void __launch_bounds__(64 * kJoinWaves) layer_loss_join_kernel(const LossJoinArgs p) {
+  __shared__ float2 part[kJoinWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t t = (int64_t)layer_block(p) * 64 + lane;
+  float2 a{-__builtin_inff(), 0.0f};
+  if (t < p.T)
+    for (int64_t q = w; q < p.Q; q += kJoinWaves) a = loss_join(a, p.parts[q * p.T + t]);
+  part[w][lane] = a;
+  __syncthreads();
+  if (w || t >= p.T) return;
+  for (int u = 1; u < kJoinWaves; ++u) a = loss_join(a, part[u][lane]);
+  const float lse = a.x + logf(a.y);
+  const bool has = (unsigned)p.labels[t] < (unsigned)p.V;
+  p.loss[t] = has ? lse - p.target[t] : 0.0f;
+  if (p.lse) p.lse[t] = lse;
+}
+
+// G^T of 64 tokens and 64 entries, through LDS.
 template <class Tag>
 __global__ void __launch_bounds__(256) layer_loss_grad_kernel(const LossGradArgs p) {
-  const int64_t t = layer_block(p);
-  if (t >= p.T) return;
-  const int label = p.labels[t];
-  const bool has = (unsigned)label < (unsigned)p.V;
-  const float lse = has ? p.lse[t] : 0.0f, d = has ? p.dloss[t] : 0.0f;
-  const float* l = p.L + t * p.ldl;
-  char* g = static_cast<char*>(p.G) + t * p.ldg * 2;
-  for (int64_t c = 8 * threadIdx.x; c < p.n; c += 8 * 256) {
-    const int nv = p.n - c >= 8 ? 8 : (int)(p.n - c);
-    float f[8];
-    layer_load8_32(reinterpret_cast<const char*>(l + c), nv, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f[e] = __expf(f[e] - lse) - (p.v0 + (int)c + e == label ? 1.0f : 0.0f);
-      f[e] = has ? f[e] * d : 0.0f;
-    }
-    layer_store8_16<Tag>(g + c * 2, nv, f);
+  __shared__ unsigned short x[64][72];  // [entry][token]; rows 16-byte aligned, banks apart
+  const unsigned across = (unsigned)(p.T8 + 63) / 64, id = layer_block(p);
+  const int64_t r = id / across;
+  const int t0 = (int)(id - (unsigned)r * across) * 64, e0 = (int)(r * 64);
+  if (r * 64 >= p.n) return;
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < 64; i += 4) {  // a wave a token
+    const int t = t0 + i, c = e0 + lane, label = t < p.T ? p.labels[t] : -1;
+    float g = 0.0f;
+    if ((unsigned)label < (unsigned)p.V && c < p.n)
+      g = p.dloss[t] * (loss_exp(p.L[t * p.ldl + c] - p.lse[t]) - (p.v0 + c == label ? 1.0f : 0.0f));
+    x[lane][i] = layer_16(Tag{}, g);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 8; i += 256) {
+    const int e = i >> 3, t = 8 * (i & 7);
+    if (e0 + e < p.n && t0 + t < p.T8)
+      *reinterpret_cast<u32x4*>(static_cast<unsigned short*>(p.G) + (int64_t)(e0 + e) * p.T8 + t0 + t) =
+          *reinterpret_cast<const u32x4*>(&x[e][t]);
   }
 }
 
-// dX from its float32 sums.
+// X with T8 rows, zeros from row T on.
+struct LossPadArgs {
+  const unsigned short* X;
+  unsigned short* to;
+  int64_t ldx, n, live;  // elements: all of them, and those of X
+  int H;
+};
+__global__ void __launch_bounds__(256) layer_loss_pad_kernel(const LossPadArgs p) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.n; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / p.H;
+    p.to[i] = i < p.live ? p.X[t * p.ldx + (i - t * p.H)] : (unsigned short)0;
+  }
+}
+// Offsets that cut n rows into S parts, for the pieces of n and for the last one.
+__global__ void __launch_bounds__(256) layer_loss_offsets_kernel(int* to, int S, int n, int last) {
+  for (int i = threadIdx.x; i <= S; i += 256) {
+    to[i] = (int)((int64_t)n * i / S);
+    to[S + 1 + i] = (int)((int64_t)last * i / S);
+  }
+}
+// dX from S float32 parts of T8 x H.
+struct LossRoundArgs {
+  const float* from;
+  unsigned short* to;
+  int64_t ld, n, stride;
+  int H, S;
+};
 template <class Tag>
-__global__ void __launch_bounds__(256) layer_loss_round_kernel(const float* from, char* to, int64_t ld, int64_t n, int H) {
-  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
-    const int64_t t = at / H;
-    reinterpret_cast<unsigned short*>(to)[t * ld + (at - t * H)] = layer_16(Tag{}, from[at]);
+__global__ void __launch_bounds__(256) layer_loss_round_kernel(const LossRoundArgs p) {
+  for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < p.n; i += 4 * (int64_t)gridDim.x * 256) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(p.from + i);  // (parts are whole fours: T8 is a multiple of 8)
+    for (int u = 1; u < p.S; ++u) {
+      const f32x4 o = *reinterpret_cast<const f32x4*>(p.from + u * p.stride + i);
+      for (int e = 0; e < 4; ++e) s[e] += o[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t t = (i + e) / p.H;
+      if (i + e < p.n) p.to[t * p.ld + (i + e - t * p.H)] = layer_16(Tag{}, s[e]);
+    }
   }
 }
 
-// Columns of a piece: as many as 256 MiB of logits hold, whole tiles.
-int64_t loss_piece(int64_t T, int64_t V) {
-  int64_t n = ((int64_t{1} << 26) / (T > 0 ? T : 1)) / 256 * 256;
-  if (n < 1024) n = 1024;
-  return n < V ? n : (V + 7) / 8 * 8;
-}
+// ------------------------------------------------------------------ the plan --
 int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
-int64_t loss_bytes(int64_t T, int64_t V, int64_t H) {
-  if (T < 1 || V < 1 || H < 0 || T > kMaxDim || V > kMaxDim || H > kMaxDim) return 0;
-  const int64_t p = loss_piece(T, V);
-  return round16(T * 12) + T * p * 4;
+
+// Sizes of a call, and where its buffers lie in the workspace (bytes).
+struct LossPlan {
+  int64_t T8, piece, sub;  // G's rows at a time, float32 logits' columns at a time
+  int64_t Q;               // parts, at most
+  int S;                   // parts of dX's sum
+  bool direct;             // dX needs no float32 sums
+  int64_t parts, target, logits, forward;      // forward: all bytes of gemm_loss
+  int64_t glogits, g, xpad, sums, offsets, grad;  // grad: all bytes of gemm_loss_grad
+};
+// False where the bytes pass 63 bits.
+bool loss_plan(int64_t T, int64_t V, int64_t H, LossPlan& q) {
+  if (T < 1 || V < 1 || H < 0 || T > kMaxDim || V > kMaxDim || H > kMaxDim) return false;
+  auto columns = [&](int64_t elements) {  // of T tokens each, whole chunks, at least one
+    int64_t n = elements / T / kLossChunk * kLossChunk;
+    if (n < kLossChunk) n = kLossChunk;
+    return n < V ? n : (V + 7) / 8 * 8;
+  };
+  q.T8 = (T + 7) / 8 * 8;
+  q.piece = columns(int64_t{1} << 28);  // 512 MiB of G
+  q.sub = columns(int64_t{1} << 25);    // 128 MiB of logits
+  q.Q = (V + 255) / 256;
+  const int64_t tiles = ((q.T8 + 255) / 256) * ((H + 255) / 256);
+  const int64_t rows = q.piece < V ? q.piece : V;
+  q.S = 1;
+  if (tiles > 0 && tiles <= 128) {
+    int64_t s = 256 / tiles;
+    if (s > rows / 1024) s = rows / 1024;
+    q.S = s > 1 ? (int)s : 1;
+  }
+  q.direct = q.S == 1 && q.piece >= V && q.T8 == T;
+  unsigned __int128 at = 0;
+  auto place = [&](int64_t& where, unsigned __int128 bytes) {
+    where = (int64_t)at;
+    at += (bytes + 15) / 16 * 16;
+  };
+  const unsigned __int128 max = INT64_MAX;
+  place(q.parts, (unsigned __int128)q.Q * T * 8);
+  place(q.target, (unsigned __int128)T * 4);
+  place(q.logits, (unsigned __int128)T * q.sub * 4);
+  if (at > max) return false;
+  q.forward = (int64_t)at;
+  at = 0;
+  place(q.glogits, (unsigned __int128)T * q.sub * 4);
+  place(q.g, (unsigned __int128)q.piece * q.T8 * 2);
+  place(q.xpad, q.T8 == T ? 0 : (unsigned __int128)q.T8 * H * 2);
+  place(q.sums, q.direct ? 0 : (unsigned __int128)q.S * q.T8 * H * 4);
+  place(q.offsets, (unsigned __int128)2 * (q.S + 1) * 4);
+  if (at > max) return false;
+  q.grad = (int64_t)at;
+  return true;
 }
-int64_t loss_grad_bytes(int64_t T, int64_t V, int64_t H) {
-  if (T < 1 || V < 1 || H < 0 || T > kMaxDim || V > kMaxDim || H > kMaxDim) return 0;
-  const int64_t p = loss_piece(T, V);
-  const unsigned __int128 b = (unsigned __int128)T * p * 6 + (unsigned __int128)T * H * 4 + 48;
-  return b > (unsigned __int128)INT64_MAX ? 0 : (int64_t)b;
+
+// Whether the logits are made on 256x256 tiles: operands in whole 16-byte pieces, and enough
+// tokens for half of a tile's columns or more than one tile.
+bool loss_tiles(const Mat& x, const Mat& w, int64_t n) {
+  auto whole = [](const Mat& m) {
+    return (uintptr_t)m.ptr % 16 == 0 && m.ld % 8 == 0 && m.ld < (int64_t{1} << 31) / (2 * 257) - 4096;
+  };
+  const int64_t tiles = ((x.rows + 255) / 256) * ((n + 255) / 256);
+  return x.cols > 0 && x.cols % 8 == 0 && whole(x) && whole(w) && x.rows > 64 && tiles < (1 << 22);
 }
 
 int check_loss(int64_t T, int64_t V, int64_t H, int dtype, const Mat& mx, const Mat& mw) {
@@ -142,45 +270,165 @@ int check_loss(int64_t T, int64_t V, int64_t H, int dtype, const Mat& mx, const 
   return check_ld(mw);
 }
 
+// f(v0, n) for pieces of V columns; the first status that is not GEMM_OK.
+template <class F>
+int loss_pieces(int64_t V, int64_t piece, F f) {
+  for (int64_t v0 = 0; v0 < V; v0 += piece) CHECK(f(v0, V - v0 < piece ? V - v0 : piece));
+  return GEMM_OK;
+}
+const char* loss_row(const Mat& m, int64_t row) { return static_cast<const char*>(m.ptr) + row * m.ld * m.elem; }
+
+// The float32 logits of columns [v0, v0 + n).
+DenseCall loss_logits(const Mat& mx, const Mat& mw, int dtype, int64_t v0, int64_t n, void* to, int64_t ld) {
+  return {mx.rows, n, mx.cols, dtype, false, true, mx.ptr, mx.ld, loss_row(mw, v0), mw.ld, nullptr, 0, to, ld, GEMM_DTYPE_F32};
+}
+
+// Both run through a call twice: without launches, so that a refusal comes before any work, and with.
+int run_loss(const LossPlan& q, const Mat& mx, const Mat& mw, int dtype, const int32_t* labels, float* loss, float* lse,
+             char* ws, bool launch, hipStream_t s) {
+  const int64_t T = mx.rows, V = mw.rows;
+  float2* const parts = reinterpret_cast<float2*>(ws + q.parts);
+  float* const target = reinterpret_cast<float*>(ws + q.target);
+  const bool tiles = loss_tiles(mx, mw, V);
+  int64_t Q = q.Q;
+  if (tiles) {
+    LossTileArgs a{};
+    a.W = mw.ptr;
+    a.X = mx.ptr;
+    a.ldw = mw.ld;
+    a.ldx = mx.ld;
+    a.n = (int)V;
+    a.T = (int)T;
+    a.H = (int)mx.cols;
+    a.labels = labels;
+    a.V = (int)V;
+    a.parts = parts;
+    a.target = target;
+    if (launch) CHECK(launched(launch_loss_tiles(dtype, false, a, s)));
+  } else {
+    Q = 0;
+    CHECK(loss_pieces(V, q.sub, [&](int64_t v0, int64_t n) -> int {
+      float* const l = reinterpret_cast<float*>(ws + q.logits);
+      CHECK(run_dense(loss_logits(mx, mw, dtype, v0, n, l, q.sub), launch, s));
+      LossRowsArgs a{};
+      a.L = l;
+      a.labels = labels;
+      a.parts = parts + Q * T;
+      a.target = target;
+      a.ldl = q.sub;
+      a.T = (int)T;
+      a.V = (int)V;
+      a.v0 = (int)v0;
+      a.n = (int)n;
+      const int64_t chunks = (n + kLossChunk - 1) / kLossChunk;
+      Q += chunks;
+      if (chunks * T > 0x7ffffff0) return fail(GEMM_ERR_UNSUPPORTED, "too many pieces of rows for one launch");
+      if (!launch) return GEMM_OK;
+      const dim3 grid = layer_grid(chunks * T, 256, a.grid_x);
+      return launched(launch_kernel(layer_loss_rows_kernel, grid, dim3(256), s, a));
+    }));
+  }
+  if (!launch) return GEMM_OK;
+  LossJoinArgs j{};
+  j.parts = parts;
+  j.target = target;
+  j.labels = labels;
+  j.loss = loss;
+  j.lse = lse;
+  j.T = (int)T;
+  j.V = (int)V;
+  j.Q = (int)Q;
+  const dim3 grid = layer_grid((T + 63) / 64, 64 * kJoinWaves, j.grid_x);
+  CHECK(launched(launch_kernel(layer_loss_join_kernel, grid, dim3(64 * kJoinWaves), s, j)));
+  set_path(tiles ? "loss on 256x256 tiles" : "loss in pieces of " + std::to_string(q.sub));
+  return GEMM_OK;
+}
+
 template <class Tag>
-int run_grad(const LossGradArgs& g0, const DenseCall& logits, float* acc, int64_t piece, const Mat& mx, const Mat& mw,
-             const Mat& mdx, const Mat& mdw, bool accumulate, int dtype, int dw_dtype, hipStream_t s) {
-  const int64_t T = g0.T, V = g0.V, H = mx.cols;
-  const bool single = piece >= V;
-  // The plan of every piece before any of them runs, so that a call is refused as a whole.
-  for (int launch = 0; launch < 2; ++launch)
-    for (int64_t v0 = 0; v0 < V; v0 += piece) {
-      const int64_t n = V - v0 < piece ? V - v0 : piece;
-      const char* const w = static_cast<const char*>(mw.ptr) + v0 * mw.ld * 2;
-      DenseCall c = logits;
-      c.N = n;
-      c.B = w;
-      CHECK(run_dense(c, launch, s));
-      if (launch) {
-        LossGradArgs g = g0;
-        g.v0 = (int)v0;
-        g.n = (int)n;
-        const dim3 grid = layer_grid(T, 256, g.grid_x);
-        CHECK(launched(launch_kernel(layer_loss_grad_kernel<Tag>, grid, dim3(256), s, g)));
-      }
-      if (mdx.ptr && H > 0) {
-        void* const to = single ? const_cast<void*>(mdx.ptr) : acc;
-        const int64_t ld = single ? mdx.ld : H;
-        const DenseCall dx{T, H, n, dtype, false, false, g0.G, g0.ldg, w, mw.ld, v0 ? acc : nullptr, H, to, ld,
-                           single ? dtype : GEMM_DTYPE_F32};
-        CHECK(run_dense(dx, launch, s));
-      }
-      if (mdw.ptr && H > 0) {
-        char* const to = static_cast<char*>(const_cast<void*>(mdw.ptr)) + v0 * mdw.ld * mdw.elem;
-        const DenseCall dw{n, H, T, dtype, true, false, g0.G, g0.ldg, mx.ptr, mx.ld, accumulate ? to : nullptr, mdw.ld, to,
-                           mdw.ld, dw_dtype};
-        CHECK(run_dense(dw, launch, s));
-      }
+int run_grad(const LossPlan& q, const Mat& mx, const Mat& mw, const Mat& mdx, const Mat& mdw, int dtype, int dw_dtype,
+             bool accumulate, const int32_t* labels, const float* lse, const float* dloss, char* ws, bool launch, hipStream_t s) {
+  const int64_t T = mx.rows, V = mw.rows, H = mx.cols;
+  const unsigned most = 4096;  // workgroups of the kernels that walk
+  auto blocks = [&](int64_t n) { return dim3((unsigned)(n < most ? (n ? n : 1) : most)); };
+  const void* x = mx.ptr;
+  int64_t ldx = mx.ld;
+  if (q.T8 != T && mdw.ptr) {
+    const LossPadArgs a{static_cast<const unsigned short*>(mx.ptr), reinterpret_cast<unsigned short*>(ws + q.xpad), mx.ld,
+                        q.T8 * H, T * H, (int)H};
+    x = a.to;
+    ldx = H;
+    if (launch) CHECK(launched(launch_kernel(layer_loss_pad_kernel, blocks((a.n + 255) / 256), dim3(256), s, a)));
+  }
+  int* const offsets = reinterpret_cast<int*>(ws + q.offsets);
+  const int64_t last = V - (V - 1) / q.piece * q.piece;
+  if (mdx.ptr && launch)
+    CHECK(launched(launch_kernel(layer_loss_offsets_kernel, dim3(1), dim3(256), s, offsets, q.S,
+                                 (int)(q.piece < V ? q.piece : V), (int)last)));
+  void* const G = ws + q.g;
+  const bool tiles = loss_tiles(mx, mw, q.piece);
+  CHECK(loss_pieces(V, q.piece, [&](int64_t v0, int64_t n) -> int {
+    if (tiles) {
+      LossTileArgs a{};
+      a.W = loss_row(mw, v0);
+      a.X = mx.ptr;
+      a.ldw = mw.ld;
+      a.ldx = mx.ld;
+      a.n = (int)n;
+      a.T = (int)T;
+      a.H = (int)H;
+      a.v0 = (int)v0;
+      a.labels = labels;
+      a.V = (int)V;
+      a.lse = lse;
+      a.dloss = dloss;
+      a.G = G;
+      a.T8 = (int)q.T8;
+      if (launch) CHECK(launched(launch_loss_tiles(dtype, true, a, s)));
+    } else {
+      CHECK(loss_pieces(n, q.sub, [&](int64_t c0, int64_t m) -> int {
+        float* const l = reinterpret_cast<float*>(ws + q.glogits);
+        CHECK(run_dense(loss_logits(mx, mw, dtype, v0 + c0, m, l, q.sub), launch, s));
+        LossGradArgs a{};
+        a.L = l;
+        a.labels = labels;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.G = static_cast<unsigned short*>(G) + c0 * q.T8;
+        a.ldl = q.sub;
+        a.T = (int)T;
+        a.T8 = (int)q.T8;
+        a.V = (int)V;
+        a.v0 = (int)(v0 + c0);
+        a.n = (int)m;
+        const int64_t squares = ((m + 63) / 64) * ((q.T8 + 63) / 64);
+        if (squares > 0x7ffffff0) return fail(GEMM_ERR_UNSUPPORTED, "too many pieces of rows for one launch");
+        if (!launch) return GEMM_OK;
+        const dim3 grid = layer_grid(squares, 256, a.grid_x);
+        return launched(launch_kernel(layer_loss_grad_kernel<Tag>, grid, dim3(256), s, a));
+      }));
     }
-  if (!mdx.ptr || H == 0 || single) return GEMM_OK;
-  const int64_t n = T * H, blocks = (n + 255) / 256;
-  return launched(launch_kernel(layer_loss_round_kernel<Tag>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), s,
-                                (const float*)acc, static_cast<char*>(const_cast<void*>(mdx.ptr)), mdx.ld, n, (int)H));
+    if (mdx.ptr) {
+      const SumsCall c{q.S, n, q.T8, H, dtype, offsets + (v0 + q.piece >= V ? q.S + 1 : 0), G, q.T8, loss_row(mw, v0), mw.ld,
+                       q.direct ? const_cast<void*>(mdx.ptr) : ws + q.sums, q.direct ? mdx.ld : H, q.T8 * H,
+                       q.direct ? dtype : GEMM_DTYPE_F32, v0 > 0};
+      CHECK(run_sums(c, launch, s));
+    }
+    if (mdw.ptr) {
+      void* const to = const_cast<char*>(loss_row(mdw, v0));
+      const DenseCall c{n, H, q.T8, dtype, false, false, G, q.T8, x, ldx, accumulate ? to : nullptr, mdw.ld, to, mdw.ld, dw_dtype};
+      CHECK(run_dense(c, launch, s));
+    }
+    return GEMM_OK;
+  }));
+  if (!launch) return GEMM_OK;
+  if (mdx.ptr && !q.direct) {
+    const LossRoundArgs a{reinterpret_cast<const float*>(ws + q.sums), static_cast<unsigned short*>(const_cast<void*>(mdx.ptr)),
+                          mdx.ld, T * H, q.T8 * H, (int)H, q.S};
+    CHECK(launched(launch_kernel(layer_loss_round_kernel<Tag>, blocks((a.n + 1023) / 1024), dim3(256), s, a)));
+  }
+  set_path(std::string(tiles ? "loss_grad on 256x256 tiles" : "loss_grad from float32 logits") + " in pieces of " +
+           std::to_string(q.piece));
+  return GEMM_OK;
 }
 
 }  // namespace
@@ -190,7 +438,10 @@ using namespace dgt;
 
 extern "C" {
 
-int64_t gemm_loss_workspace(int64_t T, int64_t V, int64_t H) { return loss_bytes(T, V, H); }
+int64_t gemm_loss_workspace(int64_t T, int64_t V, int64_t H) {
+  LossPlan q{};
+  return loss_plan(T, V, H, q) ? q.forward : 0;
+}
 
 int gemm_loss(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t ldx, const void* W, int64_t ldw,
               const int32_t* labels, float* loss, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
@@ -201,9 +452,10 @@ int gemm_loss(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t
       set_path("noop: empty output");
       return GEMM_OK;
     }
-    const int64_t need = loss_bytes(T, V, H);
+    LossPlan q{};
+    if (!loss_plan(T, V, H, q)) return fail(GEMM_ERR_UNSUPPORTED, "the workspace would be too large");
     const Mat ml{"labels", labels, 1, T, T, 4}, mo{"loss", loss, 1, T, T, 4}, me{"lse", lse, 1, T, T, 4};
-    const Mat ms{"workspace", workspace, 1, need, need, 1};
+    const Mat ms{"workspace", workspace, 1, q.forward, q.forward, 1};
     if (H > 0) {
       CHECK(check_ptr(mx));
       CHECK(check_ptr(mw));
@@ -211,44 +463,22 @@ int gemm_loss(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t
     CHECK(check_ptr(ml));
     CHECK(check_ptr(mo));
     if (lse) CHECK(check_ptr(me));
-    CHECK(check_workspace(workspace, workspace_bytes, need));
+    CHECK(check_workspace(workspace, workspace_bytes, q.forward));
     for (const Mat* w : {&mo, &me, &ms})
       for (const Mat* r : {&mx, &mw, &ml}) CHECK(check_apart(*w, *r));
     CHECK(check_apart(me, mo));
     CHECK(check_apart(ms, mo));
     CHECK(check_apart(ms, me));
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t piece = loss_piece(T, V);
-    LossArgs a{};
-    a.state = static_cast<float*>(workspace);
-    float* const l = reinterpret_cast<float*>(static_cast<char*>(workspace) + round16(T * 12));
-    a.L = l;
-    a.labels = labels;
-    a.loss = loss;
-    a.lse = lse;
-    a.ldl = piece;
-    a.T = (int)T;
-    a.V = (int)V;
     for (int launch = 0; launch < 2; ++launch)
-      for (int64_t v0 = 0; v0 < V; v0 += piece) {
-        const int64_t n = V - v0 < piece ? V - v0 : piece;
-        const DenseCall c{T, n, H, dtype, false, true, X, ldx, static_cast<const char*>(W) + v0 * ldw * 2, ldw,
-                          nullptr, 0, l, piece, GEMM_DTYPE_F32};
-        CHECK(run_dense(c, launch, s));
-        if (!launch) continue;
-        a.v0 = (int)v0;
-        a.n = (int)n;
-        a.first = v0 == 0;
-        a.last = v0 + piece >= V;
-        const dim3 grid = layer_grid(T, 256, a.grid_x);
-        CHECK(launched(launch_kernel(layer_loss_rows_kernel, grid, dim3(256), s, a)));
-      }
-    set_path("loss in pieces of " + std::to_string(piece));
+      CHECK(run_loss(q, mx, mw, dtype, labels, loss, lse, static_cast<char*>(workspace), launch, static_cast<hipStream_t>(stream)));
     return GEMM_OK;
   });
 }
 
-int64_t gemm_loss_grad_workspace(int64_t T, int64_t V, int64_t H) { return loss_grad_bytes(T, V, H); }
+int64_t gemm_loss_grad_workspace(int64_t T, int64_t V, int64_t H) {
+  LossPlan q{};
+  return loss_plan(T, V, H, q) ? q.grad : 0;
+}
 
 int gemm_loss_grad(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t ldx, const void* W, int64_t ldw,
                    const int32_t* labels, const float* lse, const float* dloss, void* dX, int64_t lddx, void* dW,
@@ -271,36 +501,24 @@ int gemm_loss_grad(int64_t T, int64_t V, int64_t H, int dtype, const void* X, in
       const DenseCall c{V, H, 0, dtype, true, false, nullptr, V, nullptr, H, nullptr, 0, dW, lddw, dw_dtype};
       return run_dense(c, true, s);
     }
-    const int64_t need = loss_grad_bytes(T, V, H);
-    if (!need) return fail(GEMM_ERR_UNSUPPORTED, "the workspace would be too large");
+    LossPlan q{};
+    if (!loss_plan(T, V, H, q)) return fail(GEMM_ERR_UNSUPPORTED, "the workspace would be too large");
     const Mat ml{"labels", labels, 1, T, T, 4}, me{"lse", lse, 1, T, T, 4}, md{"dloss", dloss, 1, T, T, 4};
-    const Mat ms{"workspace", workspace, 1, need, need, 1};
+    const Mat ms{"workspace", workspace, 1, q.grad, q.grad, 1};
     for (const Mat* m : {&mx, &mw, &ml, &me, &md}) CHECK(check_ptr(*m));
-    CHECK(check_workspace(workspace, workspace_bytes, need));
+    CHECK(check_workspace(workspace, workspace_bytes, q.grad));
     for (const Mat* w : {&mdx, &mdw, &ms})
       for (const Mat* r : {&mx, &mw, &ml, &me, &md}) CHECK(check_apart(*w, *r));
     CHECK(check_apart(mdw, mdx));
     CHECK(check_apart(ms, mdx));
     CHECK(check_apart(ms, mdw));
-    const int64_t piece = loss_piece(T, V);
-    char* const ws = static_cast<char*>(workspace);
-    float* const l = reinterpret_cast<float*>(ws);
-    void* const g = ws + round16(T * piece * 4);
-    float* const acc = reinterpret_cast<float*>(static_cast<char*>(g) + round16(T * piece * 2));
-    LossGradArgs a{};
-    a.L = l;
-    a.labels = labels;
-    a.lse = lse;
-    a.dloss = dloss;
-    a.G = g;
-    a.ldl = a.ldg = piece;
-    a.T = (int)T;
-    a.V = (int)V;
-    const DenseCall c{T, 0, H, dtype, false, true, X, ldx, nullptr, ldw, nullptr, 0, l, piece, GEMM_DTYPE_F32};
-    CHECK(dtype == GEMM_DTYPE_F16
-              ? run_grad<TagF16>(a, c, acc, piece, mx, mw, mdx, mdw, accumulate != 0, dtype, dw_dtype, s)
-              : run_grad<TagBF16>(a, c, acc, piece, mx, mw, mdx, mdw, accumulate != 0, dtype, dw_dtype, s));
-    set_path("loss_grad in pieces of " + std::to_string(piece));
+    for (int launch = 0; launch < 2; ++launch) {
+      char* const ws = static_cast<char*>(workspace);
+      CHECK(dtype == GEMM_DTYPE_F16 ? run_grad<TagF16>(q, mx, mw, mdx, mdw, dtype, dw_dtype, accumulate != 0, labels, lse, dloss,
+                                                       ws, launch, s)
+                                    : run_grad<TagBF16>(q, mx, mw, mdx, mdw, dtype, dw_dtype, accumulate != 0, labels, lse, dloss,
+                                                        ws, launch, s));
+    }
     return GEMM_OK;
   });
 }

@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(64 * kSumWaves) layer_norm_sum_kernel(const No
 
 // Waves a row and pieces a lane that hold N columns, by rising width.
 constexpr int kNormForms = 7;
-constexpr int kNormWaves[kNormForms] = {1, 1, 1, 4, 4, 16, 16}, kNormPieces[kNormForms] = {1, 2, 4, 2, 4, 2, 4};
+constexpr int kNormWaves[kNormForms] = {1, 1, 2, 4, 4, 16, 16}, kNormPieces[kNormForms] = {1, 2, 2, 2, 4, 2, 4};
 int norm_form(int64_t N) {
   int f = 0;
   while (f < kNormForms && (int64_t)kNormWaves[f] * kNormPieces[f] * 512 < N) ++f;
@@ -510,7 +510,7 @@ hipError_t norm_for(int form, F f) {
   switch (form) {
     case 0: return f(LayerConst<1>{}, LayerConst<1>{});
     case 1: return f(LayerConst<1>{}, LayerConst<2>{});
-    case 2: return f(LayerConst<1>{}, LayerConst<4>{});
+    case 2: return f(LayerConst<2>{}, LayerConst<2>{});
     case 3: return f(LayerConst<4>{}, LayerConst<2>{});
     case 4: return f(LayerConst<4>{}, LayerConst<4>{});
     case 5: return f(LayerConst<16>{}, LayerConst<2>{});
