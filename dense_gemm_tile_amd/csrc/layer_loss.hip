@@ -26,14 +26,16 @@ namespace dgt {
 
 namespace {
 
-constexpr int kLossChunk = 4096;  // logits of a row that a workgroup takes
+constexpr int kLossStep = 4096;  // logits of a row that a workgroup holds at a time
 
 // Sub-piece of float32 logits, T x n: columns [v0, v0 + n) of the vocabulary.
 struct LossRowsArgs {
   const float* L;
   const int* labels;
-  float2* parts;        // of this sub-piece: [chunks][T]
+  float2* parts;        // of this sub-piece: [T]; null: it is the only one
   float* target;
+  float* loss;          // (the only one)
+  float* lse;           // null: not wanted
   int64_t ldl;
   int T, V, v0, n;
   unsigned grid_x;
@@ -65,47 +67,57 @@ __device__ __forceinline__ float2 loss_join(float2 a, float2 b) {
   return float2{m, a.y * loss_exp(a.x - base) + b.y * loss_exp(b.x - base)};
 }
 
-// A workgroup takes kLossChunk logits of a row.
-__global__ void __launch_bounds__(256) layer_loss_rows_kernel(const LossRowsArgs p) {
-  __shared__ float2 part[4];
-  const unsigned chunks = (unsigned)(p.n + kLossChunk - 1) / kLossChunk, id = layer_block(p);
-  const int64_t t = id / chunks;
+// A workgroup takes a row. (Rows cut over workgroups and joined by a second kernel: 61 rows of
+// 32001 9 us for both, 6 so.)
+constexpr int kRowThreads = 1024;
+__global__ void __launch_bounds__(kRowThreads) layer_loss_rows_kernel(const LossRowsArgs p) {
+  __shared__ float2 part[kRowThreads / 64];
+  const int64_t t = layer_block(p);
   if (t >= p.T) return;
-  const int chunk = id - (unsigned)t * chunks, c0 = chunk * kLossChunk;
   const float* l = p.L + t * p.ldl;
-  constexpr int PER = kLossChunk / 1024;
-  float f[PER][4], m = -__builtin_inff(), s = 0.0f;
+  constexpr int PER = 8 * kLossStep / (4 * kRowThreads);  // fours of eight steps, in flight together
+  float2 a{-__builtin_inff(), 0.0f};
+  for (int64_t c0 = 0; c0 < p.n; c0 += 8 * kLossStep) {
+    f32x4 f[PER];
+    float m = a.x;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = c0 + 1024 * i + 4 * threadIdx.x;
-    if (c + 4 <= p.n) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(l + c);
+    for (int i = 0; i < PER; ++i) {
+      const int64_t c = c0 + kLossStep * i + 4 * threadIdx.x;
+      if (c + 4 <= p.n) {
+        f[i] = *reinterpret_cast<const f32x4*>(l + c);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[i][e] = v[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[i][e] = c + e < p.n ? l[c + e] : -__builtin_inff();
+        for (int e = 0; e < 4; ++e) f[i][e] = c + e < p.n ? l[c + e] : -__builtin_inff();
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = __builtin_fmaxf(m, f[i][e]);
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = __builtin_fmaxf(m, f[i][e]);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    a.y *= loss_exp(a.x - base);
+    a.x = m;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a.y += loss_exp(f[i][e] - base);
   }
-  const float base = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s += loss_exp(f[i][e] - base);
-  float2 a{m, s};
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) a = loss_join(a, float2{__shfl_xor(a.x, d, 64), __shfl_xor(a.y, d, 64)});
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
   if (threadIdx.x) return;
-  for (int w = 1; w < 4; ++w) a = loss_join(a, part[w]);
-  p.parts[(int64_t)chunk * p.T + t] = a;
+  for (int w = 1; w < kRowThreads / 64; ++w) a = loss_join(a, part[w]);
   const int label = p.labels[t];
-  if ((unsigned)label >= (unsigned)p.V) return;
-  const int at = label - p.v0;
-  if (at >= c0 && at < p.n && at - c0 < kLossChunk) p.target[t] = l[at];
+  const bool has = (unsigned)label < (unsigned)p.V, here = has && label >= p.v0 && label - p.v0 < p.n;
+  if (p.parts) {
+    p.parts[t] = a;
+    if (here) p.target[t] = l[label - p.v0];
+  } else {
+    const float lse = a.x + logf(a.y);
+    p.loss[t] = has ? lse - l[label] : 0.0f;
+    if (p.lse) p.lse[t] = lse;
+  }
 }
 
 // The parts of 64 tokens: every kJoinWaves-th for each wave, joined in wave order.
@@ -210,9 +222,9 @@ struct LossPlan {
 // False where the bytes pass 63 bits.
 bool loss_plan(int64_t T, int64_t V, int64_t H, LossPlan& q) {
   if (T < 1 || V < 1 || H < 0 || T > kMaxDim || V > kMaxDim || H > kMaxDim) return false;
-  auto columns = [&](int64_t elements) {  // of T tokens each, whole chunks, at least one
-    int64_t n = elements / T / kLossChunk * kLossChunk;
-    if (n < kLossChunk) n = kLossChunk;
+  auto columns = [&](int64_t elements) {  // of T tokens each, whole steps, at least one
+    int64_t n = elements / T / kLossStep * kLossStep;
+    if (n < kLossStep) n = kLossStep;
     return n < V ? n : (V + 7) / 8 * 8;
   };
   q.T8 = (T + 7) / 8 * 8;
@@ -313,22 +325,24 @@ int run_loss(const LossPlan& q, const Mat& mx, const Mat& mw, int dtype, const i
       LossRowsArgs a{};
       a.L = l;
       a.labels = labels;
-      a.parts = parts + Q * T;
+      a.parts = n < V ? parts + Q * T : nullptr;
       a.target = target;
+      a.loss = loss;
+      a.lse = lse;
       a.ldl = q.sub;
       a.T = (int)T;
       a.V = (int)V;
       a.v0 = (int)v0;
       a.n = (int)n;
-      const int64_t chunks = (n + kLossChunk - 1) / kLossChunk;
-      Q += chunks;
-      if (chunks * T > 0x7ffffff0) return fail(GEMM_ERR_UNSUPPORTED, "too many pieces of rows for one launch");
+      ++Q;
       if (!launch) return GEMM_OK;
-      const dim3 grid = layer_grid(chunks * T, 256, a.grid_x);
-      return launched(launch_kernel(layer_loss_rows_kernel, grid, dim3(256), s, a));
+      const dim3 grid = layer_grid(T, kRowThreads, a.grid_x);
+      return launched(launch_kernel(layer_loss_rows_kernel, grid, dim3(kRowThreads), s, a));
     }));
   }
   if (!launch) return GEMM_OK;
+  set_path(tiles ? "loss on 256x256 tiles" : "loss in pieces of " + std::to_string(q.sub));
+  if (!tiles && Q == 1) return GEMM_OK;
   LossJoinArgs j{};
   j.parts = parts;
   j.target = target;
@@ -339,9 +353,7 @@ int run_loss(const LossPlan& q, const Mat& mx, const Mat& mw, int dtype, const i
   j.V = (int)V;
   j.Q = (int)Q;
   const dim3 grid = layer_grid((T + 63) / 64, 64 * kJoinWaves, j.grid_x);
-  CHECK(launched(launch_kernel(layer_loss_join_kernel, grid, dim3(64 * kJoinWaves), s, j)));
-  set_path(tiles ? "loss on 256x256 tiles" : "loss in pieces of " + std::to_string(q.sub));
-  return GEMM_OK;
+  return launched(launch_kernel(layer_loss_join_kernel, grid, dim3(64 * kJoinWaves), s, j));
 }
 
 template <class Tag>
