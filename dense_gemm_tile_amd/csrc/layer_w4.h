@@ -26,6 +26,10 @@ struct W4Args {
   int group;
 };
 
+// Groups of K values that a call may have: 16 columns of scales and zero points, in LDS beside the
+// slices of 8 waves.
+constexpr int kW4MaxRuns = 1536;
+
 // The launches, a file for each type.
 hipError_t launch_w4_f16(const W4Args& p, hipStream_t s);
 hipError_t launch_w4_bf16(const W4Args& p, hipStream_t s);
@@ -106,8 +110,9 @@ __device__ __forceinline__ LayerTile w4_tile(const LayerArgs& p, int t, int tota
 __device__ __forceinline__ u32x4 w4_values(const char* row, int k, int K) {
   u32x4 v = {0u, 0u, 0u, 0u};
   if (k + 8 <= K) return *reinterpret_cast<const u32x4_at2*>(row + (int64_t)k * 2);
+  if (k >= K) return v;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
+  for (int e = 0; e < 7; ++e)
     if (k + e < K) v[e / 2] |= (unsigned)*reinterpret_cast<const unsigned short*>(row + (int64_t)(k + e) * 2) << (16 * (e % 2));
   return v;
 }
@@ -115,75 +120,13 @@ __device__ __forceinline__ u32x4 w4_values(const char* row, int k, int K) {
 __device__ __forceinline__ unsigned w4_word(const char* row, int k, int K) {
   if (k + 8 <= K) return *reinterpret_cast<const u32_at1*>(row + k / 2);
   unsigned q = 0;
+  if (k >= K) return q;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (k + 2 * e < K) q |= (unsigned)(unsigned char)row[k / 2 + e] << (8 * e);
   return q;
 }
 
-template <class Tag, int MODE, int MT, int NT, int KW>
-__global__ void __launch_bounds__(KW * 64, 2) layer_w4_kernel(const W4Args p) {
-  using At = SplitAtom;
-  using Sum = SplitSum<MT, NT, KW>;
-  __shared__ __attribute__((aligned(1024))) char smem[Sum::LDS_BYTES];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int total = layer_tiles<MODE, Sum::BM>(p.a, lane);
-  if ((int)blockIdx.x >= total) return;  // by rows the grid is an upper bound
-  int g;
-  const LayerTile q = w4_tile<MODE, Sum::BM, Sum::BN>(p.a, blockIdx.x, total, lane, g);
-
-  At::acc_t acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][n][v] = 0.0f;
-  const int r16 = lane & 15, oct = lane >> 4;
-  const char* scale[NT];
-  const char* zero[NT];
-  const char* codes[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    // (Columns past N repeat the last one; nothing of theirs is stored.)
-    int col = q.n0 + 16 * n + r16;
-    if (col >= q.N) col = q.N - 1;
-    codes[n] = q.B + (int64_t)col * p.a.ldb;
-    const int64_t at = ((int64_t)g * p.stride_s + (int64_t)col * p.lds) * 2;
-    scale[n] = static_cast<const char*>(p.scales) + at;
-    zero[n] = static_cast<const char*>(p.zeros) + at;
-  }
-  const u32x4 ones = {W4Type<Tag>::ONES, W4Type<Tag>::ONES, W4Type<Tag>::ONES, W4Type<Tag>::ONES};
-  const At::acc_t none = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = 32 * w; k0 < q.K; k0 += 32 * KW) {
-    u32x4 x[MT];
-    At::acc_t sx[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int row = q.m0 + 16 * i + r16;
-      x[i] = u32x4{0u, 0u, 0u, 0u};
-      if (row < q.M) x[i] = w4_order(w4_values(q.A + (int64_t)row * p.a.lda * 2, k0 + 8 * oct, q.K));
-      sx[i] = At::mma(Tag{}, x[i], ones, none);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const u32x4 c = w4_codes<Tag>(w4_word(codes[n], k0 + 8 * oct, q.K));
-      const int j = k0 / p.group;
-      const float s = layer_f32(Tag{}, reinterpret_cast<const unsigned short*>(scale[n])[j]);
-      const float z = 16.0f + (p.zeros ? layer_f32(Tag{}, reinterpret_cast<const unsigned short*>(zero[n])[j]) : 8.0f);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const At::acc_t d = At::mma(Tag{}, x[i], c, none);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][n][v] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[i][v], d[v]), acc[i][n][v]);
-      }
-    }
-  }
-  Sum::template finish<Tag>(acc, p.a, q, smem, tid, w);
-}
-
-// ------------------------------------------------------- whole 16-byte pieces --
 // As layer_split.hip does for 16-bit weights: each wave takes slices of 128 K values, every
 // KW-th, and loads them straight into LDS of its own, without a barrier; consecutive
 // lanes load consecutive bytes. A is the bulk of a slice where there are many rows, so it
@@ -196,8 +139,14 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_kernel(const W4Args p) {
 // 4 bytes that each lane reads for 32 K values lie in banks of their own. Rows of A
 // past the tile hold anything: they reach only outputs that are not stored.
 //
-// GRP: K values between which the sums are scaled: 32 or 64 where that is the group, else
-// 128.
+// WHOLE: operands in whole 16-byte pieces. Others, at any pitch and alignment, go through
+// registers to the same places in LDS: consecutive lanes still load consecutive bytes, 16 a
+// lane wherever they lie, and the last slice's ends element by element. (Fragments
+// straight from memory, whose neighbouring lanes lie in different rows, take the address
+// units four times as long: 257x1000x1032 16 us, 10 so.)
+//
+// GRP: K values between which the sums are scaled: 128 or 64 where the group is a multiple of
+// it, else 32.
 
 // The scales of a workgroup's columns lie in LDS, in rows of w4_pitch(): loaded where
 // they are used they cost as many requests as the codes do (64 experts of 2 rows,
@@ -206,21 +155,9 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_kernel(const W4Args p) {
 // Bytes of a column's scales in LDS: whole slices, and an odd number of 8 bytes, so that 16
 // columns lie in banks of their own.
 __host__ __device__ inline int w4_pitch(int K, int group) {
-  const int runs = group >= 128 ? (K + group - 1) / group : (K + 127) / 128 * (128 / group);
-  return (runs * 2 + 7) / 8 * 8 | 8;
+  const int64_t runs = ((int64_t)(K + 127) / 128 * 128 + group - 1) / group;
+  return (int)((runs * 2 + 7) / 8 * 8 | 8);
 }
-template <int S>
-struct W4Scales {  // S neighbouring ones
-  uint64_t v;
-  __device__ __forceinline__ void load(const char* p) {
-    if constexpr (S == 1) v = *reinterpret_cast<const unsigned short*>(p);
-    else if constexpr (S == 2) v = *reinterpret_cast<const unsigned*>(p);
-    else v = *reinterpret_cast<const uint64_t*>(p);
-  }
-  template <class Tag>
-  __device__ __forceinline__ float get(int i) const { return layer_f32(Tag{}, (unsigned short)(v >> (16 * i))); }
-};
-
 // A wave's part of the slices, and a workgroup's LDS beside the scales. (Rows past the
 // tile are read; the waves' sums overlay the slices.)
 template <int AL, int NT>
@@ -231,7 +168,7 @@ constexpr int w4_lds() {
   return USED > SplitSum<MT, NT, KW>::LDS_BYTES ? USED : SplitSum<MT, NT, KW>::LDS_BYTES;
 }
 
-template <class Tag, int MODE, int AL, int NT, int GRP, bool ZEROS, int KW>
+template <class Tag, int MODE, int AL, int NT, int GRP, bool ZEROS, int KW, bool WHOLE>
 __global__ void __launch_bounds__(KW * 64, 2) layer_w4_split_kernel(const W4Args p) {
   using At = SplitAtom;
   constexpr int MT = (AL + 1) / 2, BM = 8 * AL;
@@ -255,7 +192,7 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_split_kernel(const W4Args
   const auto ra = make_rsrc_n(Ab, split_records(q.M - q.m0, p.a.lda, q.K));
   const char* const Bb = q.B + (int64_t)q.n0 * p.a.ldb;
   const int rows_b = q.N - q.n0 < Sum::BN ? q.N - q.n0 : Sum::BN;
-  const auto rb = make_rsrc_n(Bb, (unsigned)((rows_b - 1) * (int)p.a.ldb + q.K / 2));
+  const auto rb = make_rsrc_n(Bb, WHOLE ? (unsigned)((rows_b - 1) * (int)p.a.ldb + q.K / 2) : 0u);
   At::acc_t acc[MT][NT], sx[MT], dot[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -276,35 +213,86 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_split_kernel(const W4Args
     const int s = j * KW + w + start;
     return j >= NJ ? KT : s >= KT ? s - KT : s;
   };
-  auto request_a = [&](int h, int j) {
-    SA::request(ra, (int)(p.a.lda * 2), q.M - q.m0, q.K, 2 * slice_of(j) + h, mine + h * A_HALF, lane);
+  u32x4 ra_next[WHOLE ? 1 : 2][WHOLE ? 1 : AL], rb_next[WHOLE ? 1 : 2][WHOLE ? 1 : NT];  // (not WHOLE) on their way
+  auto request_a = [&](int h, int j) __attribute__((always_inline)) {
+    const int at = 2 * slice_of(j) + h;  // slice of 64
+    if constexpr (WHOLE) {
+      SA::request(ra, (int)(p.a.lda * 2), q.M - q.m0, q.K, at, mine + h * A_HALF, lane);
+    } else if (at < 2 * KT) {
+      auto from = [&](int i, int& k) {
+        const int r = 8 * i + (lane >> 3), row = r < q.M - q.m0 ? r : q.M - q.m0 - 1;  // (a tile has a row)
+        k = at * 64 + 8 * ((lane & 7) ^ SA::Op::swz(r));
+        return Ab + (int64_t)row * p.a.lda * 2;
+      };
+      if ((int64_t)at * 64 + 64 <= q.K) {
+#pragma unroll
+        for (int i = 0; i < AL; ++i) {
+          int k;
+          const char* const row = from(i, k);
+          ra_next[h][i] = *reinterpret_cast<const u32x4_at2*>(row + (int64_t)k * 2);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < AL; ++i) {
+          int k;
+          const char* const row = from(i, k);
+          ra_next[h][i] = w4_values(row, k, q.K);
+        }
+      }
+    }
   };
-  auto request_b = [&](int d, int j) {
+  auto request_b = [&](int d, int j) __attribute__((always_inline)) {
     const int slice = slice_of(j);
+    const bool whole = (int64_t)slice * 128 + 128 <= q.K;
+    if (!WHOLE && slice >= KT) return;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = 16 * n + (lane >> 2), k = 128 * slice + 32 * ((lane & 3) ^ (r >> 2 & 3));
-      const int off = r < rows_b && k < q.K ? r * (int)p.a.ldb + k / 2 : kOutOfRange;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (pp_lds_ptr_t)(codes + d * B_SLICE + n * 1024), 16, off, 0, 0, 0);
+      if constexpr (WHOLE) {
+        const int off = r < rows_b && k < q.K ? r * (int)p.a.ldb + k / 2 : kOutOfRange;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (pp_lds_ptr_t)(codes + d * B_SLICE + n * 1024), 16, off, 0, 0, 0);
+      } else {
+        const char* const from = Bb + (int64_t)(r < rows_b ? r : rows_b - 1) * p.a.ldb;
+        if (whole) {
+          rb_next[d][n] = *reinterpret_cast<const u32x4_at1*>(from + k / 2);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rb_next[d][n][e] = w4_word(from, k + 8 * e, q.K);
+        }
+      }
     }
   };
   const u32x4 ones = {W4Type<Tag>::ONES, W4Type<Tag>::ONES, W4Type<Tag>::ONES, W4Type<Tag>::ONES};
   const At::acc_t none = {0.0f, 0.0f, 0.0f, 0.0f};
   // Loads are asked for in the order A(j, 0) B(j + 1) A(j, 1) A(j + 1, 0) B(j + 2) ...: after
   // each half of A one of B and one half of A.
-  auto landed = [] {
-    layer_fixed_order();
-    pp_wait_vm<AL + NT>();
-    layer_fixed_order();
+  auto landed = [&](int h, int d) __attribute__((always_inline)) {
+    if constexpr (WHOLE) {
+      layer_fixed_order();
+      pp_wait_vm<AL + NT>();
+      layer_fixed_order();
+    } else {
+#pragma unroll
+      for (int i = 0; i < AL; ++i) *reinterpret_cast<u32x4*>(mine + h * A_HALF + i * 1024 + lane * 16) = ra_next[h][i];
+      if (h == 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<u32x4*>(codes + d * B_SLICE + n * 1024 + lane * 16) = rb_next[d][n];
+      }
+      layer_wave_order();
+    }
   };
-  auto slice = [&](int d, int j) {
+  auto slice = [&](int d, int j) __attribute__((always_inline)) {
     const int at128 = slice_of(j);
-    const char* const runs_at = scales + r16 * pitch + (S == 1 ? 128 * at128 / p.group : S * at128) * 2;
+    int run[S];  // of each scale of the slice
+#pragma unroll
+    for (int u = 0; u < S; ++u)
+      run[u] = p.group == GRP ? S * at128 + u : (128 * at128 + GRP * u) / p.group;
     unsigned c[NT][4];
     float s[NT][S], z[NT][S];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      landed();
+      landed(h, d);
       u32x4 x[MT][2];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -317,17 +305,15 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_split_kernel(const W4Args
           for (int m = 0; m < 4; ++m)
             c[n][m] = *reinterpret_cast<const unsigned*>(codes + d * B_SLICE + n * 1024 + r16 * 64 +
                                                          ((m ^ (r16 >> 2)) << 4) + oct * 4);
-          W4Scales<S> sc, zr;
-          sc.load(runs_at + 16 * n * pitch);
-          if constexpr (ZEROS) zr.load(runs_at + (16 * n + Sum::BN) * pitch);
 #pragma unroll
           for (int u = 0; u < S; ++u) {
-            s[n][u] = sc.template get<Tag>(u);
-            z[n][u] = ZEROS ? 16.0f + zr.template get<Tag>(u) : 24.0f;
+            const char* const at = scales + (16 * n + r16) * pitch + run[u] * 2;
+            s[n][u] = layer_f32(Tag{}, *reinterpret_cast<const unsigned short*>(at));
+            z[n][u] = ZEROS ? 16.0f + layer_f32(Tag{}, *reinterpret_cast<const unsigned short*>(at + Sum::BN * pitch)) : 24.0f;
           }
         }
       }
-      pp_wait_lgkm0();  // read before the places are filled again
+      if constexpr (WHOLE) pp_wait_lgkm0();  // read before the places are filled again
       layer_fixed_order();
       request_a(h, j + 1);
       if (h == 0) request_b(d, j + 2);
@@ -408,37 +394,42 @@ unsigned w4_grid(LayerArgs& a, int bm, int bn) {
   return (unsigned)(((int64_t)a.M + g * (bm - 1)) / bm * a.tiles_n);
 }
 
-template <class Tag, int MODE, int MT, int NT, int KW>
-hipError_t launch(W4Args p, hipStream_t s) {
-  const unsigned n = w4_grid(p.a, 16 * MT, 16 * NT);
-  return launch_kernel(layer_w4_kernel<Tag, MODE, MT, NT, KW>, dim3(n), dim3(KW * 64), s, p);
-}
-template <class Tag, int MODE, int AL, int NT, int KW>
+template <class Tag, int MODE, int AL, int NT, int KW, bool WHOLE = true>
 struct W4Split {
-  static size_t scales(const W4Args& p) { return (size_t)w4_pitch(p.a.K, p.group) * 16 * NT * (p.zeros ? 2 : 1); }
+  static int64_t scales(const W4Args& p) { return (int64_t)w4_pitch(p.a.K, p.group) * 16 * NT * (p.zeros ? 2 : 1); }
   // Whether so many workgroups fit a CU.
   static bool fits(const W4Args& p, int count = 1) {
+    if (AL * NT >= 32 && p.group % 128) return false;  // (with smaller groups such a tile spills)
     return (w4_lds<AL, NT, KW>() + scales(p)) * count <= 160 * 1024;
   }
   static hipError_t launch(W4Args p, hipStream_t s) {
     const dim3 grid(w4_grid(p.a, 8 * AL, 16 * NT)), block(KW * 64);
     auto go = [&](auto grp) {
       constexpr int GRP = decltype(grp)::value;
-      if (p.zeros) return launch_kernel_lds(layer_w4_split_kernel<Tag, MODE, AL, NT, GRP, true, KW>, grid, block, scales(p), s, p);
-      return launch_kernel_lds(layer_w4_split_kernel<Tag, MODE, AL, NT, GRP, false, KW>, grid, block, scales(p), s, p);
+      const size_t lds = (size_t)scales(p);
+      if (p.zeros)
+        return launch_kernel_lds(layer_w4_split_kernel<Tag, MODE, AL, NT, GRP, true, KW, WHOLE>, grid, block, lds, s, p);
+      return launch_kernel_lds(layer_w4_split_kernel<Tag, MODE, AL, NT, GRP, false, KW, WHOLE>, grid, block, lds, s, p);
     };
-    if (p.group == 32) return go(LayerConst<32>{});
-    if (p.group == 64) return go(LayerConst<64>{});
-    return go(LayerConst<128>{});
+    if (p.group % 128 == 0) return go(LayerConst<128>{});
+    if constexpr (AL * NT >= 32) return hipErrorInvalidValue;  // (does not fit)
+    else if constexpr (WHOLE) return p.group % 64 == 0 ? go(LayerConst<64>{}) : go(LayerConst<32>{});
+    else return go(LayerConst<32>{});
   }
 };
-// Whether operands come in whole 16-byte pieces that 32-bit offsets reach, with groups that
-// slices of 128 are cut into or consist of.
+// Whether operands come in whole 16-byte pieces that 32-bit offsets reach.
 bool w4_whole(const W4Args& p) {
   const LayerArgs& a = p.a;
-  return a.K > 0 && a.K % 32 == 0 && (p.group == 32 || p.group == 64 || p.group % 128 == 0) &&
-         (uintptr_t)a.A % 16 == 0 && a.lda % 8 == 0 && (uintptr_t)a.B % 16 == 0 && a.ldb % 16 == 0 &&
+  return a.K % 32 == 0 && (uintptr_t)a.A % 16 == 0 && a.lda % 8 == 0 && (uintptr_t)a.B % 16 == 0 && a.ldb % 16 == 0 &&
          (a.G <= 1 || a.stride_b % 16 == 0) && a.lda < (1 << 23) && a.ldb < (1 << 24);
+}
+// The first of the forms that fits. (The last, of 16 x 16 tiles, holds the scales of kW4MaxRuns
+// groups.)
+template <class Form, class... Forms>
+hipError_t w4_first(const W4Args& p, hipStream_t s) {
+  if constexpr (sizeof...(Forms) > 0)
+    if (!Form::fits(p)) return w4_first<Forms...>(p, s);
+  return Form::launch(p, s);
 }
 // Tiles, measured (us; f16, waves x rows x columns):
 //   1x4096x4096    8x8x16 6.0, 16x8x16 6.3, 4x8x16 7.2
@@ -448,49 +439,42 @@ bool w4_whole(const W4Args& p) {
 //   256x4096x4096  6x64x64 19.1, 6x64x32 25.3, 8x32x64 22.1
 //   64 experts of 2 rows, 2048x2048: 4x8x64 41, 4x8x32 42, 2x8x64 47, 8x8x64 73; with 8 KiB
 //   more of LDS, for two workgroups a CU instead of three, 4x8x64 55
+// and through registers:
+//   257x1000x1032  4x16x32 9.8, 4x32x16 10.6, 8x48x32 10.5, 4x32x32 11.9, 8x32x32 15.4, 7x64x32 19
+//   512x4096x4104  4x32x64 48, 4x32x32 56, 7x64x32 77, 8x32x32 84
+//   48x4096x4104   8x32x32 13.2, 8x48x32 16.0, 8x32x16 21.5
 template <class Tag, int MODE>
 hipError_t launch_rows(const W4Args& p, hipStream_t s) {
   const LayerArgs& a = p.a;
-  if (w4_whole(p)) {
-    if constexpr (MODE == LAYER_ROWS) {
-      const int64_t rows = ((int64_t)a.M + a.G - 1) / a.G;  // of a group, on average
-      if (rows <= 8) {
-        using Wide = W4Split<Tag, MODE, 1, 4, 4>;
-        using Slim = W4Split<Tag, MODE, 1, 2, 4>;
-        if (Wide::fits(p, 3)) return Wide::launch(p, s);
-        if (Slim::fits(p)) return Slim::launch(p, s);
-      } else if (rows <= 16) {
-        using Wide = W4Split<Tag, MODE, 2, 2, 4>;
-        if (Wide::fits(p)) return Wide::launch(p, s);
-      } else {
-        using Wide = W4Split<Tag, MODE, 4, 4, 4>;
-        if (Wide::fits(p)) return Wide::launch(p, s);
-      }
-    } else {
-      using Wide64 = W4Split<Tag, MODE, 8, 4, 6>;
-      using Slim64 = W4Split<Tag, MODE, 8, 2, 7>;
-      using Slim48 = W4Split<Tag, MODE, 6, 2, 8>;
-      using Slim32 = W4Split<Tag, MODE, 4, 2, 8>;
-      if (a.M > 32) {
-        if (((int64_t)a.M + 63) / 64 * (((int64_t)a.N + 63) / 64) >= 256 && Wide64::fits(p)) return Wide64::launch(p, s);
-        if (a.M <= 48 && Slim48::fits(p)) return Slim48::launch(p, s);
-        if (Slim64::fits(p)) return Slim64::launch(p, s);
-      }
-      if (a.M > 16 && Slim32::fits(p)) return Slim32::launch(p, s);
-      if (a.M <= 16) {
-        using Wide16 = W4Split<Tag, MODE, 2, 2, 8>;
-        using Wide8 = W4Split<Tag, MODE, 1, 2, 8>;
-        using Slim8 = W4Split<Tag, MODE, 1, 1, 8>;
-        if (a.M > 8 && Wide16::fits(p)) return Wide16::launch(p, s);
-        if (a.M <= 8 && a.N > 16 * 256 && Wide8::fits(p)) return Wide8::launch(p, s);
-        if (a.M <= 8 && Slim8::fits(p)) return Slim8::launch(p, s);
-      }
-    }
-  }
+  // Rows of a group, on average.
   const int64_t rows = MODE == LAYER_ROWS ? ((int64_t)a.M + a.G - 1) / a.G : a.M;
-  if (rows <= 16) return launch<Tag, MODE, 1, 1, 8>(p, s);
-  if (rows <= 32) return launch<Tag, MODE, 2, 1, 8>(p, s);
-  return launch<Tag, MODE, 4, 2, 8>(p, s);
+  if (!w4_whole(p)) {
+    using R16 = W4Split<Tag, MODE, 2, 1, 8, false>;
+    if (rows <= 16) return R16::launch(p, s);
+    // (Twice the columns, 4x32x64, take 48 us instead of 56, but spill with groups of 32.)
+    if (((int64_t)a.M + 31) / 32 * (((int64_t)a.N + 31) / 32) >= 1024)
+      return w4_first<W4Split<Tag, MODE, 4, 2, 4, false>, R16>(p, s);
+    if (a.K >= 2048) return w4_first<W4Split<Tag, MODE, 4, 2, 8, false>, R16>(p, s);
+    return w4_first<W4Split<Tag, MODE, 2, 2, 4, false>, R16>(p, s);
+  }
+  using Last = W4Split<Tag, MODE, 2, 1, 8>;
+  if constexpr (MODE == LAYER_ROWS) {
+    using Wide8 = W4Split<Tag, MODE, 1, 4, 4>;
+    if (rows <= 8 && Wide8::fits(p, 3)) return Wide8::launch(p, s);
+    if (rows <= 8) return w4_first<W4Split<Tag, MODE, 1, 2, 4>, Last>(p, s);
+    if (rows <= 16) return w4_first<W4Split<Tag, MODE, 2, 2, 4>, Last>(p, s);
+    return w4_first<W4Split<Tag, MODE, 4, 4, 4>, Last>(p, s);
+  } else {
+    if (rows <= 8 && a.N <= 16 * 256) return w4_first<W4Split<Tag, MODE, 1, 1, 8>, Last>(p, s);
+    if (rows <= 8) return w4_first<W4Split<Tag, MODE, 1, 2, 8>, Last>(p, s);
+    if (rows <= 16) return w4_first<W4Split<Tag, MODE, 2, 2, 8>, Last>(p, s);
+    using Slim32 = W4Split<Tag, MODE, 4, 2, 8>;
+    if (rows <= 32) return w4_first<Slim32, Last>(p, s);
+    using Wide64 = W4Split<Tag, MODE, 8, 4, 6>;
+    if (((int64_t)a.M + 63) / 64 * (((int64_t)a.N + 63) / 64) >= 256 && Wide64::fits(p)) return Wide64::launch(p, s);
+    if (rows <= 48) return w4_first<W4Split<Tag, MODE, 6, 2, 8>, Slim32, Last>(p, s);
+    return w4_first<W4Split<Tag, MODE, 8, 2, 7>, Slim32, Last>(p, s);
+  }
 }
 
 template <class Tag>

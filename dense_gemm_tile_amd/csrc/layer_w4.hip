@@ -20,7 +20,8 @@ int run_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t*
   CHECK(check_act(act));
   if (group < 32 || group % 32) return bad("%s=%lld is not a multiple of 32", "group", group);
   const int osz = out_dtype == GEMM_DTYPE_F32 ? 4 : 2;
-  const int64_t g = dense ? 1 : G, runs = (K + group - 1) / group;
+  const int64_t g = dense ? 1 : G, runs = K / group + (K % group != 0);
+  if (runs > kW4MaxRuns) return fail(GEMM_ERR_UNSUPPORTED, "more than 1536 groups of K values");
   if (ldb % 2) return bad("%s=%lld is odd: a row of codes starts in a byte's lower half", "ldb", ldb);
   if (!dense && g > 1) {
     if (stride_b < 0 || stride_b % 2) return bad("%s=%lld is negative or odd", "stride_b", stride_b);

@@ -286,11 +286,14 @@ GEMM_API int gemm_gate_grad(int64_t T, int64_t E, int64_t top, int dtype, const 
  * scales    N x ceil(K / group) values of `dtype`, leading dimension lds.
  * zeros     the same for the zero points (any values, 7.5 as well as 8), or NULL
  *           for 8 everywhere.
- * group     codes that share a scale: a multiple of 32.
+ * group     codes that share a scale: a multiple of 32. A row has at most 1536
+ *           groups.
  * bias, act, R, Y, out_dtype: as in gemm_linear. K == 0 leaves act(bias) + R.
  *
  * The codes' products are summed group by group in float32, and each group's sum
- * is scaled in float32: no weight is rounded.
+ * is scaled in float32: no weight is rounded. (The sums are of code + 16 and of
+ * A's values, whose difference has no value where A holds an infinity: its row of
+ * Y is NaN.)
  */
 GEMM_API int gemm_linear_w4(int64_t M, int64_t N, int64_t K, int dtype, const void* A, int64_t lda,
                   const void* B, int64_t ldb, const void* scales, const void* zeros, int64_t lds,
