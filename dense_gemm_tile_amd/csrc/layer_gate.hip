@@ -8,7 +8,7 @@
 // A wave takes a token. Choices are whole numbers and must not hang on a rounding, so
 // keys count as they are in 64 bits; in 64 bits throughout, the exponentials and the
 // search take most of the time (16384 tokens, 8 of 256 experts in groups, with the
-// gradient: 68 us, 20 so). So keys are made and searched in float32, with a bound
+// gradient: 68 us, 30 so). So keys are made and searched in float32, with a bound
 // of their error, and a token two of whose keys come too close for it is done again in
 // 64 bits.
 #include "layer.h"
@@ -237,6 +237,16 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
   }
 }
 
+// exp(x) within 2^-22 of itself, and 1 / (1 + exp(-x)) within 2^-21: the exponent of 2 in two
+// floats, so that its rounding does not grow with it. (The library's exponential and
+// division: 16384 tokens, 8 of 256 experts with a bias 18 us, 16 so.)
+__device__ __forceinline__ float gate_exp(float x) {
+  const float c = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);
+  const float hi = c * kLog2e, lo = __builtin_fmaf(c, 1.92596298e-8f, __builtin_fmaf(c, kLog2e, -hi));
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return e < __builtin_inff() ? __builtin_fmaf(e, 0.6931471805599453f * lo, e) : e;
+}
+__device__ __forceinline__ float gate_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + gate_exp(-x)); }
 // Numbers as integers of the same order (NaN has no place).
 __device__ __forceinline__ unsigned gate_order32(float v) {
   const unsigned u = __builtin_bit_cast(unsigned, v);
@@ -291,18 +301,19 @@ __device__ __forceinline__ void gate_store_row(void* p, int64_t at, int lanes, i
 // integer of the float32 key's order; the largest one below the last choice is the largest of
 // (key - last) as unsigned numbers, so nothing is removed. Its lowest bits say whose it
 // is, in place of a search:
-//   ranked by logits (without a bias their order is the scores'): the expert's number from
-//     behind, so that keys of a token differ and of equal logits the first expert's is
-//     larger. Exact for 16-bit logits, which have zeros there, and for float32 ones that
-//     differ above these bits.
-//   ranked by scores: the lane's item from behind; the lane is the one that has the key.
-//     Two keys next to each other in the order have to be further apart than their errors: a
-//     score's, relative, of 2^-21 (sigmoid: an exponential, an addition and a division, one or
-//     half a step each) or 2^-17 (softmax: the largest logit taken off first, half a step of
-//     a number below 128 where the score is not 0 to float32, 2^-18; the sum, whose
-//     additions one after the other are PER + 6 at most), half a step more for the bias, and
-//     for the lowest bits 2^-19 or, of a group's rank, 2^-17.
-// (Experts' numbers in the lowest bits of scores too: one token in ten of the case above
+//   experts ranked by logits (without a bias their order is the scores'): the expert's
+//     number from behind, so that keys of a token differ and of equal logits the first
+//     expert's is larger. Exact for 16-bit logits, which have zeros there, and for
+//     float32 ones that differ above these bits.
+//   experts ranked by scores and a bias: the lane's item from behind; the lane is the one
+//     that has the key. Two keys next to each other in the order have to be further apart
+//     than their errors: relative to the score 2^-20 (sigmoid: 2^-21 and half a step) or
+//     2^-17 (softmax: the largest logit taken off first, half a step of a number below 128
+//     where the score is not 0 to float32, 2^-18; the sum, whose additions one after the
+//     other are PER + 6 at most), half a step more for the bias, and relative to the key
+//     2^-19 for the lowest bits.
+//   groups: the group's number from behind in the lowest 6 bits, 2^-17 of the rank.
+// (Experts' numbers in the lowest bits of biased keys too: one token in ten of the case above
 // was too close, 54 us for the choices alone.)
 template <class Row, int LANES, int PER, bool GROUPS>
 __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   if (t0 >= p.T) return;
   const int64_t mine = t0 + lane / LANES, t = mine < p.T ? mine : p.T - 1;  // (the last token again past it)
   const bool soft = p.score == GEMM_SCORE_SOFTMAX;
-  const bool scored = p.bias || (GROUPS && p.group_top > 1);
+  const bool scored = p.bias != nullptr, ranked = GROUPS && (scored || p.group_top > 1);  // by scores: experts, groups
   // The group that this lane holds a part of.
   const int lanes = GROUPS ? 1 << p.lanes : LANES, group = GROUPS ? li >> p.lanes : 0;
   const int in = GROUPS ? li & (lanes - 1) : li;
@@ -329,28 +340,26 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   float top = -inf, sum = 0.0f, bmax = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) odd |= soft ? !(l[i] < inf) : l[i] != l[i];
-  if (soft && (scored || !p.renorm)) {
+  float s[PER];  // scores, where they rank
+  if (soft && (scored || ranked || !p.renorm)) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) top = l[i] > top ? l[i] : top;
     top = gate_value32(gate_max32<LANES>(gate_order32(top)));
     const float base = top == -inf ? 0.0f : top;
-    float s[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      s[i] = expf(l[i] - base);
+      s[i] = l[i] == -inf ? 0.0f : gate_exp(l[i] - base);
       sum += s[i];
     }
     sum = gate_sum32<LANES>(sum);
-    if (scored) {
+    if (scored || ranked) {
       const float inv = 1.0f / sum;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) s[i] = l[i] == -inf ? -inf : s[i] * inv;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) l[i] = s[i];
+      for (int i = 0; i < PER; ++i) s[i] = s[i] * inv;
     }
-  } else if (scored) {
+  } else if (scored || ranked) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = l[i] == -inf ? -inf : 1.0f / (1.0f + expf(-l[i]));
+    for (int i = 0; i < PER; ++i) s[i] = gate_sigmoid(l[i]);
   }
   if (p.bias) {
     float b[PER];
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     for (int i = 0; i < PER; ++i) {
       const bool masked = l[i] == -inf || b[i] == -inf;
       odd |= !masked && !(__builtin_fabsf(b[i]) < inf);
-      l[i] = masked ? -inf : l[i] + b[i];
+      l[i] = masked ? -inf : s[i] + b[i];
       bmax = !masked && __builtin_fabsf(b[i]) > bmax ? __builtin_fabsf(b[i]) : bmax;
     }
     bmax = gate_value32(gate_max32<LANES>(gate_order32(bmax)));
@@ -367,23 +376,24 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
 #pragma unroll
   for (int i = 0; i < PER; ++i)  // (+ 0: -0 is no other number)
     key[i] = l[i] == -inf ? 0u : (gate_order32(l[i] + 0.0f) & ~low) | (low - (scored ? i : first + gate_item(i, lanes, in)));
-  // Whether one key (or sum of keys) may not be above the next.
-  auto unsure = [&](unsigned a, unsigned b, unsigned rest, float share, float bias) {
-    if (!scored) return sizeof(GateElem<Row>) == 4 && ((a ^ b) & ~rest) == 0;
-    const float u = gate_value32(a & ~rest), v = gate_value32(b & ~rest);
-    return u - v <= share * (__builtin_fabsf(u) + __builtin_fabsf(v) + 2.0f * bias) + 1e-30f;
+  // Whether two keys, or two ranks, a above b, are too close for their errors.
+  const float err = soft ? 0x1p-17f : 0x1p-20f;
+  auto unsure = [&](unsigned a, unsigned b, unsigned rest, float cut, float bias) {
+    const float u = gate_value32(a & ~rest), v = gate_value32(b & ~rest), size = __builtin_fabsf(u) + __builtin_fabsf(v);
+    return u - v <= cut * size + err * (size + 2.0f * bias) + 1e-30f;
   };
-  const float share = soft ? 0x1p-16f : 0x1.8p-19f;  // (of both keys: 2^-17 or 2^-21, 2^-24 and 2^-19)
+  auto same = [&](unsigned a, unsigned b) { return sizeof(GateElem<Row>) == 4 && ((a ^ b) & ~low) == 0; };
   if constexpr (GROUPS) {
-    // The group's two largest keys, in each of its lanes.
+    // The two largest keys (by logits and two of them: scores) of the group, in each of its lanes.
     unsigned a = 0, b = 0;
     auto enter = [&](unsigned k) {
       const unsigned least = k < a ? k : a;
       a = k > a ? k : a;
       b = least > b ? least : b;
     };
+    const bool scores = ranked && !scored;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) enter(key[i]);
+    for (int i = 0; i < PER; ++i) enter(scores ? (key[i] ? gate_order32(s[i]) : 0u) : key[i]);
     auto join = [&](unsigned oa, unsigned ob) {
       enter(oa);
       enter(ob);
@@ -393,9 +403,10 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     if (p.lanes > 2) join(gate_swap<0x141>(a), gate_swap<0x141>(b));
     if (p.lanes > 3) join(gate_swap<0x140>(a), gate_swap<0x140>(b));
     if (p.lanes > 4) join(__shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
-    if (scored && a) {  // the lowest bits: the group's number from behind
-      float r = gate_value32(a & ~low);
-      if (p.group_top > 1 && b) r += gate_value32(b & ~low);
+    if (ranked && a) {  // the lowest bits: the group's number from behind
+      const unsigned rest = scores ? 0u : low;
+      float r = gate_value32(a & ~rest);
+      if (p.group_top > 1 && b) r += gate_value32(b & ~rest);
       a = (gate_order32(r + 0.0f) & ~63u) | (63u - group);
     }
     // The best groups' ranks, down to the last one that is kept, and the next.
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
       rank = rank < m ? rank : 0;
     }
     const unsigned next = gate_max32<LANES>(rank);
-    close = next && unsure(last, next, scored ? 63u : low, share + 0x1p-16f, 2.0f * bmax);
+    close = next && (ranked ? unsure(last, next, 63u, 0x1p-17f, 2.0f * bmax) : same(last, next));
     if (own < last) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) key[i] = 0;
@@ -426,7 +437,7 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     m += taken;
     m = j > 0 && m >= taken ? 0 : m;
     const unsigned best = gate_max32<LANES>(m);
-    if (j > 0) close |= best && unsure(taken, best, low, share, bmax);
+    if (j > 0) close |= best && (scored ? unsure(taken, best, low, 0x1p-19f, bmax) : same(taken, best));
     int expert = low - (best & low);
     if (scored) {
       const uint64_t having = __ballot(m == best) >> (lane - li) & all;
@@ -442,12 +453,12 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   const float z = chosen ? gate_load(Row{}, p.L, t * p.ldl + id) : -inf;
   float out = 0.0f;
   if (!soft) {
-    out = 1.0f / (1.0f + expf(-z));
+    out = gate_sigmoid(z);
   } else if (p.renorm) {
     const float best = gate_value32(gate_max32<LANES>(chosen ? gate_order32(z) : 0u));
-    out = expf(z - best);
+    out = gate_exp(z - best);
   } else {
-    out = expf(z - top) / sum;
+    out = gate_exp(z - top) / sum;
   }
   out = chosen ? out : 0.0f;
   if (p.renorm) {

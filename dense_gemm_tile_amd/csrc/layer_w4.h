@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_split_kernel(const W4Args
   if ((int)blockIdx.x >= total) return;  // by rows the grid is an upper bound
   int g;
   LayerTile q = w4_tile<MODE, BM, Sum::BN>(p.a, blockIdx.x, total, lane, g);
+  if (q.M <= q.m0) return;               // (uniform) no rows, as offsets that decrease can make a tile
   if (q.M > q.m0 + BM) q.M = q.m0 + BM;  // this tile's rows
   const int r16 = lane & 15, oct = lane >> 4;
 
