@@ -30,9 +30,15 @@ struct W4Args {
 // slices of 8 waves.
 constexpr int kW4MaxRuns = 1536;
 
+// The tile that a call took.
+struct W4Form {
+  int waves, rows, columns;
+  bool whole;
+};
+
 // The launches, a file for each type.
-hipError_t launch_w4_f16(const W4Args& p, hipStream_t s);
-hipError_t launch_w4_bf16(const W4Args& p, hipStream_t s);
+hipError_t launch_w4_f16(const W4Args& p, hipStream_t s, W4Form& form);
+hipError_t launch_w4_bf16(const W4Args& p, hipStream_t s, W4Form& form);
 
 namespace {
 
@@ -403,7 +409,8 @@ struct W4Split {
     if (AL * NT >= 32 && p.group % 128) return false;  // (with smaller groups such a tile spills)
     return (w4_lds<AL, NT, KW>() + scales(p)) * count <= 160 * 1024;
   }
-  static hipError_t launch(W4Args p, hipStream_t s) {
+  static hipError_t launch(W4Args p, hipStream_t s, W4Form& form) {
+    form = {KW, 8 * AL, 16 * NT, WHOLE};
     const dim3 grid(w4_grid(p.a, 8 * AL, 16 * NT)), block(KW * 64);
     auto go = [&](auto grp) {
       constexpr int GRP = decltype(grp)::value;
@@ -427,10 +434,10 @@ bool w4_whole(const W4Args& p) {
 // The first of the forms that fits. (The last, of 16 x 16 tiles, holds the scales of kW4MaxRuns
 // groups.)
 template <class Form, class... Forms>
-hipError_t w4_first(const W4Args& p, hipStream_t s) {
+hipError_t w4_first(const W4Args& p, hipStream_t s, W4Form& form) {
   if constexpr (sizeof...(Forms) > 0)
-    if (!Form::fits(p)) return w4_first<Forms...>(p, s);
-  return Form::launch(p, s);
+    if (!Form::fits(p)) return w4_first<Forms...>(p, s, form);
+  return Form::launch(p, s, form);
 }
 // Tiles, measured (us; f16, waves x rows x columns):
 //   1x4096x4096    8x8x16 6.0, 16x8x16 6.3, 4x8x16 7.2
@@ -445,42 +452,42 @@ hipError_t w4_first(const W4Args& p, hipStream_t s) {
 //   512x4096x4104  4x32x64 48, 4x32x32 56, 7x64x32 77, 8x32x32 84
 //   48x4096x4104   8x32x32 13.2, 8x48x32 16.0, 8x32x16 21.5
 template <class Tag, int MODE>
-hipError_t launch_rows(const W4Args& p, hipStream_t s) {
+hipError_t launch_rows(const W4Args& p, hipStream_t s, W4Form& form) {
   const LayerArgs& a = p.a;
   // Rows of a group, on average.
   const int64_t rows = MODE == LAYER_ROWS ? ((int64_t)a.M + a.G - 1) / a.G : a.M;
   if (!w4_whole(p)) {
     using R16 = W4Split<Tag, MODE, 2, 1, 8, false>;
-    if (rows <= 16) return R16::launch(p, s);
+    if (rows <= 16) return R16::launch(p, s, form);
     // (Twice the columns, 4x32x64, take 48 us instead of 56, but spill with groups of 32.)
     if (((int64_t)a.M + 31) / 32 * (((int64_t)a.N + 31) / 32) >= 1024)
-      return w4_first<W4Split<Tag, MODE, 4, 2, 4, false>, R16>(p, s);
-    if (a.K >= 2048) return w4_first<W4Split<Tag, MODE, 4, 2, 8, false>, R16>(p, s);
-    return w4_first<W4Split<Tag, MODE, 2, 2, 4, false>, R16>(p, s);
+      return w4_first<W4Split<Tag, MODE, 4, 2, 4, false>, R16>(p, s, form);
+    if (a.K >= 2048) return w4_first<W4Split<Tag, MODE, 4, 2, 8, false>, R16>(p, s, form);
+    return w4_first<W4Split<Tag, MODE, 2, 2, 4, false>, R16>(p, s, form);
   }
   using Last = W4Split<Tag, MODE, 2, 1, 8>;
   if constexpr (MODE == LAYER_ROWS) {
     using Wide8 = W4Split<Tag, MODE, 1, 4, 4>;
-    if (rows <= 8 && Wide8::fits(p, 3)) return Wide8::launch(p, s);
-    if (rows <= 8) return w4_first<W4Split<Tag, MODE, 1, 2, 4>, Last>(p, s);
-    if (rows <= 16) return w4_first<W4Split<Tag, MODE, 2, 2, 4>, Last>(p, s);
-    return w4_first<W4Split<Tag, MODE, 4, 4, 4>, Last>(p, s);
+    if (rows <= 8 && Wide8::fits(p, 3)) return Wide8::launch(p, s, form);
+    if (rows <= 8) return w4_first<W4Split<Tag, MODE, 1, 2, 4>, Last>(p, s, form);
+    if (rows <= 16) return w4_first<W4Split<Tag, MODE, 2, 2, 4>, Last>(p, s, form);
+    return w4_first<W4Split<Tag, MODE, 4, 4, 4>, Last>(p, s, form);
   } else {
-    if (rows <= 8 && a.N <= 16 * 256) return w4_first<W4Split<Tag, MODE, 1, 1, 8>, Last>(p, s);
-    if (rows <= 8) return w4_first<W4Split<Tag, MODE, 1, 2, 8>, Last>(p, s);
-    if (rows <= 16) return w4_first<W4Split<Tag, MODE, 2, 2, 8>, Last>(p, s);
+    if (rows <= 8 && a.N <= 16 * 256) return w4_first<W4Split<Tag, MODE, 1, 1, 8>, Last>(p, s, form);
+    if (rows <= 8) return w4_first<W4Split<Tag, MODE, 1, 2, 8>, Last>(p, s, form);
+    if (rows <= 16) return w4_first<W4Split<Tag, MODE, 2, 2, 8>, Last>(p, s, form);
     using Slim32 = W4Split<Tag, MODE, 4, 2, 8>;
-    if (rows <= 32) return w4_first<Slim32, Last>(p, s);
+    if (rows <= 32) return w4_first<Slim32, Last>(p, s, form);
     using Wide64 = W4Split<Tag, MODE, 8, 4, 6>;
-    if (((int64_t)a.M + 63) / 64 * (((int64_t)a.N + 63) / 64) >= 256 && Wide64::fits(p)) return Wide64::launch(p, s);
-    if (rows <= 48) return w4_first<W4Split<Tag, MODE, 6, 2, 8>, Slim32, Last>(p, s);
-    return w4_first<W4Split<Tag, MODE, 8, 2, 7>, Slim32, Last>(p, s);
+    if (((int64_t)a.M + 63) / 64 * (((int64_t)a.N + 63) / 64) >= 256 && Wide64::fits(p)) return Wide64::launch(p, s, form);
+    if (rows <= 48) return w4_first<W4Split<Tag, MODE, 6, 2, 8>, Slim32, Last>(p, s, form);
+    return w4_first<W4Split<Tag, MODE, 8, 2, 7>, Slim32, Last>(p, s, form);
   }
 }
 
 template <class Tag>
-hipError_t launch_modes(const W4Args& p, hipStream_t s) {
-  return p.a.mode == LAYER_ROWS ? launch_rows<Tag, LAYER_ROWS>(p, s) : launch_rows<Tag, LAYER_DENSE>(p, s);
+hipError_t launch_modes(const W4Args& p, hipStream_t s, W4Form& form) {
+  return p.a.mode == LAYER_ROWS ? launch_rows<Tag, LAYER_ROWS>(p, s, form) : launch_rows<Tag, LAYER_DENSE>(p, s, form);
 }
 
 }  // namespace

@@ -6,6 +6,16 @@ namespace dgt {
 
 namespace {
 
+thread_local struct {
+  bool dense;
+  W4Form form;
+} g_w4_path;
+void write_w4_path(std::string& to) {
+  const W4Form& f = g_w4_path.form;
+  to = std::string(g_w4_path.dense ? "linear_w4" : "grouped_w4") + " mfma w" + std::to_string(f.waves) + " t" +
+       std::to_string(f.rows) + "x" + std::to_string(f.columns) + (f.whole ? "" : " through registers");
+}
+
 // Both entry points (G < 0: dense).
 int run_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t* offsets, const void* A, int64_t lda,
            const void* B, int64_t ldb, int64_t stride_b, const void* scales, const void* zeros, int64_t lds,
@@ -83,9 +93,11 @@ int run_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t*
   p.lds = lds;
   p.stride_s = stride_s;
   p.group = (int)(group < kMaxDim ? group : kMaxDim / 32 * 32);
-  set_path(dense ? "linear_w4" : "grouped_w4");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return launched(dtype == GEMM_DTYPE_F16 ? launch_w4_f16(p, s) : launch_w4_bf16(p, s));
+  W4Form& form = g_w4_path.form;
+  g_w4_path.dense = dense;
+  set_path_writer(write_w4_path);
+  return launched(dtype == GEMM_DTYPE_F16 ? launch_w4_f16(p, s, form) : launch_w4_bf16(p, s, form));
 }
 
 }  // namespace

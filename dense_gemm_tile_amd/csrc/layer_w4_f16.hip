@@ -3,6 +3,8 @@
 
 namespace dgt {
 
-hipError_t launch_w4_f16(const W4Args& p, hipStream_t s) { return launch_modes<TagF16>(p, s); }
+hipError_t launch_w4_f16(const W4Args& p, hipStream_t s, W4Form& form) {
+  return launch_modes<TagF16>(p, s, form);
+}
 
 }  // namespace dgt

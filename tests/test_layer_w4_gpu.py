@@ -87,6 +87,36 @@ def test_linear_w4_row_ends_starts_and_pitches():
         linear(gen, 70, 20, 127 + i, 128, "bf16", pad=1, wpad=i % 3, residual=True, inplace=i % 2 == 0)
 
 
+@pytest.mark.parametrize("M,N,K,group,zeros,pad,path", [
+    (1, 4096, 512, 128, True, 0, "w8 t8x16"), (8, 4112, 384, 64, False, 0, "w8 t8x32"), (9, 4112, 160, 32, True, 0, "w8 t16x32"),
+    (31, 500, 2048, 32, True, 0, "w8 t32x32"), (47, 260, 1184, 64, True, 0, "w8 t48x32"), (64, 72, 1024, 96, True, 0, "w7 t64x32"),
+    (130, 200, 640, 32, False, 0, "w7 t64x32"), (520, 1900, 384, 128, True, 0, "w6 t64x64"), (520, 1900, 256, 64, True, 0, "w7 t64x32"),
+    (40, 64, 45056, 32, True, 0, "w8 t16x16"), (13, 300, 1000, 64, True, 1, "w8 t16x16 through registers"),
+    (60, 200, 2100, 128, True, 1, "w8 t32x32 through registers"), (50, 130, 333, 96, False, 3, "w4 t16x32 through registers"),
+    (1060, 1000, 200, 32, True, 1, "w4 t32x32 through registers"), (30, 50, 45057, 32, True, 0, "w8 t16x16 through registers")])
+def test_every_tile(M, N, K, group, zeros, pad, path):
+    need_gpu()
+    import dense_gemm_tile_amd as dgt
+    gen = torch.Generator().manual_seed(M + N)
+    for dtype in ("bf16", "f16"):
+        linear(gen, M, N, K, group, dtype, zeros=zeros, act="silu", bias=True, residual=True, out_dtype="f32", pad=pad)
+        assert dgt.gemm_last_path().endswith(path), dgt.gemm_last_path()
+
+
+@pytest.mark.parametrize("sizes,N,K,group,zeros,path", [
+    ([2, 0, 8, 5], 130, 1024, 128, False, "w4 t8x64"), ([2, 0, 8, 5], 130, 4096, 32, True, "w4 t8x32"),
+    ([20, 0, 13], 130, 640, 64, True, "w4 t16x32"), ([50, 1, 70], 130, 640, 96, True, "w4 t32x64"),
+    ([5, 0, 3], 40, 45056, 32, True, "w8 t16x16"), ([5, 0, 19], 40, 77, 32, True, "w8 t16x16 through registers"),
+    ([60, 0, 30], 40, 2100, 128, False, "w8 t32x32 through registers"), ([60, 0, 30], 40, 90, 32, True, "w4 t16x32 through registers")])
+def test_every_grouped_tile(sizes, N, K, group, zeros, path):
+    need_gpu()
+    import dense_gemm_tile_amd as dgt
+    gen = torch.Generator().manual_seed(N + K)
+    for dtype in ("bf16", "f16"):
+        grouped(gen, sizes, N, K, group, dtype, zeros=zeros, act="gelu", bias=True, residual=True, spare=2)
+        assert dgt.gemm_last_path().endswith(path), dgt.gemm_last_path()
+
+
 def test_linear_w4_without_a_sum_and_every_code():
     need_gpu()
     import dense_gemm_tile_amd as dgt
@@ -146,19 +176,20 @@ def test_grouped_w4(sizes, dtype):
     grouped(gen, sizes, 16, 512, 128, dtype, zeros=True, out_dtype="f32", spare=1, shared=True)
 
 
-def test_offsets_of_another_program():
+@pytest.mark.parametrize("K", [64, 40, 2100])
+def test_offsets_of_another_program(K):
     """Offsets that decrease or pass the rows stay inside the buffers: rows past M are not there, and
     what lies around Y keeps its values."""
     need_gpu()
     import dense_gemm_tile_amd as dgt
     gen = torch.Generator().manual_seed(9)
-    M, N, K = 20, 40, 64
+    M, N, runs = 20, 40, -(-K // 32)
     x = randn(gen, M, K, dtype="bf16")
     codes, s, _, _, _ = weights(gen, (4, N), K, 32, False, "bf16")
     for off in ([0, 30, 10, 50, 20], [5, -7, 100, 3, 2 ** 31 - 1], [0, 0, 0, 0, 10 ** 6]):
         wide = out(M + 8, N, dtype="bf16")
         dgt.gemm_grouped_w4(4, M, N, K, "bf16", torch.tensor(off, dtype=torch.int32, device=DEV), x, K, codes, K, N * K, s,
-                            None, 2, N * 2, 32, None, "none", None, 0, wide[4:], N, "bf16",
+                            None, runs, N * runs, 32, None, "none", None, 0, wide[4:], N, "bf16",
                             stream=torch.cuda.current_stream())
         torch.cuda.synchronize()
         assert torch.isnan(wide[:4]).all() and torch.isnan(wide[-4:]).all()
