@@ -13,7 +13,7 @@
 namespace dgt {
 
 enum LayerMode : int { LAYER_DENSE = 0, LAYER_ROWS = 1, LAYER_SUM = 2 };
-enum LayerAct : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_ERF = 3, ACT_SILU = 4 };
+enum LayerAct : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_ERF = 3, ACT_SILU = 4, ACT_SCALE = 5 };
 
 struct LayerArgs {
   const void* A;
@@ -23,6 +23,7 @@ struct LayerArgs {
   void* Y;
   void* Z;           // null: not kept
   const int* offsets;
+  const float* scale;  // ACT_SCALE, of products that are a step of another operator: z *scale
   int64_t lda, ldb, ldr, ldy, ldz;  // elements
   int64_t stride_b;  // by rows: elements from one group's B to the next
   int64_t stride_y;  // by sum: elements from one group's Y (and R) to the next
@@ -325,12 +326,17 @@ __device__ __forceinline__ void layer_act8_of(float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = layer_act<ACT>(f[e]);
 }
-__device__ __forceinline__ void layer_act8(float (&f)[8], int act) {
-  switch (act) {  // uniform over the launch
+__device__ __forceinline__ void layer_scale8(float (&f)[8], float by) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= by;
+}
+__device__ __forceinline__ void layer_act8(float (&f)[8], const LayerArgs& p) {
+  switch (p.act) {  // uniform over the launch
     case ACT_RELU: layer_act8_of<ACT_RELU>(f); break;
     case ACT_GELU: layer_act8_of<ACT_GELU>(f); break;
     case ACT_GELU_ERF: layer_act8_of<ACT_GELU_ERF>(f); break;
     case ACT_SILU: layer_act8_of<ACT_SILU>(f); break;
+    case ACT_SCALE: layer_scale8(f, *p.scale); break;
     default: break;
   }
 }
@@ -408,7 +414,7 @@ __device__ __forceinline__ void layer_finish8(const LayerArgs& p, const LayerTil
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] += bias[e];
   if (q.Z) layer_store8_16<Tag>(q.Z + ((int64_t)r * p.ldz + c) * 2, nv, x);
-  layer_act8(x, p.act);
+  layer_act8(x, p);
   if (q.R) {
     float rv[8];
     if (p.out32) layer_load8_32(q.R + ((int64_t)r * p.ldr + c) * 4, nv, rv);
@@ -502,7 +508,8 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
       for (int e = 0; e < 8; ++e) x[e] += bias[e];
       if (row < q.M && c < q.N) {
         if (q.Z) *reinterpret_cast<u32x4_at2*>(z) = layer_pack8<Tag>(x);
-        layer_act8_of<ACT>(x);
+        if constexpr (ACT == ACT_SCALE) layer_scale8(x, *p.scale);
+        else layer_act8_of<ACT>(x);
         if (q.R) {
           float f[8];
           if (p.out32) {
@@ -563,6 +570,7 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
         case ACT_GELU: layer_passes<E, Tag, ACT_GELU>(p, q, r + rl, c, from, bias, res); break;
         case ACT_GELU_ERF: layer_passes<E, Tag, ACT_GELU_ERF>(p, q, r + rl, c, from, bias, res); break;
         case ACT_SILU: layer_passes<E, Tag, ACT_SILU>(p, q, r + rl, c, from, bias, res); break;
+        case ACT_SCALE: layer_passes<E, Tag, ACT_SCALE>(p, q, r + rl, c, from, bias, res); break;
         default: layer_passes<E, Tag, ACT_NONE>(p, q, r + rl, c, from, bias, res); break;
       }
     } else {

@@ -145,7 +145,8 @@ int choose_grouped(const LayerPlan& pl) {
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
-int choose_kernel(const LayerPlan& pl) {
+// own: a product that is a step of another operator.
+int choose_kernel(const LayerPlan& pl, bool own) {
   const LayerArgs& a = pl.a;
   auto tiles = [&](int k) { return count_tiles(a, kLayerKernels[k]); };
   if (!kernel_runs(pl, LK_PP256)) {
@@ -193,6 +194,16 @@ int choose_kernel(const LayerPlan& pl) {
   const bool split = kernel_runs(pl, LK_SKINNY64N64);
   // Few rows: the weights' bytes count.
   if (split && !pl.ta && a.M <= 64) {
+    // Many columns, one tile of 64 to a CU or more (us, bf16, float32 out, K of 2048; of
+    // 1024 and 4096 the same way):
+    //                     16384   32001   65536   128000 columns
+    //   61 rows, s64x32    21.4    41.6    78.4    152
+    //            s64x64    17.1    32.9    64.6    131
+    //   24 rows, s32x32    16.7    32.4    62.5    121
+    //            s64x64    15.5    30.3    58.4    115
+    // and at 8192, 128 tiles, s64x32 9.3, s64x64 11.1. (gemm_linear's own calls keep the
+    // order of their sums.)
+    if (own && a.M > 16 && tiles(LK_SKINNY64N64) >= 256) return LK_SKINNY64N64;
     // (16 columns of B stored [K][N] would be a quarter of a line.)
     if (a.M <= 16) return pl.tb && a.N <= 16 * 256 ? LK_SKINNY16N16 : LK_SKINNY16;
     if (a.M <= 32 || tiles(LK_SKINNY32) <= 256) return LK_SKINNY32;
@@ -212,10 +223,10 @@ int choose_kernel(const LayerPlan& pl) {
   return tiles(LK_PP128) > 256 ? LK_PP128 : LK_PP128_DEEP;
 }
 
-// forced: GEMM_LAYER_TILE counts.
+// forced: GEMM_LAYER_TILE counts; without it the product is a step of another operator.
 int plan_tiles(LayerPlan& pl, const char* op, bool forced = true) {
   LayerArgs& a = pl.a;
-  pl.kernel = choose_kernel(pl);
+  pl.kernel = choose_kernel(pl, !forced);
   if (const char* want = forced ? forced_layer_tile() : nullptr) {
     int found = -1;
     for (int k = 0; k < NUM_LAYER_KERNELS; ++k)
@@ -457,12 +468,19 @@ int check_span(int64_t blocks) {
 
 }  // namespace
 
+static void scale_product(LayerPlan& pl, const float* scale) {
+  if (!scale) return;
+  pl.a.act = ACT_SCALE;
+  pl.a.scale = scale;
+}
+
 int run_dense(const DenseCall& c, bool launch, hipStream_t s) {
   LayerPlan pl;
   bool noop;
   CHECK(plan_product(-1, c.M, c.N, c.K, c.dtype, c.ta, c.tb, nullptr, c.A, c.lda, c.B, c.ldb, 0,
                      nullptr, GEMM_ACT_NONE, c.R, c.ldr, c.Y, c.ldy, c.out_dtype, nullptr, 0, pl, noop,
                      false));
+  scale_product(pl, c.scale);
   return noop || !launch ? GEMM_OK : launched(launch_product(pl, s));
 }
 
@@ -471,6 +489,7 @@ int run_sums(const SumsCall& c, bool launch, hipStream_t s) {
   bool noop;
   CHECK(plan_grad_weight(c.G, c.M, c.N, c.K, c.dtype, c.offsets, c.A, c.lda, c.B, c.ldb, c.D, c.ldd, c.stride_d,
                          c.out_dtype, c.accumulate, pl, noop, false));
+  scale_product(pl, c.scale);
   return noop || !launch ? GEMM_OK : launched(launch_product(pl, s));
 }
 

@@ -154,6 +154,7 @@ struct DenseCall {
   void* Y;
   int64_t ldy;
   int out_dtype;
+  const float* scale;  // a factor of the product on the GPU; null: none
 };
 int run_dense(const DenseCall& c, bool launch, hipStream_t s);
 
@@ -170,6 +171,7 @@ struct SumsCall {
   int64_t ldd, stride_d;
   int out_dtype;
   bool accumulate;
+  const float* scale;  // as above
 };
 int run_sums(const SumsCall& c, bool launch, hipStream_t s);
 

@@ -22,6 +22,7 @@ struct LossTileArgs {
   // Gradient.
   const float* lse;
   const float* dloss;
+  const float* scale;  // dloss is taken relative to it
   void* G;             // n x T8 of the operands' type
   int T8;              // T as a multiple of 8, G's pitch; 0 in the columns from T on
 };

@@ -14,6 +14,12 @@
 //        in float32
 // X is copied to T8 rows where T is not a multiple of 8.
 //
+// The matrix cores take G in 16 bits. It is held relative to the largest |dloss| (scale:
+// 2^-15 of it), which its products multiply back in float32: f16 has room for probabilities
+// down to 2^-39 beside 1 whatever dloss is, and where all tokens weigh the same, as in a mean,
+// dloss is not rounded at all, nor, nearly, is the label's element of a token far from its
+// label, the row's largest.
+//
 // The logits come from layer_loss_pp256.hip, which turns them into parts or G in
 // registers. Fewer tokens, and operands not in whole 16-byte pieces, take a product of
 // gemm_linear in float32 and a kernel over its rows instead.
@@ -54,6 +60,7 @@ struct LossGradArgs {
   const int* labels;
   const float* lse;
   const float* dloss;
+  const float* scale;
   void* G;              // n x T8
   int64_t ldl;
   int T, T8, V, v0, n;
@@ -127,8 +134,17 @@ __global__ void __launch_bounds__(64 * kJoinWaves) layer_loss_join_kernel(const 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t t = (int64_t)layer_block(p) * 64 + lane;
   float2 a{-__builtin_inff(), 0.0f};
-  if (t < p.T)
-    for (int64_t q = w; q < p.Q; q += kJoinWaves) a = loss_join(a, p.parts[q * p.T + t]);
+  if (t < p.T) {
+    constexpr int AHEAD = 8;  // parts in flight together
+    for (int64_t q = w; q < p.Q; q += AHEAD * kJoinWaves) {
+      float2 v[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        v[u] = q + u * kJoinWaves < p.Q ? p.parts[(q + u * kJoinWaves) * p.T + t] : float2{-__builtin_inff(), 0.0f};
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) a = loss_join(a, v[u]);
+    }
+  }
   part[w][lane] = a;
   __syncthreads();
   if (w || t >= p.T) return;
@@ -152,7 +168,7 @@ __global__ void __launch_bounds__(256) layer_loss_grad_kernel(const LossGradArgs
     const int t = t0 + i, c = e0 + lane, label = t < p.T ? p.labels[t] : -1;
     float g = 0.0f;
     if ((unsigned)label < (unsigned)p.V && c < p.n)
-      g = p.dloss[t] * (loss_exp(p.L[t * p.ldl + c] - p.lse[t]) - (p.v0 + c == label ? 1.0f : 0.0f));
+      g = p.dloss[t] / *p.scale * (loss_exp(p.L[t * p.ldl + c] - p.lse[t]) - (p.v0 + c == label ? 1.0f : 0.0f));
     x[lane][i] = layer_16(Tag{}, g);
   }
   __syncthreads();
@@ -177,22 +193,48 @@ __global__ void __launch_bounds__(256) layer_loss_pad_kernel(const LossPadArgs p
     p.to[i] = i < p.live ? p.X[t * p.ldx + (i - t * p.H)] : (unsigned short)0;
   }
 }
-// Offsets that cut n rows into S parts, for the pieces of n and for the last one.
-__global__ void __launch_bounds__(256) layer_loss_offsets_kernel(int* to, int S, int n, int last) {
-  for (int i = threadIdx.x; i <= S; i += 256) {
-    to[i] = (int)((int64_t)n * i / S);
-    to[S + 1 + i] = (int)((int64_t)last * i / S);
+// What a gradient's other kernels read: the scale of G, 2^-15 of the largest finite |dloss| of a
+// token that has a label, and offsets that cut n rows into S parts, for the pieces of n and for
+// the last one.
+struct LossStartArgs {
+  const int* labels;
+  const float* dloss;
+  float* scale;
+  int* offsets;
+  int T, V, S, n, last;
+};
+__global__ void __launch_bounds__(1024) layer_loss_start_kernel(const LossStartArgs p) {
+  __shared__ float part[16];
+  for (int i = threadIdx.x; i <= p.S; i += 1024) {
+    p.offsets[i] = (int)((int64_t)p.n * i / p.S);
+    p.offsets[p.S + 1 + i] = (int)((int64_t)p.last * i / p.S);
   }
+  float m = 0.0f;
+#pragma unroll 8
+  for (int64_t t = threadIdx.x; t < p.T; t += 1024) {
+    const float d = __builtin_fabsf(p.dloss[t]);
+    if ((unsigned)p.labels[t] < (unsigned)p.V && d < __builtin_inff()) m = __builtin_fmaxf(m, d);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d, 64));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < 16; ++w) m = __builtin_fmaxf(m, part[w]);
+  m *= 0x1p-15f;
+  *p.scale = m > 0.0f ? m : 1.0f;
 }
 // dX from S float32 parts of T8 x H.
 struct LossRoundArgs {
   const float* from;
+  const float* scale;
   unsigned short* to;
   int64_t ld, n, stride;
   int H, S;
 };
 template <class Tag>
 __global__ void __launch_bounds__(256) layer_loss_round_kernel(const LossRoundArgs p) {
+  const float scale = *p.scale;
   for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < p.n; i += 4 * (int64_t)gridDim.x * 256) {
     f32x4 s = *reinterpret_cast<const f32x4*>(p.from + i);  // (parts are whole fours: T8 is a multiple of 8)
     for (int u = 1; u < p.S; ++u) {
@@ -202,7 +244,7 @@ __global__ void __launch_bounds__(256) layer_loss_round_kernel(const LossRoundAr
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t t = (i + e) / p.H;
-      if (i + e < p.n) p.to[t * p.ld + (i + e - t * p.H)] = layer_16(Tag{}, s[e]);
+      if (i + e < p.n) p.to[t * p.ld + (i + e - t * p.H)] = layer_16(Tag{}, s[e] * scale);
     }
   }
 }
@@ -217,7 +259,7 @@ struct LossPlan {
   int S;                   // parts of dX's sum
   bool direct;             // dX needs no float32 sums
   int64_t parts, target, logits, forward;      // forward: all bytes of gemm_loss
-  int64_t glogits, g, xpad, sums, offsets, grad;  // grad: all bytes of gemm_loss_grad
+  int64_t glogits, g, xpad, sums, offsets, scale, grad;  // grad: all bytes of gemm_loss_grad
 };
 // False where the bytes pass 63 bits.
 bool loss_plan(int64_t T, int64_t V, int64_t H, LossPlan& q) {
@@ -257,6 +299,7 @@ bool loss_plan(int64_t T, int64_t V, int64_t H, LossPlan& q) {
   place(q.xpad, q.T8 == T ? 0 : (unsigned __int128)q.T8 * H * 2);
   place(q.sums, q.direct ? 0 : (unsigned __int128)q.S * q.T8 * H * 4);
   place(q.offsets, (unsigned __int128)2 * (q.S + 1) * 4);
+  place(q.scale, 4);
   if (at > max) return false;
   q.grad = (int64_t)at;
   return true;
@@ -292,7 +335,8 @@ const char* loss_row(const Mat& m, int64_t row) { return static_cast<const char*
 
 // The float32 logits of columns [v0, v0 + n).
 DenseCall loss_logits(const Mat& mx, const Mat& mw, int dtype, int64_t v0, int64_t n, void* to, int64_t ld) {
-  return {mx.rows, n, mx.cols, dtype, false, true, mx.ptr, mx.ld, loss_row(mw, v0), mw.ld, nullptr, 0, to, ld, GEMM_DTYPE_F32};
+  return {mx.rows, n, mx.cols, dtype, false, true, mx.ptr, mx.ld, loss_row(mw, v0), mw.ld, nullptr, 0, to, ld, GEMM_DTYPE_F32,
+          nullptr};
 }
 
 // Both run through a call twice: without launches, so that a refusal comes before any work, and with.
@@ -372,10 +416,12 @@ int run_grad(const LossPlan& q, const Mat& mx, const Mat& mw, const Mat& mdx, co
     if (launch) CHECK(launched(launch_kernel(layer_loss_pad_kernel, blocks((a.n + 255) / 256), dim3(256), s, a)));
   }
   int* const offsets = reinterpret_cast<int*>(ws + q.offsets);
-  const int64_t last = V - (V - 1) / q.piece * q.piece;
-  if (mdx.ptr && launch)
-    CHECK(launched(launch_kernel(layer_loss_offsets_kernel, dim3(1), dim3(256), s, offsets, q.S,
-                                 (int)(q.piece < V ? q.piece : V), (int)last)));
+  float* const scale = reinterpret_cast<float*>(ws + q.scale);
+  if (launch) {
+    const int64_t last = V - (V - 1) / q.piece * q.piece;
+    const LossStartArgs a{labels, dloss, scale, offsets, (int)T, (int)V, q.S, (int)(q.piece < V ? q.piece : V), (int)last};
+    CHECK(launched(launch_kernel(layer_loss_start_kernel, dim3(1), dim3(1024), s, a)));
+  }
   void* const G = ws + q.g;
   const bool tiles = loss_tiles(mx, mw, q.piece);
   CHECK(loss_pieces(V, q.piece, [&](int64_t v0, int64_t n) -> int {
@@ -393,6 +439,7 @@ int run_grad(const LossPlan& q, const Mat& mx, const Mat& mw, const Mat& mdx, co
       a.V = (int)V;
       a.lse = lse;
       a.dloss = dloss;
+      a.scale = scale;
       a.G = G;
       a.T8 = (int)q.T8;
       if (launch) CHECK(launched(launch_loss_tiles(dtype, true, a, s)));
@@ -405,6 +452,7 @@ int run_grad(const LossPlan& q, const Mat& mx, const Mat& mw, const Mat& mdx, co
         a.labels = labels;
         a.lse = lse;
         a.dloss = dloss;
+        a.scale = scale;
         a.G = static_cast<unsigned short*>(G) + c0 * q.T8;
         a.ldl = q.sub;
         a.T = (int)T;
@@ -422,19 +470,21 @@ int run_grad(const LossPlan& q, const Mat& mx, const Mat& mw, const Mat& mdx, co
     if (mdx.ptr) {
       const SumsCall c{q.S, n, q.T8, H, dtype, offsets + (v0 + q.piece >= V ? q.S + 1 : 0), G, q.T8, loss_row(mw, v0), mw.ld,
                        q.direct ? const_cast<void*>(mdx.ptr) : ws + q.sums, q.direct ? mdx.ld : H, q.T8 * H,
-                       q.direct ? dtype : GEMM_DTYPE_F32, v0 > 0};
+                       q.direct ? dtype : GEMM_DTYPE_F32, v0 > 0,
+                       q.direct ? scale : nullptr};
       CHECK(run_sums(c, launch, s));
     }
     if (mdw.ptr) {
       void* const to = const_cast<char*>(loss_row(mdw, v0));
-      const DenseCall c{n, H, q.T8, dtype, false, false, G, q.T8, x, ldx, accumulate ? to : nullptr, mdw.ld, to, mdw.ld, dw_dtype};
+      const DenseCall c{n, H, q.T8, dtype, false, false, G, q.T8, x, ldx, accumulate ? to : nullptr, mdw.ld, to, mdw.ld, dw_dtype,
+                        scale};
       CHECK(run_dense(c, launch, s));
     }
     return GEMM_OK;
   }));
   if (!launch) return GEMM_OK;
   if (mdx.ptr && !q.direct) {
-    const LossRoundArgs a{reinterpret_cast<const float*>(ws + q.sums), static_cast<unsigned short*>(const_cast<void*>(mdx.ptr)),
+    const LossRoundArgs a{reinterpret_cast<const float*>(ws + q.sums), scale, static_cast<unsigned short*>(const_cast<void*>(mdx.ptr)),
                           mdx.ld, T * H, q.T8 * H, (int)H, q.S};
     CHECK(launched(launch_kernel(layer_loss_round_kernel<Tag>, blocks((a.n + 1023) / 1024), dim3(256), s, a)));
   }
@@ -510,7 +560,8 @@ int gemm_loss_grad(int64_t T, int64_t V, int64_t H, int dtype, const void* X, in
     if (dX && T > 0) CHECK(check_ptr(mdx));
     if (dW) CHECK(check_ptr(mdw));
     if (T == 0) {  // no rows: zeros
-      const DenseCall c{V, H, 0, dtype, true, false, nullptr, V, nullptr, H, nullptr, 0, dW, lddw, dw_dtype};
+      const DenseCall c{V, H, 0, dtype, true, false, nullptr, V, nullptr, H, nullptr, 0, dW, lddw, dw_dtype,
+                        nullptr};
       return run_dense(c, true, s);
     }
     LossPlan q{};

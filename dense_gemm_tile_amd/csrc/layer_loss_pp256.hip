@@ -6,8 +6,8 @@
 //   forward   largest logit and sum of exponentials of a tile's 256 entries for each token:
 //             in the lane, over the lane groups, then over the two waves that share a
 //             column; and the label's logit, where the tile has it
-//   gradient  G = dloss (exp(L - lse) - [v = label]), rounded to the operands' type, which
-//             the matrix cores read next; rows through LDS so that stores are whole lines
+//   gradient  G = dloss / scale (exp(L - lse) - [v = label]), rounded to the operands' type,
+//             which the matrix cores read next; rows through LDS so that stores are whole lines
 //
 // The exponentials take most of the epilogue: 128 a lane at 16 cycles a wave.
 #include "gemm_mfma_pingpong.h"
@@ -91,13 +91,14 @@ __device__ __forceinline__ void loss_gradient(At::acc_t (&acc)[C::TM][C::TN], co
   const int m0 = tm * C::BM + wm * C::WTM, c = tn * C::BN + wn * C::WTN + cl;
   float lse[8], d[8];
   int label[8];  // -1: no gradient
+  const float scale = *p.scale;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int t = c + e;
     label[e] = t < p.T ? p.labels[t] : -1;
     if ((unsigned)label[e] >= (unsigned)p.V) label[e] = -1;
     lse[e] = label[e] >= 0 ? p.lse[t] : 0.0f;
-    d[e] = label[e] >= 0 ? p.dloss[t] : 0.0f;
+    d[e] = label[e] >= 0 ? p.dloss[t] / scale : 0.0f;
   }
 #pragma unroll
   for (int b = 0; b < C::TM / AR; ++b) {

@@ -10,7 +10,8 @@ namespace dgt {
 // n workgroups as a grid. A launch holds less than 2^32 threads along a
 // dimension (and one of more computes a part without an error), so further
 // workgroups go along z, the last of them in part past n. grid_x: workgroups of
-// one z, which the kernel gets among its arguments (layer_block()): the built-in is a hidden argument more for every launch.
+// one z, which the kernel gets among its arguments (layer_block()): the built-in
+// is a hidden argument more for every launch.
 inline dim3 layer_grid(int64_t n, unsigned threads, unsigned& grid_x, unsigned y = 1) {
   const int64_t most = ((int64_t{1} << 32) - 1) / threads;
   const int64_t z = (n + most - 1) / most;

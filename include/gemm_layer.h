@@ -251,7 +251,8 @@ GEMM_API int64_t gemm_norm_grad_workspace(int64_t M, int64_t N);
  *   weights[T * top]  scale * s[ids], renormalised if wanted
  *
  * Keys are compared as they come out in 64 bits, so that a choice does not hang
- * on a rounding. An expert whose logit or bias is -infinity is masked: it is not
+ * on a rounding; without a bias experts are compared by their logits, whose order
+ * the scores have, also where scores are equal to 64 bits. An expert whose logit or bias is -infinity is masked: it is not
  * chosen, and adds nothing to its group's rank (a group of masked experts ranks
  * last). Choices that a token has no expert left for are dropped: id -1 and
  * weight 0, which gemm_route, gemm_combine and gemm_gate_grad leave out. NaN
@@ -340,8 +341,10 @@ GEMM_API int64_t gemm_loss_workspace(int64_t T, int64_t V, int64_t H);
  * (0 for a token whose label is outside [0, V), whose dloss is not read),
  *   dX = G @ W,   dW = G^T @ X.
  * The logits are made again in pieces of the vocabulary, and G is rounded to
- * `dtype`, as the matrix cores read it, before its two products: an f16 call
- * wants a dloss that carries the training's loss scale.
+ * `dtype`, as the matrix cores read it, before its two products, relative to the
+ * largest finite |dloss| of a token that counts: dloss may be of any size (in f16
+ * a token whose |dloss| is below 2^-24 of that loses bits). dX in f16 wants a loss
+ * scale all the same, as any gradient in f16.
  *
  * dX        T x H of `dtype`, or NULL when not wanted.
  * dW        V x H of dw_dtype (`dtype` or GEMM_DTYPE_F32), or NULL when not

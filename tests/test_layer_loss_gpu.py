@@ -125,6 +125,13 @@ def test_several_pieces(T, V, H):
     both(torch.Generator().manual_seed(T), T, V, H, "bf16", dw_dtype="f32")
 
 
+@pytest.mark.parametrize("T,V,H,dtype", [(1000, 64 * 256 + 100, 1032, "f16"), (300, 33000, 1024, "bf16"), (200, 65700, 1024, "bf16")])
+def test_long_rows_on_many_tiles(T, V, H, dtype):
+    """A few tiles more than there are workgroups, dX's sum in parts, rows of more than a slice's multiple."""
+    need_gpu()
+    both(torch.Generator().manual_seed(T), T, V, H, dtype, dw_dtype="f32")
+
+
 def test_large_logits():
     """Logits of thousands: exponentials relative to the largest neither overflow nor vanish together."""
     need_gpu()
@@ -179,6 +186,79 @@ def test_gradient_is_the_slope():
                     d += k * float(f(*args)) / (2 * h)
                 # G and dX in f16: half a step of each of the V (or T) products, of sizes below 4
                 assert abs(float(got[i, j]) - d) < 4 * 10 * 2.0 ** -11, (m, i, j)
+
+
+def grad(x, w, labels, lse, dloss, dtype, dw_dtype="f32"):
+    import dense_gemm_tile_amd as dgt
+    (T, H), V = x.shape, w.shape[0]
+    dx, dw = out(T, H, dtype=dtype), out(V, H, dtype=dw_dtype)
+    size = dgt.gemm_loss_grad_workspace(T, V, H)
+    dgt.gemm_loss_grad(T, V, H, dtype, x, ld(x), w, ld(w), labels, lse, dloss, dx, ld(dx), dw, ld(dw), dw_dtype, False,
+                       workspace(size), size, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    return dx, dw
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,V,H", [(40, 500, 64), (260, 2048, 128), (300, 1000, 72)])
+def test_dloss_of_any_size(dtype, T, V, H):
+    """A factor 2^k of dloss is the same factor of the gradients, bit for bit: no size of it is rounded away
+    (probabilities of 1e-3 and a dloss of 2^-40 would not be numbers of f16, nor 2^40)."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(7)
+    x, w = randn(gen, T, H, dtype=dtype), randn(gen, V, H, dtype=dtype, scale=H ** -0.5)
+    labels = torch.randint(0, V, (T,), generator=gen).to(DEV, torch.int32)
+    labels[5] = -1
+    lse, dloss = loss(x, w, labels, dtype, V)[1], randn(gen, 1, T)[0]
+    dx, dw = grad(x, w, labels, lse, dloss, dtype)
+    check_grad(x, w, labels, lse, dloss, dtype, dx, dw, "f32")
+    for k in (-40, -10, 10, 40):
+        got = grad(x, w, labels, lse, dloss * 2.0 ** k, dtype)
+        assert torch.equal(got[1], dw * 2.0 ** k), k
+        if dtype == "bf16":
+            assert torch.equal(got[0], dx * 2.0 ** k), k
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_dloss_without_a_value(T):
+    """A token's infinite dloss, or its NaN, stays with its row of dX; zeros alone give zeros."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(8)
+    x, w = randn(gen, T, 64, dtype="f16"), randn(gen, 500, 64, dtype="f16", scale=0.125)
+    labels = torch.randint(0, 500, (T,), generator=gen).to(DEV, torch.int32)
+    lse, dloss = loss(x, w, labels, "f16", 500)[1], torch.full((T,), 0.5, device=DEV)
+    want = grad(x, w, labels, lse, dloss, "f16")[0]
+    dloss[3], dloss[8], dloss[T - 1] = float("inf"), float("nan"), -float("inf")
+    got, bad = grad(x, w, labels, lse, dloss, "f16")[0], [3, 8, T - 1]
+    assert not torch.isfinite(got[bad]).any()
+    left = torch.ones(T, dtype=torch.bool, device=DEV)
+    left[bad] = False
+    assert torch.equal(got[left], want[left])
+    for m in grad(x, w, labels, lse, 0 * want[:, 0].float(), "f16"):
+        assert torch.equal(m, torch.zeros_like(m))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_mean_of_hard_tokens(dtype):
+    """Where all tokens weigh the same and are far from their labels, G's largest elements, the labels', are not
+    rounded: dW comes out closer than G's rounding to 16 bits would let it, whatever the weight."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(9)
+    T, V, H = 320, 40000, 64
+    x, w = randn(gen, T, H, dtype=dtype), randn(gen, V, H, dtype=dtype, scale=0.02)
+    labels = torch.randperm(V, generator=gen)[:T].to(DEV, torch.int32)
+    lse, weight = loss(x, w, labels, dtype, V)[1], 0.7 / T
+    got = grad(x, w, labels, lse, torch.full((T,), weight, device=DEV), dtype)[1][labels.long()].double()
+    # Row labels[t]: weight times (p - 1) x[t], and probabilities p below 1e-4 of the other tokens: each
+    # product off by half a step at most where it is a p, the label's by the 1e-4 that may round away.
+    L = x.double() @ w.double().T
+    p = torch.exp(L - lse.double()[:, None])
+    assert float(p.max()) < 1e-4
+    G = (p[:, labels.long()] - torch.eye(T, dtype=torch.float64, device=DEV)) * weight
+    want = G.T @ x.double()
+    off = torch.linalg.norm(got - want) / torch.linalg.norm(want)
+    print(f"relative error {float(off):.2e}", flush=True)
+    assert float(off) < 1.5e-4
 
 
 def test_runs_repeat():
