@@ -261,6 +261,24 @@ def test_a_mean_of_hard_tokens(dtype):
     assert float(off) < 1.5e-4
 
 
+def test_products_inside_take_no_named_tile(monkeypatch):
+    """GEMM_LAYER_TILE names the kernel of a call's own product, not those of the loss."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(10)
+    x, w = randn(gen, 40, 64, dtype="bf16"), randn(gen, 500, 64, dtype="bf16")
+    labels = torch.randint(0, 500, (40,), generator=gen).to(DEV, torch.int32)
+    dloss = torch.ones(40, device=DEV)
+
+    def both_calls():
+        found, lse = loss(x, w, labels, "bf16", 500)
+        return (found, lse, *grad(x, w, labels, lse, dloss, "bf16"))
+    want = both_calls()
+    for name in ("pp256x256", "no such kernel"):
+        monkeypatch.setenv("GEMM_LAYER_TILE", name)
+        for a, b in zip(both_calls(), want):
+            assert torch.equal(a, b)
+
+
 def test_runs_repeat():
     need_gpu()
     gen = torch.Generator().manual_seed(6)
