@@ -8,9 +8,8 @@
 // A wave takes a token. Choices are whole numbers and must not hang on a rounding, so
 // keys count as they are in 64 bits; in 64 bits throughout, the exponentials and the
 // search take most of the time (16384 tokens, 8 of 256 experts in groups, with the
-// gradient: 68 us, 30 so). So keys are made and searched in float32, with a bound
-// of their error, and a token two of whose keys come too close for it is done again in
-// 64 bits.
+// gradient: 68 us, 24 so). So keys are made and searched in float32, with a bound
+// of their error, and what comes too close for it is decided in 64 bits.
 #include "layer.h"
 #include "layer_checks.h"
 
@@ -84,6 +83,10 @@ __device__ __forceinline__ uint64_t gate_order(double v) {
   if (v != v) return kGateNan;
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   return u >> 63 ? ~u : u | ((uint64_t)1 << 63);
+}
+
+__device__ __forceinline__ double gate_value(uint64_t k) {
+  return k == kGateNan ? __builtin_nan("") : __builtin_bit_cast(double, k >> 63 ? k & ~((uint64_t)1 << 63) : ~k);
 }
 
 // Reductions over groups of 16 or of all 64 lanes, by lane swaps; every lane gets the result.
@@ -188,10 +191,7 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
         }
       }
       if (p.group_top > 1 && b != kGateMasked) {
-        auto value = [](uint64_t k) {
-          return k == kGateNan ? __builtin_nan("") : __builtin_bit_cast(double, k >> 63 ? k & ~((uint64_t)1 << 63) : ~k);
-        };
-        a = gate_order(value(a) + value(b));
+        a = gate_order(gate_value(a) + gate_value(b));
       }
       rank[g] = a;
     }
@@ -297,6 +297,36 @@ __device__ __forceinline__ void gate_store_row(void* p, int64_t at, int lanes, i
   }
 }
 
+// A group's place among its token's by their ranks in 64 bits, for sigmoid scores: the group is
+// shared by `lanes` lanes, of which this is the in-th; items: bits of this lane's experts that
+// count; base: the token's first lane.
+template <class Row>
+__device__ __forceinline__ int gate_group_place(const GateArgs& p, int64_t t, unsigned items, int group, int in, int lanes, int base) {
+  const int first = group * (p.E / p.groups);
+  uint64_t a = kGateMasked, b = kGateMasked;  // the two largest keys
+  auto enter = [&](uint64_t k) __attribute__((always_inline)) {
+    const uint64_t least = k < a ? k : a;
+    a = k > a ? k : a;
+    b = least > b ? least : b;
+  };
+  for (; items; items &= items - 1) {
+    const int e = first + gate_item(__builtin_ctz(items), lanes, in);
+    enter(gate_order(1.0 / (1.0 + exp(-(double)gate_load(Row{}, p.L, t * p.ldl + e))) + (p.bias ? (double)p.bias[e] : 0.0)));
+  }
+  for (int d = 1; d < lanes; d <<= 1) {
+    const uint64_t oa = __shfl_xor(a, d, 64), ob = __shfl_xor(b, d, 64);
+    enter(oa);
+    enter(ob);
+  }
+  if (p.group_top > 1 && b != kGateMasked) a = gate_order(gate_value(a) + gate_value(b));
+  int at = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const uint64_t k = __shfl(a, base + g * lanes, 64);
+    at += k > a || (k == a && g < group);
+  }
+  return at;
+}
+
 // The float32 search. LANES lanes take a token (four tokens a wave, or one). A key is an
 // integer of the float32 key's order; the largest one below the last choice is the largest of
 // (key - last) as unsigned numbers, so nothing is removed. Its lowest bits say whose it
@@ -306,15 +336,21 @@ __device__ __forceinline__ void gate_store_row(void* p, int64_t at, int lanes, i
 //     expert's is larger. Exact for 16-bit logits, which have zeros there, and for
 //     float32 ones that differ above these bits.
 //   experts ranked by scores and a bias: the lane's item from behind; the lane is the one
-//     that has the key. Two keys next to each other in the order have to be further apart
-//     than their errors: relative to the score 2^-20 (sigmoid: 2^-21 and half a step) or
-//     2^-17 (softmax: the largest logit taken off first, half a step of a number below 128
-//     where the score is not 0 to float32, 2^-18; the sum, whose additions one after the
-//     other are PER + 6 at most), half a step more for the bias, and relative to the key
-//     2^-19 for the lowest bits.
-//   groups: the group's number from behind in the lowest 6 bits, 2^-17 of the rank.
+//     that has the key, the first of several. Two keys next to each other in the order have
+//     to be further apart than their errors: relative to the score 1.25 2^-21 (sigmoid: 2^-21,
+//     and half a step for the bias) or 2^-17 (softmax: the largest logit taken off first,
+//     half a step of a number below 128 where the score is not 0 to float32, 2^-18; the
+//     sum, whose additions one after the other are PER + 6 at most), and relative to the
+//     key 2^-19 for the lowest bits.
+//   groups: ranks without such bits, apart by their keys' errors and half a step of the sum.
 // (Experts' numbers in the lowest bits of biased keys too: one token in ten of the case above
 // was too close, 54 us for the choices alone.)
+//
+// Neighbours that are too close are one token in 300 there, and one token done again in 64 bits
+// takes about 10 us more than the others (22 us in all; 16.5 so). So with sigmoid scores, whose keys do not
+// hang on each other, what is close is put right alone: groups are ranked by their keys in 64
+// bits before the search, and behind it, which then goes on to the first key that is clear of
+// the last choice, the choices and those beyond them, a lane each, are sorted.
 template <class Row, int LANES, int PER, bool GROUPS>
 __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   constexpr int WIDE = 64 / LANES;                     // tokens a wave
@@ -377,23 +413,24 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   for (int i = 0; i < PER; ++i)  // (+ 0: -0 is no other number)
     key[i] = l[i] == -inf ? 0u : (gate_order32(l[i] + 0.0f) & ~low) | (low - (scored ? i : first + gate_item(i, lanes, in)));
   // Whether two keys, or two ranks, a above b, are too close for their errors.
-  const float err = soft ? 0x1p-17f : 0x1p-20f;
+  const float err = soft ? 0x1p-17f : 0x1.4p-21f;
   auto unsure = [&](unsigned a, unsigned b, unsigned rest, float cut, float bias) {
     const float u = gate_value32(a & ~rest), v = gate_value32(b & ~rest), size = __builtin_fabsf(u) + __builtin_fabsf(v);
     return u - v <= cut * size + err * (size + 2.0f * bias) + 1e-30f;
   };
   auto same = [&](unsigned a, unsigned b) { return sizeof(GateElem<Row>) == 4 && ((a ^ b) & ~low) == 0; };
+  constexpr uint64_t all = LANES == 64 ? ~(uint64_t)0 : ((uint64_t)1 << (LANES & 63)) - 1;
   if constexpr (GROUPS) {
-    // The two largest keys (by logits and two of them: scores) of the group, in each of its lanes.
+    // The two largest keys (where scores rank groups: without their lowest bits' numbers) of the
+    // group, in each of its lanes.
     unsigned a = 0, b = 0;
     auto enter = [&](unsigned k) {
       const unsigned least = k < a ? k : a;
       a = k > a ? k : a;
       b = least > b ? least : b;
     };
-    const bool scores = ranked && !scored;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) enter(scores ? (key[i] ? gate_order32(s[i]) : 0u) : key[i]);
+    for (int i = 0; i < PER; ++i) enter(ranked ? (key[i] ? gate_order32((scored ? l[i] : s[i]) + 0.0f) : 0u) : key[i]);
     auto join = [&](unsigned oa, unsigned ob) {
       enter(oa);
       enter(ob);
@@ -403,51 +440,104 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     if (p.lanes > 2) join(gate_swap<0x141>(a), gate_swap<0x141>(b));
     if (p.lanes > 3) join(gate_swap<0x140>(a), gate_swap<0x140>(b));
     if (p.lanes > 4) join(__shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
-    if (ranked && a) {  // the lowest bits: the group's number from behind
-      const unsigned rest = scores ? 0u : low;
-      float r = gate_value32(a & ~rest);
-      if (p.group_top > 1 && b) r += gate_value32(b & ~rest);
-      a = (gate_order32(r + 0.0f) & ~63u) | (63u - group);
-    }
+    if (ranked && a && p.group_top > 1 && b) a = gate_order32(gate_value32(a) + gate_value32(b) + 0.0f);
     // The best groups' ranks, down to the last one that is kept, and the next.
     unsigned rank = group < p.groups ? a : 0, last = ~0u;
     const unsigned own = rank;
+    int kept = 0;  // (groups of one rank leave together)
     for (int j = 0; j < p.top_groups; ++j) {
       const unsigned m = gate_max32<LANES>(rank);
-      last = m ? m : last;
-      rank = rank < m ? rank : 0;
+      const int many = __builtin_popcountll(__ballot(rank == m) >> (lane - li) & all) >> p.lanes;
+      if (m && kept < p.top_groups) {
+        last = m;
+        kept += many;
+        rank = rank < m ? rank : 0;
+      }
     }
     const unsigned next = gate_max32<LANES>(rank);
-    close = next && (ranked ? unsure(last, next, 63u, 0x1p-17f, 2.0f * bmax) : same(last, next));
-    if (own < last) {
+    // (A sum of two keys: half a step.)
+    close = kept > p.top_groups || (next && (ranked ? unsure(last, next, 0u, 0x1p-23f, 2.0f * bmax) : same(last, next)));
+    bool out = own < last;
+    if (ranked && !soft && __ballot(close)) {
+      // Of the groups of such tokens the keys that may be one of the two largest.
+      const float second = b ? gate_value32(b) : -inf;
+      const float least = second - (2.0f * err * (__builtin_fabsf(second) + 2.0f * bmax) + 1e-30f);
+      unsigned items = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) items |= (key[i] && (scored ? l[i] : s[i]) >= least ? 1u : 0u) << i;
+      const bool better =
+          gate_group_place<Row>(p, t, close ? items : 0u, group, in, lanes, lane - li) < p.top_groups;
+      out = close ? !better : out;
+      close = false;
+    }
+    if (out) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) key[i] = 0;
     }
   }
-  // The choices, and one more that the last one must be clear of. Lane j keeps choice j.
-  constexpr uint64_t all = LANES == 64 ? ~(uint64_t)0 : ((uint64_t)1 << (LANES & 63)) - 1;
-  unsigned taken = 0;
-  int id = -1;
-  for (int j = 0; j <= p.top; ++j) {
+  // The choices in falling order, and one more that the last one must be clear of. Lane j keeps
+  // choice j: its key and the lane that has it. (What is done with them is done once, behind.)
+  const bool sorted = scored && !soft;
+  unsigned best = 0, below = 0, kept = 0;  // below: what this lane's next key is less than
+  int from = 0, at = 0;
+  auto step = [&](bool first) __attribute__((always_inline)) {
     unsigned m = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) m = key[i] - taken > m ? key[i] - taken : m;
-    // (Before the first: taken is 0 and m the largest key. Where none is left below taken, m is
-    // a difference to one above it.)
-    m += taken;
-    m = j > 0 && m >= taken ? 0 : m;
-    const unsigned best = gate_max32<LANES>(m);
-    if (j > 0) close |= best && (scored ? unsure(taken, best, low, 0x1p-19f, bmax) : same(taken, best));
-    int expert = low - (best & low);
-    if (scored) {
-      const uint64_t having = __ballot(m == best) >> (lane - li) & all;
-      close |= best && (having & (having - 1));  // (several: not decided here)
-      const int from = __builtin_ctzll(having), fin = GROUPS ? from & (lanes - 1) : from;
-      expert = (GROUPS ? (from >> p.lanes) * (p.E / p.groups) : 0) + gate_item(expert, lanes, fin);
+    for (int i = 0; i < PER; ++i) m = key[i] - below > m ? key[i] - below : m;
+    // (Before the first: below is 0 and m the largest key. Where none is left below it, m is a
+    // difference to one that is not.)
+    m += below;
+    m = !first && m >= below ? 0 : m;
+    best = gate_max32<LANES>(m);
+    below = best;
+    if (scored) {  // of several the first; the others' lanes have theirs ahead of them
+      from = __builtin_ctzll(__ballot(m == best) >> (lane - li) & all);
+      below += li > from;
     }
-    if (j < p.top && li == j && best) id = expert;
-    taken = best ? best : 1;  // (nothing lies below 1)
+  };
+  for (int j = 0; j <= p.top; ++j) {
+    step(j == 0);
+    kept = li == j ? best : kept;
+    at = li == j ? from : at;
   }
+  // Whether lane j's is too close to the one before; in front of the first none is.
+  auto doubtful = [&](unsigned a, unsigned b) { return b && (scored ? unsure(a, b, low, 0x1p-19f, bmax) : same(a, b)); };
+  const unsigned before = __shfl_up(kept, 1, LANES);
+  const uint64_t doubts = __ballot(li > 0 && li <= p.top && doubtful(before, kept)) >> (lane - li) & all;
+  bool near = doubts != 0, open = sorted && p.top < LANES && (doubts >> (p.top & 63) & 1);
+  if (p.top == LANES)  // (no lane for the one beyond)
+    close |= (__ballot(li == LANES - 1 && doubtful(kept, best)) >> (lane - li) & all) != 0;
+  // Where 64 bits decide about the last choice, those beyond it, to the first that is clear.
+  if (li == p.top && !open) kept = 0;
+  for (int j = p.top + 1; j < LANES && __ballot(open); ++j) {
+    const unsigned last = best;
+    step(false);
+    open = open && doubtful(last, best);
+    if (li == j && open) {
+      kept = best;
+      at = from;
+    }
+  }
+  close |= sorted ? open : near;  // (more than a lane each)
+  int id = low - (kept & low);
+  if (scored) id = (GROUPS ? (at >> p.lanes) * (p.E / p.groups) : 0) + gate_item(id, lanes, GROUPS ? at & (lanes - 1) : at);
+  if (!kept) id = -1;
+  if (sorted && __ballot(near)) {
+    uint64_t exact = kGateMasked;
+    if (id >= 0) {
+      const double score = 1.0 / (1.0 + exp(-(double)gate_load(Row{}, p.L, t * p.ldl + id)));
+      exact = gate_order(score + (double)p.bias[id]);
+    }
+    int place = id >= 0 ? 0 : li;
+#pragma unroll 4
+    for (int u = 0; u < LANES; ++u) {
+      const int other = __shfl(id, u, LANES);
+      const uint64_t k = __shfl(exact, u, LANES);
+      place += id >= 0 && other >= 0 && (k > exact || (k == exact && other < id));
+    }
+    id = __builtin_amdgcn_ds_permute((lane - li + place) << 2, id);
+  }
+  if (li >= p.top) id = -1;
   // Weights. Renormalised softmax scores are the softmax of the chosen logits.
   const bool chosen = id >= 0;
   const float z = chosen ? gate_load(Row{}, p.L, t * p.ldl + id) : -inf;
@@ -631,7 +721,7 @@ int gemm_gate(int64_t T, int64_t E, int64_t top, int dtype, const void* L, int64
     if (top_groups < 1 || top_groups > groups)
       return bad("%s=%lld is not between 1 and %lld groups", "top_groups", top_groups, groups);
     const int64_t size = E / groups;
-    if (group_top < 1 || group_top > 2 || (group_top > 1 && (groups == 1 || group_top > size)))
+    if (group_top < 1 || group_top > 2 || (groups > 1 && group_top > size))
       return bad("%s=%lld is neither 1 nor 2, or more than a group's %lld experts", "group_top", group_top, size);
     if (top > top_groups * size) return bad("%s=%lld is more than the %lld experts to choose from", "top", top, top_groups * size);
     const int64_t n = T * top;

@@ -241,7 +241,7 @@ GEMM_API int64_t gemm_norm_grad_workspace(int64_t M, int64_t N);
  * groups    >= 1, divides E. Experts form `groups` groups of neighbours. A
  *           group's rank is the sum of its group_top (1 or 2) largest keys, and
  *           only the experts of the top_groups best groups are chosen from.
- *           groups == 1: all of them (top_groups and group_top are 1).
+ *           groups == 1: all of them (top_groups is 1; group_top changes nothing).
  * top       experts a token, at most top_groups * (E / groups), and at most 64.
  * renorm    != 0: the weights of a token's choices are divided by their sum
  *           (where that is 0 they stay 0).

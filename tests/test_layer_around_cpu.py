@@ -61,7 +61,7 @@ def gate(T=4, E=64, top=4, dtype="f32", L=P[0], ldl=64, score="softmax", bias=P[
     (dict(E=1025, ldl=1025), 2), (dict(E=128, ldl=128, top=65), 2), (dict(E=3, ldl=3), 1), (dict(dtype=3), 2), (dict(ldl=63), 1),
     (dict(score=2), 1), (dict(score=-1), 1), (dict(groups=0), 1), (dict(groups=5), 1), (dict(groups=-8), 1),
     (dict(groups=8, top_groups=0), 1), (dict(groups=8, top_groups=9), 1), (dict(groups=8, top_groups=4, group_top=3), 1),
-    (dict(groups=8, top_groups=4, group_top=0), 1), (dict(group_top=2), 1), (dict(groups=64, top_groups=8, group_top=2), 1),
+    (dict(groups=8, top_groups=4, group_top=0), 1), (dict(group_top=3), 1), (dict(groups=64, top_groups=8, group_top=2), 1),
     (dict(groups=32, top_groups=1, top=3), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(L=None), 1),
     (dict(L=P[0] + 2), 1), (dict(bias=P[1] + 2), 1), (dict(ids=None), 1), (dict(weights=None), 1), (dict(ids=P[2] + 2), 1),
     (dict(ids=P[0]), 3), (dict(weights=P[0] + 1020), 3), (dict(weights=P[1]), 3), (dict(weights=P[2] + 60), 3),

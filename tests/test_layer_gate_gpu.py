@@ -135,6 +135,9 @@ def test_groups(score, group_top):
         check(gen, T, E, top, "f32", score, bias=True, groups=groups, top_groups=top_groups, group_top=group_top)
         check(gen, T, E, top, "bf16", score, groups=groups, top_groups=top_groups, group_top=group_top, renorm=False)
     check(gen, 5, 12, 2, groups=12, top_groups=3)  # groups of one
+    for E in (1, 8, 200):  # a single group: no ranks
+        check(gen, 5, E, 1, "f32", score, group_top=group_top)
+        check(gen, 5, E, 1, "bf16", score, bias=True, group_top=group_top)
 
 
 def test_equal_scores_take_the_lowest_number():
@@ -163,6 +166,23 @@ def test_scores_that_differ_in_64_bits_alone():
         bias = (0.75 - scores64(L.double(), score)[0]).float()  # every key is 0.75 to float32
         check(gen, 200, 64, 8, "f32", score, logits=L.to(DEV), bias=bias.to(DEV))
         check(gen, 200, 64, 8, "f32", score, logits=L.to(DEV), bias=bias.to(DEV), groups=8, top_groups=3, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_few_close_scores(score):
+    """Two, three or more keys in a row that float32 does not tell apart, among and beyond the choices, in one
+    lane's experts and in several; in all tokens, or in one of many."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(8)
+    for E, top in ((64, 4), (256, 8), (100, 16), (512, 20), (1024, 64)):
+        for step, part in ((8.0, 1.0), (2.0, 1.0), (8.0, 0.02)):
+            L = torch.randn(150, E, generator=gen)
+            near = torch.round(L * step) / step + torch.randint(-2, 3, (150, E), generator=gen) * 2.0 ** -23
+            L = torch.where(torch.rand(150, 1, generator=gen) < part, near, L).to(DEV)
+            bias = (torch.randint(-2, 3, (E,), generator=gen) * 2.0 ** -24).to(DEV)
+            check(gen, 150, E, top, "f32", score, logits=L, bias=bias)
+            check(gen, 150, E, top, "f32", score, logits=L, bias=torch.zeros(E, device=DEV), renorm=False)
+            check(gen, 150, E, top, "f32", score, logits=L, bias=bias, groups=4, top_groups=2, group_top=2)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
