@@ -618,7 +618,8 @@ __global__ void __launch_bounds__(256) layer_gate_grad_kernel(const GateGradArgs
     const float z = expf(-l), r = 1.0f / (1.0f + z);
     s = chosen ? r : 0.0f;
     if (p.renorm) {
-      const float sum = gate_sum32<LANES>(s), mean = gate_sum32<LANES>(g * s) / sum;
+      // (s / sum first: a single choice's gradient is exactly 0.)
+      const float sum = gate_sum32<LANES>(s), mean = gate_sum32<LANES>(g * (s / sum));
       ds = sum == 0.0f ? 0.0f : (g - mean) / sum;
     }
     ds = chosen ? s * (l > 0.0f ? z * r : 1.0f - s) * ds : 0.0f;  // (1 - s = z / (1 + z))

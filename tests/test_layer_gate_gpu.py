@@ -231,6 +231,21 @@ def test_zero_sums_stay_zero():
     assert ids.tolist() == [[0, 1], [0, 1]] and (w == 0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_single_choice_has_the_whole_weight(score):
+    need_gpu()
+    import dense_gemm_tile_amd as dgt
+    gen = torch.Generator().manual_seed(9)
+    for T, E in ((300, 64), (40, 500)):
+        L, dw = randn(gen, T, E), randn(gen, T, 1)
+        ids, w = gate(L, "f32", score, None, 1, 1, 1, 1, True, 2.5)
+        assert torch.equal(w, torch.full_like(w, 2.5))
+        dl = out(T, E)
+        dgt.gemm_gate_grad(T, E, 1, "f32", L, E, score, True, 2.5, ids, dw, dl, E, stream=torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        assert torch.equal(dl, torch.zeros_like(dl))
+
+
 def test_ids_of_another_program():
     """Ids outside the range are left out; the same one twice counts twice."""
     need_gpu()
