@@ -487,7 +487,7 @@ __device__ __forceinline__ void layer_group_r(LayerGroupR<GROUP>& v, const Layer
 template <class E, class Tag, int ACT>
 __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile& q, int r, int c,
                                              const float* lds, const float (&bias)[8],
-                                             LayerGroupR<E::GROUP>& res) {
+                                             LayerGroupR<E::GROUP>& res, float scale) {
   const int osz = p.out32 ? 4 : 2;
   const int64_t ystep = E::RPP * p.ldy * osz, zstep = E::RPP * p.ldz * 2;
   char* y = q.Y + ((int64_t)r * p.ldy + c) * osz;
@@ -508,7 +508,7 @@ __device__ __forceinline__ void layer_passes(const LayerArgs& p, const LayerTile
       for (int e = 0; e < 8; ++e) x[e] += bias[e];
       if (row < q.M && c < q.N) {
         if (q.Z) *reinterpret_cast<u32x4_at2*>(z) = layer_pack8<Tag>(x);
-        if constexpr (ACT == ACT_SCALE) layer_scale8(x, *p.scale);
+        if constexpr (ACT == ACT_SCALE) layer_scale8(x, scale);
         else layer_act8_of<ACT>(x);
         if (q.R) {
           float f[8];
@@ -541,7 +541,8 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
   constexpr int P = E::P, AR = E::BATCH / At::M;  // atom rows of a batch
   const int cl = 8 * (lane % E::LPR), rl = lane / E::LPR;
   const int c = c0 + cl, nv = q.N - c >= 8 ? 8 : q.N - c;
-  float bias[8];
+  float bias[8], scale = 1.0f;
+  if (p.act == ACT_SCALE) scale = *p.scale;  // (uniform; read for every row it cost 3 us a 256 x 256 tile)
 #pragma unroll
   for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
   if (q.bias && nv > 0) {
@@ -566,12 +567,12 @@ __device__ __forceinline__ void layer_store(typename C::At::acc_t (&acc)[C::TM][
     const float* const from = lds + rl * P + cl;
     if (p.whole8) {
       switch (p.act) {
-        case ACT_RELU: layer_passes<E, Tag, ACT_RELU>(p, q, r + rl, c, from, bias, res); break;
-        case ACT_GELU: layer_passes<E, Tag, ACT_GELU>(p, q, r + rl, c, from, bias, res); break;
-        case ACT_GELU_ERF: layer_passes<E, Tag, ACT_GELU_ERF>(p, q, r + rl, c, from, bias, res); break;
-        case ACT_SILU: layer_passes<E, Tag, ACT_SILU>(p, q, r + rl, c, from, bias, res); break;
-        case ACT_SCALE: layer_passes<E, Tag, ACT_SCALE>(p, q, r + rl, c, from, bias, res); break;
-        default: layer_passes<E, Tag, ACT_NONE>(p, q, r + rl, c, from, bias, res); break;
+        case ACT_RELU: layer_passes<E, Tag, ACT_RELU>(p, q, r + rl, c, from, bias, res, scale); break;
+        case ACT_GELU: layer_passes<E, Tag, ACT_GELU>(p, q, r + rl, c, from, bias, res, scale); break;
+        case ACT_GELU_ERF: layer_passes<E, Tag, ACT_GELU_ERF>(p, q, r + rl, c, from, bias, res, scale); break;
+        case ACT_SILU: layer_passes<E, Tag, ACT_SILU>(p, q, r + rl, c, from, bias, res, scale); break;
+        case ACT_SCALE: layer_passes<E, Tag, ACT_SCALE>(p, q, r + rl, c, from, bias, res, scale); break;
+        default: layer_passes<E, Tag, ACT_NONE>(p, q, r + rl, c, from, bias, res, scale); break;
       }
     } else {
 #pragma unroll 1
