@@ -593,10 +593,11 @@ __global__ void __launch_bounds__(256) layer_gate_exact_kernel(const GateArgs p)
   }
 }
 
+constexpr float kGateNoScore = -709.78271484375f;  // exp(-it) is infinity in 64 bits
 // With the chosen s_j, their sum S and g_j = scale dw_j:
 //   ds_j = g_j, or renormalised (g_j - sum_k g_k s_k / S) / S
 //   softmax: dl_e = s_e (ds_e - sum_j ds_j s_j), the sum 0 where renormalised
-//   sigmoid: dl_j = s_j (1 - s_j) ds_j
+//   sigmoid: dl_j = s_j (1 - s_j) ds_j, renormalised s_j / S (1 - s_j) (g_j - sum_k g_k s_k / S)
 // Renormalised softmax weights need the chosen logits alone: s_j / S is their own
 // softmax.
 template <class Row, int LANES, int PER>
@@ -618,11 +619,19 @@ __global__ void __launch_bounds__(256) layer_gate_grad_kernel(const GateGradArgs
     const float z = expf(-l), r = 1.0f / (1.0f + z);
     s = chosen ? r : 0.0f;
     if (p.renorm) {
-      // (s / sum first: a single choice's gradient is exactly 0.)
-      const float sum = gate_sum32<LANES>(s), mean = gate_sum32<LANES>(g * (s / sum));
-      ds = sum == 0.0f ? 0.0f : (g - mean) / sum;
+      // The shares s / sum have ordinary sizes also where s does not (from -88 on float32 has no
+      // number for it), so they are made of scores over exp(low): exp(l - low) / (1 + exp(l)).
+      const float top = gate_value32(gate_max32<LANES>(l == l && chosen ? gate_order32(l) : 0u));
+      const float low = top < 0.0f ? top : 0.0f;
+      const float up = chosen ? (l > 0.0f ? r : expf(l - low) / (1.0f + expf(l))) : 0.0f;
+      const float share = up / gate_sum32<LANES>(up);  // (of a single choice exactly 1, its gradient 0)
+      const float mean = gate_sum32<LANES>(chosen ? g * share : 0.0f);
+      // Past the last logit whose score is above 0 in 64 bits the weights are 0, and stay so.
+      s = top <= kGateNoScore ? 0.0f : share;
+      ds = g - mean;
     }
-    ds = chosen ? s * (l > 0.0f ? z * r : 1.0f - s) * ds : 0.0f;  // (1 - s = z / (1 + z))
+    // (1 - s = z / (1 + z))
+    ds = chosen ? s * (l > 0.0f ? z * r : 1.0f - r) * ds : 0.0f;
   } else if (p.renorm) {
     const bool nan = l != l;
     const float top = gate_value32(gate_max32<LANES>(nan ? 0u : gate_order32(l)));

@@ -269,8 +269,9 @@ GEMM_API int gemm_gate(int64_t T, int64_t E, int64_t top, int dtype, const void*
  * gemm_gate_grad: dL (T x E of `dtype`), the gradient of L from the gradients
  * dweights of gemm_gate's weights, for the choices in ids. An id outside [0, E)
  * is a dropped choice, whose gradient is not read; a token without choices gets
- * zeros. The gradient does not depend on the bias and the groups except through
- * ids. dL may be L itself (same pointer and leading dimension).
+ * zeros, and one whose renormalised weights gemm_gate leaves at 0. The gradient does
+ * not depend on the bias and the groups except through ids. dL may be L itself
+ * (same pointer and leading dimension).
  */
 GEMM_API int gemm_gate_grad(int64_t T, int64_t E, int64_t top, int dtype, const void* L,
                   int64_t ldl, int score, int renorm, float scale, const int32_t* ids,
