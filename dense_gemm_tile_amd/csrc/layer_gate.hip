@@ -165,12 +165,21 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
 #pragma unroll
     for (int i = 0; i < PER; ++i) s[i] = key[i] == kGateMasked ? 0.0 : 1.0 / (1.0 + exp(-s[i]));
   }
+  // Without a bias the order is the logits', also where scores are equal; groups that two scores
+  // rank have their sum.
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 64 + lane;
     const double bias = p.bias && e < p.E ? (double)p.bias[e] : 0.0;
     if (key[i] != kGateMasked) key[i] = bias == -__builtin_inf() ? kGateMasked : gate_order(s[i] + bias);
   }
+  auto by_logits = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)  // (+ 0: -0 is no other number)
+      if (key[i] != kGateMasked && key[i] != kGateNan)
+        key[i] = gate_order((double)gate_load(Row{}, p.L, t * p.ldl + i * 64 + lane) + 0.0);
+  };
+  if (!p.bias && !(GROUPS && p.group_top > 1)) by_logits();
   if constexpr (GROUPS) {
     // Each lane ranks groups lane, lane + 64, ... from the keys in LDS.
     uint64_t* const rank = all + 64 * PER;
@@ -211,6 +220,7 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
       const int e = i * 64 + lane;
       if (e < p.E && rank[e / size] != ~(uint64_t)0) key[i] = kGateMasked;
     }
+    if (!p.bias && p.group_top > 1) by_logits();
   }
   // Choices in falling order.
   id = -1;
