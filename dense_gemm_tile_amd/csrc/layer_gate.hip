@@ -133,8 +133,8 @@ __device__ __forceinline__ GateBest gate_best(GateBest b) {
 }
 
 // The choices of token t in 64 bits: lane j gets the id and the score of choice j (-1 and 0
-// past the last). Lane l holds experts l, l + 64, ... all: 2 * 64 * PER numbers of LDS,
-// this wave's own (GROUPS).
+// past the last), renormalised softmax scores over the largest of them. Lane l holds experts
+// l, l + 64, ... all: 2 * 64 * PER numbers of LDS, this wave's own (GROUPS).
 template <class Row, int PER, bool GROUPS>
 __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, uint64_t* all, int& id, double& weight) {
   const int lane = threadIdx.x & 63;
@@ -244,6 +244,13 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (b.at == i * 64 + lane) key[i] = kGateMasked;
+  }
+  // Renormalised softmax scores are the softmax of the chosen logits, which has a sum also where
+  // all chosen scores are 0 in 64 bits, as far below the largest logit as a bias can reach.
+  if (p.score == GEMM_SCORE_SOFTMAX && p.renorm) {
+    const double l = id >= 0 ? (double)gate_load(Row{}, p.L, t * p.ldl + id) : -__builtin_inf();
+    const double best = gate_wave_max(l);
+    if (id >= 0 && weight == weight) weight = exp(l - best);
   }
 }
 

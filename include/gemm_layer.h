@@ -243,8 +243,8 @@ GEMM_API int64_t gemm_norm_grad_workspace(int64_t M, int64_t N);
  *           only the experts of the top_groups best groups are chosen from.
  *           groups == 1: all of them (top_groups is 1; group_top changes nothing).
  * top       experts a token, at most top_groups * (E / groups), and at most 64.
- * renorm    != 0: the weights of a token's choices are divided by their sum
- *           (where that is 0 they stay 0).
+ * renorm    != 0: the weights of a token's choices are divided by their sum (sigmoid
+ *           scores that are all 0 in 64 bits stay 0).
  * scale     a factor of every weight.
  *   ids[T * top]      the chosen experts, by falling key; equal ones by rising
  *                     number (of groups too)

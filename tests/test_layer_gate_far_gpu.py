@@ -1,5 +1,5 @@
 """The gate far from 0: sigmoid scores next to float32's smallest numbers and past 64 bits' smallest, and their
-gradient."""
+gradient; softmax scores that are 0 in 64 bits."""
 import math
 
 import pytest
@@ -7,6 +7,7 @@ import torch
 
 from gpu_helpers import need_gpu, say
 from layer_helpers import DEV, DT, U32, close, half_step, out, tiny
+from test_layer_gate_gpu import gate
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,25 @@ def test_nan_and_infinite_logits_of_the_gradient():
     assert torch.isnan(dl[0, :2]).all() and dl[0, 2] == 0
     assert dl[1, 0] == 0 and abs(float(dl[1, 1])) < 1e-40 and dl[1, 2] == 0
     assert torch.equal(dl[2], torch.zeros(3, device=DEV))  # a single choice that is left
+
+
+def test_renormalised_softmax_far_below_the_largest():
+    """Choices whose softmax scores are 0 in 64 bits still have the weights that their logits give, in every form: a
+    bias or the groups can pick them."""
+    need_gpu()
+    for E, groups, top_groups in ((8, 1, 1), (64, 8, 1), (130, 65, 1)):
+        size = E // groups
+        L = torch.full((4, E), -3000.0)
+        at = torch.arange(2) + (size if groups > 1 else 2)  # chosen by their bias
+        L[:, 0] = 0.0
+        L[:, at[0]], L[:, at[1]] = -1000.0, -1001.0
+        L[1, at[0]] = -3.4e38  # the lowest number beside a number
+        L[2, at] = -3.4e38
+        L[3, E - 1] = math.nan
+        bias = torch.zeros(E)
+        bias[at] = torch.tensor([9.0, 8.0])
+        ids, w = gate(L.to(DEV), "f32", "softmax", bias.to(DEV), groups, top_groups, 1, 2, True, 2.0)
+        assert torch.equal(ids[:3].cpu(), at.to(torch.int32).expand(3, 2)), (E, ids)
+        want = 2.0 * torch.softmax(L[:3, at].double(), 1)
+        close(w[:3], want.to(DEV), 40 * U32 * want.to(DEV) + 1e-45, "weights")
+        assert torch.isnan(w[3]).all()
