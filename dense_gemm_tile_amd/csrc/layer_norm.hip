@@ -268,9 +268,10 @@ __global__ void __launch_bounds__(W > 4 ? 64 * W : 256) layer_norm_grad_kernel(c
       if (p.R) r[v].get(rr[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool has = 8 * lane + v * SPAN + e < p.N;
+        // (A row that is not there reads the last one, where dX may stand by now: no element of it counts.)
+        const bool has = in && 8 * lane + v * SPAN + e < p.N;
         u[v][e] = has ? (u[v][e] - m) * rs : 0.0f;
-        h[v][e] = has && in ? h[v][e] : 0.0f;
+        h[v][e] = has ? h[v][e] : 0.0f;
         sg[v][e] = __builtin_fmaf(h[v][e], u[v][e], sg[v][e]);
         sb[v][e] += h[v][e];
         h[v][e] *= g[v][e];
