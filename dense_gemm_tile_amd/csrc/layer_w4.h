@@ -30,10 +30,10 @@ struct W4Args {
 // slices of 8 waves.
 constexpr int kW4MaxRuns = 1536;
 
-// The tile that a call took.
+// The tile that a call took, and whether one launch does not hold so many of it.
 struct W4Form {
   int waves, rows, columns;
-  bool whole;
+  bool whole, many;
 };
 
 // The launches, a file for each type.
@@ -393,12 +393,12 @@ __global__ void __launch_bounds__(KW * 64, 2) layer_w4_split_kernel(const W4Args
 
 // ------------------------------------------------------------------ launches --
 // Workgroups of tiles of bm x bn: by rows as many as groups of any sizes need.
-unsigned w4_grid(LayerArgs& a, int bm, int bn) {
+int64_t w4_grid(LayerArgs& a, int bm, int bn) {
   a.tiles_m = (a.M + bm - 1) / bm;
   a.tiles_n = (a.N + bn - 1) / bn;
   a.group_m = 8;
   const int64_t g = a.mode == LAYER_DENSE ? 1 : a.G < a.M ? a.G : a.M;
-  return (unsigned)(((int64_t)a.M + g * (bm - 1)) / bm * a.tiles_n);
+  return ((int64_t)a.M + g * (bm - 1)) / bm * a.tiles_n;
 }
 
 template <class Tag, int MODE, int AL, int NT, int KW, bool WHOLE = true>
@@ -410,8 +410,10 @@ struct W4Split {
     return (w4_lds<AL, NT, KW>() + scales(p)) * count <= 160 * 1024;
   }
   static hipError_t launch(W4Args p, hipStream_t s, W4Form& form) {
-    form = {KW, 8 * AL, 16 * NT, WHOLE};
-    const dim3 grid(w4_grid(p.a, 8 * AL, 16 * NT)), block(KW * 64);
+    const int64_t tiles = w4_grid(p.a, 8 * AL, 16 * NT);
+    form = {KW, 8 * AL, 16 * NT, WHOLE, tiles > 0xffffffffll / (KW * 64)};
+    if (form.many) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)tiles), block(KW * 64);
     auto go = [&](auto grp) {
       constexpr int GRP = decltype(grp)::value;
       const size_t lds = (size_t)scales(p);

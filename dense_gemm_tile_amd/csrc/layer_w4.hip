@@ -65,9 +65,6 @@ int run_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t*
     CHECK(check_ptr(moff));
     CHECK(check_apart(my, moff));
   }
-  // (A launch holds less than 2^32 threads; tiles are at least 8 x 16, and groups' last ones cut short.)
-  const __int128 tiles = ((__int128)M / 8 + (g < M ? g : M) + 1) * ((N + 15) / 16);
-  if (tiles > ((int64_t{1} << 32) - 1) / 512) return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles for one launch");
   W4Args p{};
   LayerArgs& a = p.a;
   a.A = A;
@@ -96,8 +93,10 @@ int run_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dtype, const int32_t*
   hipStream_t s = static_cast<hipStream_t>(stream);
   W4Form& form = g_w4_path.form;
   g_w4_path.dense = dense;
+  const hipError_t e = dtype == GEMM_DTYPE_F16 ? launch_w4_f16(p, s, form) : launch_w4_bf16(p, s, form);
+  if (form.many) return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles for one launch");
   set_path_writer(write_w4_path);
-  return launched(dtype == GEMM_DTYPE_F16 ? launch_w4_f16(p, s, form) : launch_w4_bf16(p, s, form));
+  return launched(e);
 }
 
 }  // namespace
