@@ -254,9 +254,20 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
   }
 }
 
-// exp(x) within 2^-22 of itself, and 1 / (1 + exp(-x)) within 2^-21: the exponent of 2 in two
-// floats, so that its rounding does not grow with it. (The library's exponential and
-// division: 16384 tokens, 8 of 256 experts with a bias 18 us, 16 so.)
+// A sigmoid score and one less it, each to a few half steps of itself, also among float32's
+// subnormal numbers.
+struct GateScore {
+  float s, rest, t;  // t: exp(-|l|)
+};
+__device__ __forceinline__ GateScore gate_scores(float l) {
+  const float t = expf(-__builtin_fabsf(l)), one = 1.0f / (1.0f + t), small = t / (1.0f + t);
+  return l < 0.0f ? GateScore{small, one, t} : GateScore{one, small, t};
+}
+
+// For keys: exp(x) within 2^-22 of itself, and 1 / (1 + exp(-x)) within 2^-21, where |x| is below
+// 87; below 2^-125 both may be 0, which the 1e-30 of unsure() covers. The exponent of 2 in
+// two floats, so that its rounding does not grow with it. (The library's exponential
+// and division: 16384 tokens, 8 of 256 experts with a bias 18 us, 16 so.)
 __device__ __forceinline__ float gate_exp(float x) {
   const float c = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);
   const float hi = c * kLog2e, lo = __builtin_fmaf(c, 1.92596298e-8f, __builtin_fmaf(c, kLog2e, -hi));
@@ -560,12 +571,12 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
   const float z = chosen ? gate_load(Row{}, p.L, t * p.ldl + id) : -inf;
   float out = 0.0f;
   if (!soft) {
-    out = gate_sigmoid(z);
+    out = gate_scores(z).s;
   } else if (p.renorm) {
     const float best = gate_value32(gate_max32<LANES>(chosen ? gate_order32(z) : 0u));
-    out = gate_exp(z - best);
+    out = expf(z - best);
   } else {
-    out = gate_exp(z - top) / sum;
+    out = expf(z - top) / sum;
   }
   out = chosen ? out : 0.0f;
   if (p.renorm) {
@@ -633,22 +644,21 @@ __global__ void __launch_bounds__(256) layer_gate_grad_kernel(const GateGradArgs
 #pragma unroll
   for (int i = 0; i < PER; ++i) d[i] = 0.0f;
   if (p.score == GEMM_SCORE_SIGMOID) {
-    const float z = expf(-l), r = 1.0f / (1.0f + z);
-    s = chosen ? r : 0.0f;
+    const GateScore z = gate_scores(l);
+    s = chosen ? z.s : 0.0f;
     if (p.renorm) {
-      // The shares s / sum have ordinary sizes also where s does not (from -88 on float32 has no
+      // The shares s / sum have ordinary sizes also where s does not (from -104 on float32 has no
       // number for it), so they are made of scores over exp(low): exp(l - low) / (1 + exp(l)).
       const float top = gate_value32(gate_max32<LANES>(l == l && chosen ? gate_order32(l) : 0u));
       const float low = top < 0.0f ? top : 0.0f;
-      const float up = chosen ? (l > 0.0f ? r : expf(l - low) / (1.0f + expf(l))) : 0.0f;
+      const float up = chosen ? (l < 0.0f ? expf(l - low) / (1.0f + z.t) : z.s) : 0.0f;
       const float share = up / gate_sum32<LANES>(up);  // (of a single choice exactly 1, its gradient 0)
       const float mean = gate_sum32<LANES>(chosen ? g * share : 0.0f);
       // Past the last logit whose score is above 0 in 64 bits the weights are 0, and stay so.
       s = top <= kGateNoScore ? 0.0f : share;
       ds = g - mean;
     }
-    // (1 - s = z / (1 + z))
-    ds = chosen ? s * (l > 0.0f ? z * r : 1.0f - r) * ds : 0.0f;
+    ds = chosen ? s * z.rest * ds : 0.0f;
   } else if (p.renorm) {
     const bool nan = l != l;
     const float top = gate_value32(gate_max32<LANES>(nan ? 0u : gate_order32(l)));

@@ -113,3 +113,31 @@ def test_renormalised_softmax_far_below_the_largest():
         want = 2.0 * torch.softmax(L[:3, at].double(), 1)
         close(w[:3], want.to(DEV), 40 * U32 * want.to(DEV) + 1e-45, "weights")
         assert torch.isnan(w[3]).all()
+
+
+@pytest.mark.parametrize("base,spread", [(-40, 64), (-88, 15)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_weights_of_small_scores(dtype, base, spread):
+    """Scores among float32's subnormal numbers are weights as they are, and so are their gradients."""
+    need_gpu()
+    import dense_gemm_tile_amd as dgt
+    T, E, top = 64, 16, 3
+    L = (base - spread * torch.rand(T, E, generator=torch.Generator().manual_seed(2))).to(DEV, DT[dtype])
+    ids, w = gate(L, dtype, "sigmoid", None, 1, 1, 1, top, False, 1.0)
+    L64 = L.double()
+    want = torch.sigmoid(L64).gather(1, ids.long())
+    assert float(want.min()) > 0 and (base > -88 or float(want.min()) < 2.0 ** -130)
+    # An exponential of a number that is held, a sum and a division; among the subnormal numbers the exponential
+    # and the quotient are each off by a step of 2^-149 at most.
+    close(w, want, 12 * U32 * want + 2 * 2.0 ** -149, "sigmoid")
+    dw, dl = torch.full((T, top), 3.0, device=DEV), out(T, E, dtype="f32")
+    L32 = L.float()
+    dgt.gemm_gate_grad(T, E, top, "f32", L32, E, "sigmoid", False, 1.0, ids, dw, dl, E, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    want = torch.zeros_like(L64).scatter(1, ids.long(), 3 * want)
+    close(dl, want, 16 * U32 * want + 3 * 2 * 2.0 ** -149, "dL")
+    # Softmax scores beside a logit of 0, which the difference to it leaves exact here.
+    L[:, 0] = 0
+    ids, w = gate(L, dtype, "softmax", None, 1, 1, 1, top, False, 1.0)
+    want = torch.softmax(L.double(), 1).gather(1, ids.long())
+    close(w, want, (E / 16 + 24) * U32 * want + 2 * 2.0 ** -149, "softmax")
