@@ -1,9 +1,13 @@
 // What the kernels of the output layer's cross entropy share.
 #pragma once
 
+#include "layer.h"
 #include "layer_rows.h"
 
 namespace dgt {
+
+// exp(x): the hardware's, of an exponent rounded once (about |x| half steps of the result, and one step).
+__device__ __forceinline__ float loss_exp(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
 
 // One product of the loss on 256x256 tiles: logits of n vocabulary entries from v0 on (rows) for
 // T tokens (columns), and what becomes of them.

@@ -1,5 +1,5 @@
-// Cross entropy of an output layer: logits L = X W^T made in pieces of the vocabulary, and
-// never all of them held.
+// Cross entropy of an output layer: logits L = X W^T, of which pieces of the vocabulary are held
+// at a time.
 //
 //   lse = log sum exp L,  loss = lse - L[label]
 //   G = dloss (exp(L - lse) - [v = label]),  dX = G W,  dW = G^T X
@@ -22,10 +22,11 @@
 //
 // The logits come from layer_loss_pp256.hip, which turns them into parts or G in
 // registers. Fewer tokens, and operands not in whole 16-byte pieces, take a product of
-// gemm_linear in float32 and a kernel over its rows instead.
+// gemm_linear in float32 and a kernel over its rows instead. The workspace has room for those
+// float32 logits whatever a call takes, since its size is asked for before pitches and
+// addresses are known.
 #include "layer_loss.h"
 
-#include "layer.h"
 #include "layer_checks.h"
 
 namespace dgt {
@@ -67,7 +68,6 @@ struct LossGradArgs {
   unsigned grid_x;
 };
 
-__device__ __forceinline__ float loss_exp(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
 // Two partial (largest, sum) as one. A side without logits has (-inf, 0).
 __device__ __forceinline__ float2 loss_join(float2 a, float2 b) {
   const float m = __builtin_fmaxf(a.x, b.x), base = m == -__builtin_inff() ? 0.0f : m;

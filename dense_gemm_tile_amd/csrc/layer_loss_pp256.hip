@@ -11,7 +11,6 @@
 //
 // The exponentials take most of the epilogue: 128 a lane at 16 cycles a wave.
 #include "gemm_mfma_pingpong.h"
-#include "layer.h"
 #include "layer_loss.h"
 
 namespace dgt {
@@ -20,8 +19,6 @@ namespace {
 
 using C = PingPongCfgT<16>;
 using At = C::At;
-
-__device__ __forceinline__ float loss_exp(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
 
 // Of the four lanes that hold a column: lanes l, l ^ 16, l ^ 32, l ^ 48.
 template <class F>

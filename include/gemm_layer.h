@@ -321,7 +321,9 @@ GEMM_API int gemm_grouped_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dty
  * gemm_loss: cross entropy of an output layer, for T tokens and a vocabulary of
  * V: with the logits L = X @ W^T,
  *   lse[t] = log(sum over v of exp(L[t][v])),   loss[t] = lse[t] - L[t][labels[t]].
- * The logits are made in pieces and not kept.
+ * The logits are not kept. Calls of more than 64 tokens whose operands come in whole
+ * 16-byte pieces (addresses, pitches and H) sum them where they are made; others hold
+ * pieces of them in float32.
  *
  * X         T x H, W: V x H, of `dtype` (f16 or bf16). H == 0: all logits are 0.
  * labels    T int32. A token whose label is outside [0, V) has the loss 0.
@@ -329,7 +331,9 @@ GEMM_API int gemm_grouped_w4(int64_t G, int64_t M, int64_t N, int64_t K, int dty
  *           reads it).
  * V         >= 1.
  * workspace gemm_loss_workspace(T, V, H) bytes on the device, 16-byte aligned,
- *           used until the call's work has run.
+ *           used until the call's work has run. The size has room for the float32
+ *           pieces whatever the call needs: all T x V, or the more of 2^25 values and
+ *           4096 for each token.
  */
 GEMM_API int gemm_loss(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t ldx,
                   const void* W, int64_t ldw, const int32_t* labels, float* loss, float* lse,
@@ -343,16 +347,20 @@ GEMM_API int64_t gemm_loss_workspace(int64_t T, int64_t V, int64_t H);
  *   G[t][v] = dloss[t] * (exp(L[t][v] - lse[t]) - (v == labels[t]))
  * (0 for a token whose label is outside [0, V), whose dloss is not read),
  *   dX = G @ W,   dW = G^T @ X.
- * The logits are made again in pieces of the vocabulary, and G is rounded to
- * `dtype`, as the matrix cores read it, before its two products, relative to the
- * largest finite |dloss| of a token that counts: dloss may be of any size (in f16
- * a token whose |dloss| is below 2^-24 of that loses bits). dX in f16 wants a loss
+ * The logits are made again, in pieces of the vocabulary of 2^28 values where they
+ * are more, and G is rounded to `dtype`, as the matrix cores read it, before its two
+ * products, relative to the largest finite |dloss| of a token that counts: dloss may
+ * be of any size (in f16 a token whose |dloss| is below 2^-24 of that loses bits). Of
+ * a token whose |dloss| is not that one's, also the label's element is rounded, to
+ * half a step of dloss. dX in f16 wants a loss
  * scale all the same, as any gradient in f16.
  *
  * dX        T x H of `dtype`, or NULL when not wanted.
  * dW        V x H of dw_dtype (`dtype` or GEMM_DTYPE_F32), or NULL when not
  *           wanted. accumulate != 0 adds to what dW holds.
- * workspace gemm_loss_grad_workspace(T, V, H) bytes, as above.
+ * workspace gemm_loss_grad_workspace(T, V, H) bytes, as above; also for G in 16
+ *           bits (all of it, or the more of 2^28 values and 4096 for each token) and
+ *           float32 parts of dX.
  */
 GEMM_API int gemm_loss_grad(int64_t T, int64_t V, int64_t H, int dtype, const void* X, int64_t ldx,
                   const void* W, int64_t ldw, const int32_t* labels, const float* lse,
