@@ -254,6 +254,12 @@ __device__ __forceinline__ void gate_in_64_bits(const GateArgs& p, int64_t t, ui
   }
 }
 
+// The weight of a choice of score s among scores that sum to `total`: 0 without a choice, also
+// beside a NaN.
+__device__ __forceinline__ float gate_weight(const GateArgs& p, int id, double s, double total) {
+  return id < 0 || total == 0 ? 0.0f : (float)(s / total * (double)p.scale);
+}
+
 // A sigmoid score and one less it, each to a few half steps of itself, also among float32's
 // subnormal numbers.
 struct GateScore {
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(256) layer_gate_kernel(const GateArgs p) {
     const double total = p.renorm ? gate_wave_sum(exact) : 1.0;
     if (lane < p.top) {
       p.ids[(t0 + u) * p.top + lane] = found;
-      p.weights[(t0 + u) * p.top + lane] = total == 0 ? 0.0f : (float)(exact / total * (double)p.scale);
+      p.weights[(t0 + u) * p.top + lane] = gate_weight(p, found, exact, total);
     }
   }
 }
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(256) layer_gate_exact_kernel(const GateArgs p)
   const double total = p.renorm ? gate_wave_sum(weight) : 1.0;
   if (lane < p.top) {
     p.ids[t * p.top + lane] = id;
-    p.weights[t * p.top + lane] = total == 0 ? 0.0f : (float)(weight / total * (double)p.scale);
+    p.weights[t * p.top + lane] = gate_weight(p, id, weight, total);
   }
 }
 

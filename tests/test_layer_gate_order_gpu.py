@@ -1,4 +1,5 @@
-"""The gate without a bias: experts by their logits, whatever else a token holds."""
+"""The gate without a bias: experts by their logits, whatever else a token holds; choices that are dropped beside a
+NaN."""
 import math
 
 import pytest
@@ -96,3 +97,17 @@ def test_a_token_alone_and_beside_others():
             ids, _ = gate(torch.tensor([row], device=DEV), "f32", score, None, 1, 1, 1, 5, False, 1.0)
             ids = ids[0].tolist()
             assert ids.index(1) < ids.index(0), (score, change, ids)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_dropped_choices_beside_nan(score, renorm):
+    """A choice without an expert has the weight 0, whatever the others' weights are."""
+    need_gpu()
+    for E, groups in ((8, 1), (64, 8), (130, 65)):
+        L = torch.full((3, E), -math.inf)
+        L[:, 1], L[1:, 0] = math.nan, 2.0
+        ids, w = gate(L.to(DEV), "f32", score, None, groups, groups, 1, 4, renorm, 1.0)
+        assert ids.tolist() == [[1, -1, -1, -1], [0, 1, -1, -1], [0, 1, -1, -1]]
+        assert torch.isnan(w[0, 0]) and torch.isnan(w[1:, 1]).all()
+        assert (w[0, 1:] == 0).all() and (w[1:, 2:] == 0).all()
