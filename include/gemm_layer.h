@@ -197,6 +197,8 @@ GEMM_API int gemm_combine_grad(int64_t T, int64_t top, int64_t H, int dtype, con
  * gamma     N values of `dtype`, or NULL for ones. beta: the same, or NULL for
  *           zeros.
  * eps       finite and >= 0.
+ *           (Sums are float32: the differences to the mean count as far as their
+ *           squares are numbers of it, up to 1.8e19.)
  * mean,     M float32 values each, written when not NULL (kept for the backward
  * rstd      pass).
  */
